@@ -18,7 +18,9 @@ Layouts (C-contiguous device tensors, see include/qmv.h):
     x_scales float16 [...][K/32] for int8 activations
 bf16 activations with 2-bit or 3-bit weights (x_scales None) are quantized
 to int8 per 32 inside the kernel (QMV_A_BF16_Q8); MXFP4 weights take bf16
-activations or int8 activations with their scales (QMV_A_Q8B32).
+activations, int8 activations with their scales (QMV_A_Q8B32), or MXFP4
+activations (QMV_A_MXFP4: x uint8 [M][K/2] of e2m1 codes, x_scales uint8
+[M][K/32]), which qmx_quantize and qmx_rmsnorm write (qmx.py).
 """
 from __future__ import annotations
 
@@ -31,12 +33,14 @@ __all__ = ["qmv_dense", "qmv_gather_moe", "qmv_gather_moe_swiglu", "qmv_gather_m
            "qmv_gather_moe_combine_noalloc",
            "qmv_strerror",
            "qmv_probe_stream_read", "qmv_probe_clock", "lib", "LIB_PATH",
-           "W_MXFP4", "W_CB2", "W_CB3", "A_BF16", "A_Q8B32", "A_BF16_Q8", "QmvError"]
+           "W_MXFP4", "W_CB2", "W_CB3", "A_BF16", "A_Q8B32", "A_BF16_Q8", "A_MXFP4", "QmvError",
+           "qmx_rmsnorm", "qmx_router", "qmx_quantize", "qmx_dequantize", "qmx_strerror", "qmx_lib",
+           "QMX_LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqmv.so")
 
 W_MXFP4, W_CB2, W_CB3 = 0, 1, 2
-A_BF16, A_Q8B32, A_BF16_Q8 = 0, 1, 2
+A_BF16, A_Q8B32, A_BF16_Q8, A_MXFP4 = 0, 1, 2, 4
 _WFMT = {"mxfp4": W_MXFP4, "cb2": W_CB2, "cb3": W_CB3}
 _AFMT_OF = {W_MXFP4: A_BF16, W_CB2: A_Q8B32, W_CB3: A_Q8B32}
 STATUS = {0: "QMV_OK", 1: "QMV_EINVAL", 2: "QMV_EUNSUPPORTED", 3: "QMV_EHIP", 4: "QMV_ESCRATCH"}
@@ -121,10 +125,12 @@ _SCALE_DT = (torch.uint8, torch.float16)
 
 def _afmt(w, x):
     """Activation format from the weight format and x's dtype: MXFP4 takes
-    bf16 or int8 (+ scales); 2-/3-bit weights take int8 (+ scales) or bf16
-    (quantized in-kernel)."""
+    bf16, int8 (+ scales) or uint8 e2m1 codes (+ scales); 2-/3-bit weights
+    take int8 (+ scales) or bf16 (quantized in-kernel)."""
     is_bf16 = isinstance(x, torch.Tensor) and x.dtype == torch.bfloat16
     if w == W_MXFP4:
+        if isinstance(x, torch.Tensor) and x.dtype == torch.uint8:
+            return A_MXFP4, (torch.uint8,)
         return (A_BF16, (torch.bfloat16,)) if is_bf16 else (A_Q8B32, (torch.int8,))
     if is_bf16:
         return A_BF16_Q8, (torch.bfloat16,)
@@ -167,17 +173,32 @@ def _check_weights(w, codes, scales, lead, K, what=("w_codes", "w_scales")):
 
 def _check_x(x, x_scales, vectors, K, a):
     """x holds ``vectors`` activation vectors of K values, and x_scales (int8
-    activations) one fp16 scale per 32 of them."""
+    or MXFP4 activations) one fp16 or E8M0 scale per 32 of them."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
-    _need(x.dim() >= 1 and x.shape[-1] == K and x.numel() == vectors * K,
+    held = K // 2 if a == A_MXFP4 else K
+    _need(x.dim() >= 1 and x.shape[-1] == held and x.numel() == vectors * held,
           f"x has shape {tuple(x.shape)}, expected {vectors} vectors of K={K}")
+    if a == A_MXFP4:
+        _need(isinstance(x_scales, torch.Tensor), "MXFP4 activations need x_scales (uint8, one per 32)")
+        _need(x_scales.numel() == vectors * (K // 32),
+              f"x_scales has shape {tuple(x_scales.shape)}, expected {vectors} x {K // 32} E8M0 scales")
+        return
     if a == A_Q8B32:
         _need(isinstance(x_scales, torch.Tensor), "int8 activations need x_scales (float16, one per 32)")
         _need(x_scales.numel() == vectors * (K // 32),
               f"x_scales has shape {tuple(x_scales.shape)}, expected {vectors} x {K // 32} fp16 scales")
     else:
         _need(x_scales is None, "x_scales is only used with int8 activations")
+
+
+def _k_of(w, x):
+    """K from x's last dimension (two codes per byte for MXFP4 activations)."""
+    return x.shape[-1] * (2 if _afmt(w, x)[0] == A_MXFP4 else 1)
+
+
+def _xs_dtypes(a):
+    return (torch.uint8,) if a == A_MXFP4 else (torch.float16,)
 
 
 def _check_y(y, shape):
@@ -216,7 +237,7 @@ def qmv_dense(wfmt, w_codes, w_scales, x, x_scales=None, y=None, stream=None):
     ``x`` is [M][K]."""
     w = _wfmt(wfmt)
     _need(isinstance(x, torch.Tensor) and x.dim() == 2, "x must be a 2-D tensor [M][K]")
-    M, K = x.shape
+    M, K = x.shape[0], _k_of(w, x)
     N = w_codes.shape[0]
     a, xd = _afmt(w, x)
     _check_weights(w, w_codes, w_scales, (N,), K)
@@ -230,7 +251,7 @@ def qmv_dense(wfmt, w_codes, w_scales, x, x_scales=None, y=None, stream=None):
     s = lib().qmv_dense(w, _dev_ptr(w_codes, "w_codes", (torch.uint8,), dev),
                         _dev_ptr(w_scales, "w_scales", _SCALE_DT, dev), a,
                         _dev_ptr(x, "x", xd, dev),
-                        _dev_ptr(x_scales, "x_scales", (torch.float16,), dev),
+                        _dev_ptr(x_scales, "x_scales", _xs_dtypes(a), dev),
                         _dev_ptr(y, "y", (torch.float32,), dev), M, N, K, _stream(dev, stream))
     _check(s)
     return y
@@ -246,7 +267,7 @@ def qmv_gather_moe(wfmt, w_codes, w_scales, expert_ids, x, x_scales=None, x_per_
     w = _wfmt(wfmt)
     M, top_k = _check_ids(expert_ids)
     E, N = w_codes.shape[0], w_codes.shape[1]
-    K = x.shape[-1]
+    K = _k_of(w, x)
     per_slot = _per_slot(x, x_per_slot, M, top_k)
     a, xd = _afmt(w, x)
     _check_weights(w, w_codes, w_scales, (E, N), K)
@@ -261,7 +282,7 @@ def qmv_gather_moe(wfmt, w_codes, w_scales, expert_ids, x, x_scales=None, x_per_
                              _dev_ptr(w_scales, "w_scales", _SCALE_DT, dev), E,
                              _dev_ptr(expert_ids, "expert_ids", (torch.int32,), dev), M, top_k, a,
                              _dev_ptr(x, "x", xd, dev),
-                             _dev_ptr(x_scales, "x_scales", (torch.float16,), dev),
+                             _dev_ptr(x_scales, "x_scales", _xs_dtypes(a), dev),
                              int(per_slot),
                              _dev_ptr(y, "y", (torch.float32,), dev), N, K, _stream(dev, stream))
     _check(s)
@@ -275,7 +296,7 @@ def qmv_gather_moe_swiglu(wfmt, gate_codes, gate_scales, up_codes, up_scales, ex
     w = _wfmt(wfmt)
     M, top_k = _check_ids(expert_ids)
     E, N = gate_codes.shape[0], gate_codes.shape[1]
-    K = x.shape[-1]
+    K = _k_of(w, x)
     a, xd = _afmt(w, x)
     _check_weights(w, gate_codes, gate_scales, (E, N), K, ("gate_codes", "gate_scales"))
     _check_weights(w, up_codes, up_scales, (E, N), K, ("up_codes", "up_scales"))
@@ -292,7 +313,7 @@ def qmv_gather_moe_swiglu(wfmt, gate_codes, gate_scales, up_codes, up_scales, ex
         _dev_ptr(up_codes, "up_codes", (torch.uint8,), dev),
         _dev_ptr(up_scales, "up_scales", _SCALE_DT, dev), E,
         _dev_ptr(expert_ids, "expert_ids", (torch.int32,), dev), M, top_k, a,
-        _dev_ptr(x, "x", xd, dev), _dev_ptr(x_scales, "x_scales", (torch.float16,), dev),
+        _dev_ptr(x, "x", xd, dev), _dev_ptr(x_scales, "x_scales", _xs_dtypes(a), dev),
         _dev_ptr(y, "y", (torch.float32,), dev), N, K, _stream(dev, stream))
     _check(s)
     return y
@@ -331,7 +352,7 @@ def _combine(entry, wfmt, w_codes, w_scales, expert_ids, route_weights, x, x_sca
         raise TypeError("route_weights must be a torch.Tensor")
     _need(tuple(route_weights.shape) == (M, top_k),
           f"route_weights has shape {tuple(route_weights.shape)}, expected {(M, top_k)}")
-    K = x.shape[-1]
+    K = _k_of(w, x)
     per_slot = _per_slot(x, x_per_slot, M, top_k)
     a, xd = _afmt(w, x)
     _check_weights(w, w_codes, w_scales, (E, N), K)
@@ -347,7 +368,7 @@ def _combine(entry, wfmt, w_codes, w_scales, expert_ids, route_weights, x, x_sca
         _dev_ptr(w_scales, "w_scales", _SCALE_DT, dev), E,
         _dev_ptr(expert_ids, "expert_ids", (torch.int32,), dev),
         _dev_ptr(route_weights, "route_weights", (torch.float32,), dev), M, top_k, a,
-        _dev_ptr(x, "x", xd, dev), _dev_ptr(x_scales, "x_scales", (torch.float16,), dev),
+        _dev_ptr(x, "x", xd, dev), _dev_ptr(x_scales, "x_scales", _xs_dtypes(a), dev),
         int(per_slot), _dev_ptr(y, "y", (torch.float32,), dev), N, K,
         _stream(dev, stream))
     _check(s)
@@ -375,3 +396,7 @@ def qmv_probe_clock(out, stream=None):
     (include/qmv_probe.h)."""
     dev = out.device
     _check(lib().qmv_probe_clock(_dev_ptr(out, "out", (torch.int64,), dev), _stream(dev, stream)))
+
+
+from .qmx import (QMX_LIB_PATH, qmx_dequantize, qmx_lib, qmx_quantize, qmx_rmsnorm,  # noqa: E402
+                  qmx_router, qmx_strerror)

@@ -65,6 +65,12 @@ namespace qmv {
 extern const void *const kTableBatchedKS[3];
 }
 
+// MXFP4 x MXFP4 on the block-scaled matrix cores (qmv_k_mx4.hip): [plain,
+// gate/up, combine].
+namespace qmv {
+extern const void *const kTableMx4Few[3];
+}
+
 namespace qmv {
 constexpr int kBatchedMenu = 6;
 extern const int kBatchedShapes[kBatchedMenu][3];
@@ -574,6 +580,27 @@ qmv_status_t launch_dense4(const void *codes, const void *scales, const void *x,
     return QMV_OK;
 }
 
+// MXFP4 x MXFP4.  route_w non-null: the combine of up to 4 tokens.
+qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes2, const void *scales2, int E,
+                        const int32_t *ids, const float *route_w, int M, int top_k, const void *x,
+                        const void *xs, int x_per_slot, float *y, int N, int K, hipStream_t stream)
+{
+    const bool gather = ids != nullptr;
+    Args a = base_args(QMV_W_MXFP4, QMV_A_MXFP4, kMXFP4, codes, scales, gather ? E : 1, ids, M,
+                       gather ? top_k : 1, x, xs, gather ? x_per_slot : 0, y, N, K);
+    a.codes2 = (const uint8_t *)codes2;
+    a.scales2 = (const uint8_t *)scales2;
+    a.route_w = route_w;
+    a.x_vec_bytes = K / 2;
+    const int mode = route_w ? 2 : codes2 ? 1 : 0;
+    const int pairs = gather ? M * top_k : M;
+    const dim3 grid((unsigned)((N + 15) / 16), (unsigned)(route_w ? M : gather ? (pairs < E ? pairs : E) : (M + 15) / 16));
+    const size_t lds = 4 * (mode == 1 ? 2 : 1) * 1024 + kPairCountBytes + (((size_t)2 * pairs + 15) & ~(size_t)15);
+    void *kargs[] = {&a};
+    return hipLaunchKernel(kTableMx4Few[mode], grid, dim3(256), kargs, lds, stream) == hipSuccess ? QMV_OK
+                                                                                                  : QMV_EHIP;
+}
+
 // codes2/scales2 non-null selects the gate/up mode: codes/scales are the gate
 // projection, codes2/scales2 the up projection, y = swiglu(gate x, up x).
 qmv_status_t launch(int wfmt, int afmt, const void *codes, const void *scales, const void *codes2,
@@ -583,6 +610,9 @@ qmv_status_t launch(int wfmt, int afmt, const void *codes, const void *scales, c
 {
     const bool gather = ids != nullptr;
     const bool gate_up = codes2 != nullptr;
+    if (afmt == QMV_A_MXFP4)
+        return launch_mx4(codes, scales, codes2, scales2, E, ids, nullptr, M, top_k, x, xs, x_per_slot, y, N, K,
+                          stream);
     const int kind = kind_of(wfmt, afmt, K);
     // Dense MXFP4 x bf16 with 9 to 64 vectors: K-split tiles, one launch.
     // Measured on 7168 x 7168: 16 vectors 34.3 us as four 4-vector launches,
@@ -856,6 +886,9 @@ qmv_status_t launch_combine(int wfmt, int afmt, const void *codes, const void *s
             return st;
         return fe == hipSuccess ? QMV_OK : QMV_EHIP;
     }
+    if (afmt == QMV_A_MXFP4)
+        return launch_mx4(codes, scales, nullptr, nullptr, E, ids, route_w, M, top_k, x, xs, x_per_slot, y, N, K,
+                          stream);
     const int kind = kind_of(wfmt, afmt, K);
     Args a = base_args(wfmt, afmt, kind, codes, scales, E, ids, M, top_k, x, xs, x_per_slot, y, N, K);
     a.route_w = route_w;
@@ -901,7 +934,7 @@ QMV_API qmv_status_t qmv_dense(qmv_wfmt_t wfmt, const void *w_codes, const void 
     if (s != QMV_OK)
         return s;
     return launch(wfmt, afmt, w_codes, w_scales, nullptr, nullptr, 1, nullptr, M, 1, x,
-                  afmt == QMV_A_Q8B32 ? x_scales : nullptr, 0, y, N, K, stream);
+                  used_xs(afmt, x_scales), 0, y, N, K, stream);
 }
 
 QMV_API qmv_status_t qmv_gather_moe(qmv_wfmt_t wfmt, const void *w_codes, const void *w_scales, int E,
@@ -914,7 +947,7 @@ QMV_API qmv_status_t qmv_gather_moe(qmv_wfmt_t wfmt, const void *w_codes, const 
     if (s != QMV_OK)
         return s;
     return launch(wfmt, afmt, w_codes, w_scales, nullptr, nullptr, E, expert_ids, M, top_k, x,
-                  afmt == QMV_A_Q8B32 ? x_scales : nullptr, x_per_slot ? 1 : 0, y, N, K, stream);
+                  used_xs(afmt, x_scales), x_per_slot ? 1 : 0, y, N, K, stream);
 }
 
 QMV_API qmv_status_t qmv_gather_moe_swiglu(qmv_wfmt_t wfmt, const void *gate_codes, const void *gate_scales,

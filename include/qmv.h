@@ -66,9 +66,16 @@
  *                    and no page value pins it (parity unpinned against
  *                    the pages; the CPU oracle implements the same
  *                    reading).
- * Supported pairs: (MXFP4, BF16), (MXFP4, Q8B32), (CB2, Q8B32), (CB3, Q8B32),
- * (CB2, BF16_Q8), (CB3, BF16_Q8).  With (MXFP4, Q8B32) every 32-weight block
- * shares one E8M0 weight scale and one activation scale (both are per 32 of
+ *   QMV_A_MXFP4  x   uint8 [V][K/2] of e2m1 nibbles with x_scales uint8
+ *                    [V][K/32] (E8M0), the layout of MXFP4 weights (qmx.h has
+ *                    the quantizer and a norm that write it).  The products
+ *                    run on the block-scaled matrix cores, sums in fp32 (an
+ *                    output one of whose blocks sums to 2^128 or more need not
+ *                    be finite); a NaN scale (255) of either side makes the
+ *                    outputs of its row or vector NaN.
+ * Supported pairs: (MXFP4, BF16), (MXFP4, Q8B32), (MXFP4, MXFP4),
+ * (CB2, Q8B32), (CB3, Q8B32), (CB2, BF16_Q8), (CB3, BF16_Q8).  With
+ * (MXFP4, Q8B32) every 32-weight block shares one E8M0 weight scale and one activation scale (both are per 32 of
  * k), and the block's sum of e2m1 x int8 products is formed exactly (it is
  * the integer dot product of the 2*e2m1 values with q, times the weight
  * scale / 2) before the activation scale multiplies it.
@@ -85,7 +92,8 @@
  * host threads and streams.
  *
  * Alignment: codes 16 bytes (8 for CB2 when K % 64 != 0), x 16 bytes,
- * scales, x_scales, expert ids and y 4 bytes.
+ * scales, x_scales, expert ids and y 4 bytes; E8M0 scales (of weights or
+ * activations) may start at any byte.
  *
  * Limits: M >= 1, 1 <= top_k <= 16, K % 32 == 0, 32 <= K <= 16384, N >= 1,
  * E >= 1, M * top_k * N < 2^31.  With M > 4 (a prefill chunk or a wide
@@ -120,7 +128,7 @@ extern "C" {
 #endif
 
 typedef enum { QMV_W_MXFP4 = 0, QMV_W_CB2 = 1, QMV_W_CB3 = 2 } qmv_wfmt_t;
-typedef enum { QMV_A_BF16 = 0, QMV_A_Q8B32 = 1, QMV_A_BF16_Q8 = 2 } qmv_afmt_t;
+typedef enum { QMV_A_BF16 = 0, QMV_A_Q8B32 = 1, QMV_A_BF16_Q8 = 2, QMV_A_MXFP4 = 4 } qmv_afmt_t;
 
 typedef enum {
     QMV_OK = 0,
