@@ -69,7 +69,7 @@ extern const void *const kTableBatchedKS[3];
 // gate/up, combine].
 namespace qmv {
 extern const void *const kTableMx4Few[3];
-extern const void *const kTableMx4Tile[3];
+extern const void *const kTableMx4Tile[2];
 }
 
 namespace qmv {
@@ -581,8 +581,17 @@ qmv_status_t launch_dense4(const void *codes, const void *scales, const void *x,
     return QMV_OK;
 }
 
-std::once_flag g_mx4_once[3];
-hipError_t g_mx4_err[3];
+std::once_flag g_mx4_once[2];
+hipError_t g_mx4_err[2];
+
+// LDS of a tile workgroup: the chunk's list, two buffers of vector codes (64
+// vectors x 128 bytes) and of scale bytes (256 rows and 64 vectors x 16), the
+// waves' weight pieces (256 rows x 128 bytes).
+#ifndef XRF
+#define XRF 4
+#endif
+constexpr int kMx4RF = XRF;
+constexpr int kMx4TileLds = 128 + 2 * 64 * 128 + 2 * (64 * kMx4RF + 64) * 16 + 64 * kMx4RF * 128;
 
 // MXFP4 x MXFP4.  route_w non-null: the combine of up to 4 tokens.
 qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes2, const void *scales2, int E,
@@ -598,27 +607,22 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
     a.x_vec_bytes = K / 2;
     const int mode = route_w ? 2 : codes2 ? 1 : 0;
     const int pairs = gather ? M * top_k : M;
-    const size_t list = gather ? kPairCountBytes + (((size_t)2 * pairs + 15) & ~(size_t)15) : 0;
     if (mode != 2 && pairs >= (gather ? 2 * E : 17)) {
-        const bool wide = !gather && M > 64;
-        const int fn = wide ? 2 : mode;
-        const int nwr = wide ? 4 : 8, rf = wide ? 4 : 2, ct = wide ? 16 : 4;
-        const int rows = 16 * rf * nwr / (mode == 1 ? 2 : 1);
+        const int rows = (mode == 1 ? 32 : 64) * kMx4RF;
         a.bt_row_tiles = (N + rows - 1) / rows;
-        a.bt_vmax = 4;
-        a.bt_tiles = a.bt_row_tiles * (gather ? E : (M + 16 * ct - 1) / (16 * ct));
-        a.bt_per_xcd = (a.bt_tiles + 7) / 8;
-        a.lds_vec_bytes = 2 * (4 * ct * 1024 + 512 * 16);
-        const size_t lds = a.lds_vec_bytes + list;
+        // items at most: a chunk per 64 pairs and a rest per expert
+        const long long items = gather ? (pairs < E ? pairs : E) + pairs / 64 : (M + 63) / 64;
+        const long long tiles = items * a.bt_row_tiles;
+        const int fn = mode;
         std::call_once(g_mx4_once[fn], [&] {
             g_mx4_err[fn] = hipFuncSetAttribute(kTableMx4Tile[fn], hipFuncAttributeMaxDynamicSharedMemorySize,
-                                                160 * 1024);
+                                                kMx4TileLds);
         });
         if (g_mx4_err[fn] != hipSuccess)
             return QMV_EHIP;
         void *kargs[] = {&a};
-        return hipLaunchKernel(kTableMx4Tile[fn], dim3((unsigned)(8 * a.bt_per_xcd)), dim3(512), kargs, lds,
-                               stream) == hipSuccess ? QMV_OK : QMV_EHIP;
+        return hipLaunchKernel(kTableMx4Tile[fn], dim3((unsigned)(8 * ((tiles + 7) / 8))), dim3(256), kargs,
+                               kMx4TileLds, stream) == hipSuccess ? QMV_OK : QMV_EHIP;
     }
     const dim3 grid((unsigned)((N + 15) / 16), (unsigned)(route_w ? M : gather ? (pairs < E ? pairs : E) : (M + 15) / 16));
     const size_t lds = 4 * (mode == 1 ? 2 : 1) * 1024 + kPairCountBytes + (((size_t)2 * pairs + 15) & ~(size_t)15);

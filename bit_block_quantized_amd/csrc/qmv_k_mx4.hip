@@ -182,20 +182,28 @@ const void *const kTableMx4Few[3] = {
 };
 
 // ------------------------------------------------------------- many vectors
-// A tile is (expert, 16 RF NWR weight rows) against a chunk of its vectors,
-// NWR x NWC waves of RF x CF fragments each.  K goes in slabs of 512 weights
-// (4 MFMA steps):
-//   codes of the rows   straight from memory into the A operands, one slab
-//                       ahead (lane (c, q): row c's block q of a step -- 16
-//                       rows x 64 bytes a load, which streams within 3% of
-//                       contiguous reads on MI355X)
-//   codes of the vectors  staged in LDS in operand order (a fragment of a
-//                       step is 64 lanes x 16 bytes, read without bank
-//                       conflicts), double-buffered, loaded one slab ahead
-//   scale bytes         staged in LDS per slab as 16 bytes a row, transposed
-//                       so that lane (c, q) reads its four steps' bytes as one
-//                       dword, which the instruction indexes itself
-// One barrier per slab.
+// A tile is (expert, 16 RF NW weight rows) against a chunk of its vectors, NW
+// waves of RF x CF fragments each.  K goes in slabs of 512 weights (4 MFMA
+// steps) of two units (2 steps, 128 code bytes a row).
+//
+// The MFMA wants lane (c, q) = lane 16 q + c to hold 16 bytes of row c, but a
+// load whose neighbouring lanes lie in different rows costs the address unit
+// a cycle per lane (16 bytes per cycle and CU -- hardly more than the CU's
+// share of HBM).  So codes are loaded as they lie -- 8 lanes take a row's 128
+// bytes, 8 rows a load -- and turned into operand order by a pass through
+// LDS: chunk k (16 bytes) of row r stands at 128 r + 16 (k ^ (r/2 % 8)), so
+// that the 16 lanes of a write and of a read each touch 16 different bank
+// groups.
+//   codes of the rows   through a piece of LDS of the wave's own (LDS keeps a
+//                       wave's accesses in order: no barrier), two units ahead
+//                       in registers
+//   codes of the vectors  staged by all waves, double-buffered, one unit ahead
+//   scale bytes         staged per slab, one row's 16 bytes a thread,
+//                       transposed so that lane (c, q) reads its four steps'
+//                       bytes as one dword, which the instruction indexes
+// One barrier per unit; two workgroups of 4 waves share a CU.
+__device__ __forceinline__ int swz_chunk(int row, int chunk) { return row * 128 + 16 * (chunk ^ ((row >> 1) & 7)); }
+
 // A row's 16 scale bytes of a slab as loaded: five whole dwords around them.
 struct ScaleSeg {
     u32x4 d;
@@ -241,31 +249,121 @@ __device__ __forceinline__ u32x4 seg_order(const ScaleSeg &s, uint32_t o, int n)
                  perm(h23, h01, 0x07060302u)};
 }
 
-template <int MODE, bool DENSE, int RF, int CF, int NWR, int NWC, int AD>
+// The routed calls' work: an expert's pairs in chunks of at most kMx4Chunk.
+// Every workgroup counts the pairs per expert itself (LDS atomics on whole
+// numbers: the same counts everywhere), so the grid needs no device-wide
+// knowledge: item i is the i-th (expert, chunk) of the experts in order.
+constexpr int kMx4Chunk = 64;
+
+struct Mx4Item {
+    int e;               // expert
+    int nv;              // vectors of the chunk (0: no pair has an id in [0, E))
+    int items;           // items of the call
+};
+
+// cnt: 1024 + 8 words of LDS.  `pick` maps the number of items to this
+// workgroup's item (or -1); the chunk's pairs go to list.  ids: thread t
+// looks at ids t, t + 256, ...
+template <class Pick>
+__device__ __forceinline__ Mx4Item mx4_item(const int32_t *ids, int P, int E, int *cnt, uint16_t *list, Pick pick)
+{
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    int *const info = cnt + 1024;
+    int idv[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        if (j * 256 < P) idv[j] = ids[min(tid + j * 256, P - 1)];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) cnt[tid + 256 * i] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        if (j * 256 < P) {
+            if (tid + j * 256 < P && (unsigned)idv[j] < (unsigned)E) atomicAdd(&cnt[idv[j]], 1);
+        }
+    __syncthreads();
+    // thread t: experts 4 t .. 4 t + 3; items before them
+    int c[4], n = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        c[i] = 4 * tid + i < E ? cnt[4 * tid + i] : 0;
+        n += (c[i] + kMx4Chunk - 1) / kMx4Chunk;
+    }
+    int before = n;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int t = __shfl_up(before, d);
+        if (lane >= d) before += t;
+    }
+    if (lane == 63) info[w] = before;
+    __syncthreads();
+    int items = 0;
+    for (int i = 0; i < 4; ++i) {
+        if (i < w) before += info[i];
+        items += info[i];
+    }
+    before -= n;
+    const int item = pick(items);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int k = (c[i] + kMx4Chunk - 1) / kMx4Chunk;
+        if (item >= before && item < before + k) {
+            info[4] = 4 * tid + i;
+            info[5] = item - before;
+        }
+        before += k;
+    }
+    __syncthreads();
+    Mx4Item it = {0, 0, items};
+    if (item < 0 || item >= items) return it;
+    it.e = info[4];
+    const int chunk = info[5], total = cnt[it.e];
+    const int nch = (total + kMx4Chunk - 1) / kMx4Chunk;
+    const int cs = (total + nch - 1) / nch;           // equal chunks
+    it.nv = min(cs, total - chunk * cs);
+    // the pairs of e in (thread, round) order: this chunk's ranks
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        if (j * 256 < P) m |= (uint32_t)(idv[j] == it.e && tid + j * 256 < P) << j;
+    n = __popc(m);
+    int rank = n;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int t = __shfl_up(rank, d);
+        if (lane >= d) rank += t;
+    }
+    __syncthreads();                                  // (info is read above)
+    if (lane == 63) info[w] = rank;
+    __syncthreads();
+    for (int i = 0; i < 4; ++i)
+        if (i < w) rank += info[i];
+    rank -= n + chunk * cs;
+    for (; m; m &= m - 1, ++rank)
+        if (rank >= 0 && rank < it.nv) list[rank] = (uint16_t)(tid + 256 * (__ffs(m) - 1));
+    __syncthreads();
+    return it;
+}
+
+template <int MODE, int RF, int CF, int NW, int NA>
 __device__ __forceinline__ void mx4_tile_chunk(const Args &a, uint8_t *lds, int e, int row_base,
                                                const uint16_t *vecs, int vstart, int nv)
 {
-    constexpr int NW = NWR * NWC;
-    constexpr int CT = CF * NWC;                     // column fragments of the chunk
-    constexpr int BR = 16 * RF * NWR;                // weight rows of the tile (gate/up: of both)
+    constexpr int BR = 16 * RF * NW;                 // weight rows of the tile (gate/up: of both)
     constexpr int RH = MODE == 1 ? RF / 2 : RF;      // output row fragments per wave
-    constexpr int XU = (4 * CT + NW - 1) / NW;       // staged fragments per wave and slab
-    constexpr int NP = XU > 4 ? 4 : 1;               // staged in this many portions
-    constexpr int XP = XU / NP;
-    constexpr int XG = CT > NW ? CT / NW : 1;        // distinct column fragments a wave stages
-    constexpr int GB = CF > 4 ? 4 : CF;              // column fragments read from LDS at a time
-    constexpr int NS = 64 * NW;                      // staged scale segments (one per thread)
-    static_assert(BR + 16 * CT <= NS && (MODE == 1 ? BR / 2 : BR) % 64 == 0, "one thread per staged scale row");
-    static_assert(4 * CT % NW == 0 || 4 * CT < NW, "staging split");
-    uint8_t *const lx = lds;
-    uint8_t *const ls = lx + 2 * 4 * CT * 1024;
-    int tid = threadIdx.x;
-    asm volatile("" : "+v"(tid));                    // (keeps the offsets below inside the chunk loop)
+    constexpr int XU = (2 * CF + NW - 1) / NW;       // staged pieces (8 vectors x 128 bytes) per wave and unit
+    constexpr int NS = BR + 64;                      // staged scale rows
+    constexpr int XB = CF * 2048;                    // bytes of one vector buffer
+    static_assert(64 * NW % BR == 0 && NW == 4 && CF <= 4 && RF % 2 == 0, "one scale row a thread, 16 vectors a wave");
+    uint8_t *const lx = lds;                         // [2][CF][16 rows x 128 bytes]
+    uint8_t *const ls = lx + 2 * XB;                 // [2][NS] x 16 bytes
+    const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wr = NWC == 1 ? w : w / NWC, wc = NWC == 1 ? 0 : w % NWC;
+    uint8_t *const la = ls + 2 * NS * 16 + w * (RF * 2048);   // [RF][16 rows x 128 bytes], this wave's
     const int c = lane & 15, q = lane >> 4;
-    const bool gather = !DENSE && a.ids != nullptr;
+    const int lr = lane >> 3, lc = lane & 7;         // row and chunk of a load
+    const bool gather = vecs != nullptr;
     const int U = a.units;
     const int S = (U + 3) >> 2;                      // steps
     const int J = (S + 3) >> 2;                      // slabs
@@ -280,21 +378,32 @@ __device__ __forceinline__ void mx4_tile_chunk(const Args &a, uint8_t *lds, int 
     const long long eo = e;
     const __amdgpu_buffer_rsrc_t rc0 = buffer_rsrc(a.codes + eo * a.expert_cb, a.expert_cb);
     const __amdgpu_buffer_rsrc_t rc1 = buffer_rsrc((MODE == 1 ? a.codes2 : a.codes) + eo * a.expert_cb, a.expert_cb);
-    uint32_t oc[RF];
+    uint32_t oc[RF][2];
 #pragma unroll
-    for (int f = 0; f < RF; ++f) {
-        const int n = min(row_base + 16 * RH * wr + 16 * (MODE == 1 ? f % RH : f) + c, a.N - 1);
-        oc[f] = (uint32_t)n * (uint32_t)a.rcb + 16u * q;
-    }
-    auto load_a = [&](int s, u32x4 (&A)[RF]) {
-        const uint32_t so = s < S ? 64u * s : kXPast;           // (oc < 2^31: the sum does not wrap)
+    for (int f = 0; f < RF; ++f)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int n = min(row_base + 16 * RH * w + 16 * (MODE == 1 ? f % RH : f) + 8 * i + lr, a.N - 1);
+            oc[f][i] = (uint32_t)n * (uint32_t)a.rcb + 16u * lc;
+        }
+    auto load_a = [&](int u, u32x4 (&A)[RF][2]) {
+        const uint32_t so = 2 * u < S ? 128u * u : kXPast;      // (oc < 2^31: the sum does not wrap)
 #pragma unroll
         for (int f = 0; f < RF; ++f)
-            A[f] = __builtin_amdgcn_raw_buffer_load_b128(MODE == 1 && f >= RH ? rc1 : rc0, oc[f] + so, 0, 0);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                A[f][i] = __builtin_amdgcn_raw_buffer_load_b128(MODE == 1 && f >= RH ? rc1 : rc0, oc[f][i] + so, 0, 0);
+    };
+    const int wst = swz_chunk(lr, lc);               // rows 8 further: + 1024, ^ 64
+    auto store_a = [&](const u32x4 (&A)[RF][2]) {
+#pragma unroll
+        for (int f = 0; f < RF; ++f) {
+            *(u32x4 *)(la + f * 2048 + wst) = A[f][0];
+            *(u32x4 *)(la + f * 2048 + 1024 + (wst ^ 64)) = A[f][1];
+        }
     };
 
-    // staged vectors: fragment (step s, column fragment g) = unit s CT + g,
-    // wave w takes units w, w + NW, ...
+    // staged vectors: piece p = vectors 8 p .. 8 p + 7; wave w takes pieces w, w + NW, ...
     const int top_k = a.top_k;
     const bool by_token = gather && !a.x_per_slot;
     auto vec_row = [&](int v) -> uint32_t {
@@ -303,134 +412,126 @@ __device__ __forceinline__ void mx4_tile_chunk(const Args &a, uint8_t *lds, int 
     };
     const int x_rows = gather && a.x_per_slot ? a.M * a.top_k : a.M;
     const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(a.x, (long long)x_rows * a.x_vec_bytes);
-    uint32_t ox[XG];
+    uint32_t ox[XU];
 #pragma unroll
-    for (int k = 0; k < XG; ++k) {
-        const int v = 16 * ((w + NW * k) % CT) + c;
-        ox[k] = v < nv && w < 4 * CT ? vec_row(v) * (uint32_t)a.x_vec_bytes + 16u * q : kXPast;
+    for (int k = 0; k < XU; ++k) {
+        const int v = 8 * (w + NW * k) + lr;
+        ox[k] = v < nv ? vec_row(v) * (uint32_t)a.x_vec_bytes + 16u * lc : kXPast;
     }
-    auto load_x = [&](int j, int p, u32x4 (&X)[XP]) {
+    auto load_x = [&](int u, u32x4 (&X)[XU]) {
 #pragma unroll
-        for (int k = 0; k < XP; ++k) {
-            const int u = w + NW * (p * XP + k);
-            const int s = 4 * j + u / CT;
-            const uint32_t o = ox[XG == 1 ? 0 : (p * XP + k) % XG];
-            const bool ok = 4 * s + q < U && o != kXPast;
-            X[k] = __builtin_amdgcn_raw_buffer_load_b128(rx, ok ? o + 64u * s : kXPast, 0, 0);
+        for (int k = 0; k < XU; ++k) {
+            const bool ok = 8 * u + lc < U && ox[k] != kXPast;
+            X[k] = __builtin_amdgcn_raw_buffer_load_b128(rx, ok ? ox[k] + 128u * u : kXPast, 0, 0);
         }
     };
-    auto store_x = [&](int j, int p, const u32x4 (&X)[XP]) {
+    auto store_x = [&](int buf, const u32x4 (&X)[XU]) {
 #pragma unroll
-        for (int k = 0; k < XP; ++k) {
-            const int u = w + NW * (p * XP + k);
-            if (4 * CT >= NW || w < 4 * CT) *(u32x4 *)(lx + ((j & 1) * 4 * CT + u) * 1024 + 16 * lane) = X[k];
+        for (int k = 0; k < XU; ++k) {
+            const int p = w + NW * k;
+            if (2 * CF >= NW || w < 2 * CF)
+                *(u32x4 *)(lx + buf * XB + p * 1024 + (wst ^ ((p & 1) << 6))) = X[k];
         }
     };
 
-    // staged scales: one row's 16 bytes a thread -- first the tile's rows
-    // (gate/up: the gate's, then the up's), then the chunk's vectors.  Which
-    // of the three a wave reads is the same for all its lanes.
-    const int role = w < (MODE == 1 ? BR / 2 : BR) / 64 ? 0 : w < BR / 64 ? 1 : 2;
-    const uintptr_t ps = role == 2 ? (uintptr_t)a.xs
-                                   : (uintptr_t)((MODE == 1 && role == 1 ? a.scales2 : a.scales) + eo * a.expert_sb);
-    const long long zs = (long long)(ps & 3) + (role == 2 ? (long long)x_rows * a.rsb : a.expert_sb);
-    const __amdgpu_buffer_rsrc_t rs = buffer_rsrc((const void *)(ps & ~(uintptr_t)3), (zs + 3) & ~3ll);
-    uint32_t os;
-    {
-        const int t = MODE == 1 ? tid & (BR / 2 - 1) : tid;
-        const uint32_t row = role == 2 ? vec_row(tid - BR < nv ? tid - BR : 0)
-                                       : (uint32_t)min(row_base + t, a.N - 1);
-        os = (uint32_t)(ps & 3) + row * (uint32_t)a.rsb;
-    }
+    // staged scales: thread t takes row t % BR of the tile (gate/up: the gate's
+    // rows, then the up's -- the same tensor for all lanes of a wave), and
+    // wave w's lanes vectors 16 w .. 16 w + 15 of the chunk, four lanes each
+    // (what several lanes take they all write)
+    const int sr = tid & (BR - 1);
+    const bool up = MODE == 1 && (64 * w & (BR - 1)) >= BR / 2;
+    const uintptr_t pa = (uintptr_t)((up ? a.scales2 : a.scales) + eo * a.expert_sb), pb = (uintptr_t)a.xs;
+    const __amdgpu_buffer_rsrc_t rsa =
+        buffer_rsrc((const void *)(pa & ~(uintptr_t)3), ((long long)(pa & 3) + a.expert_sb + 3) & ~3ll);
+    const __amdgpu_buffer_rsrc_t rsb =
+        buffer_rsrc((const void *)(pb & ~(uintptr_t)3), ((long long)(pb & 3) + (long long)x_rows * a.rsb + 3) & ~3ll);
+    const int vs = 16 * w + c;
+    const uint32_t osa = (uint32_t)(pa & 3) +
+                         (uint32_t)min(row_base + (MODE == 1 ? tid & (BR / 2 - 1) : sr), a.N - 1) * (uint32_t)a.rsb;
+    const uint32_t osb = (uint32_t)(pb & 3) + vec_row(vs < nv ? vs : 0) * (uint32_t)a.rsb;
     // where the wave's fragments' scales stand
-    auto seg_of_row = [&](int f) { return MODE == 1 ? (f >= RH ? BR / 2 : 0) + 16 * (wr * RH + f % RH) : 16 * (wr * RF + f); };
+    auto seg_of_row = [&](int f) { return MODE == 1 ? (f >= RH ? BR / 2 : 0) + 16 * (w * RH + f % RH) : 16 * (w * RF + f); };
+    auto store_s = [&](int buf, const u32x4 &ra, const u32x4 &rb) {
+        *(u32x4 *)(ls + buf * (NS * 16) + sr * 16) = ra;
+        *(u32x4 *)(ls + buf * (NS * 16) + (BR + vs) * 16) = rb;
+    };
 
-    u32x4 A[AD][RF];
+    u32x4 A[NA][RF][2];
     {
-        const ScaleSeg sg = load_seg<true>(rs, os);
-#pragma unroll
-        for (int p = 0; p < NP; ++p) {
-            u32x4 X[XP];
-            load_x(0, p, X);
-            if (p == NP - 1) {
-#pragma unroll
-                for (int s = 0; s < AD; ++s) load_a(s, A[s]);
-            }
-            store_x(0, p, X);
-        }
-        *(u32x4 *)(ls + tid * 16) = seg_order<true>(sg, os, U);
+        u32x4 X[XU], A0[RF][2];
+        load_a(0, A0);
+        load_x(0, X);
+        const ScaleSeg sa = load_seg<true>(rsa, osa), sb = load_seg<true>(rsb, osb);
+        load_a(1, A[NA - 1]);
+        if constexpr (NA == 2) load_a(2, A[0]);
+        store_a(A0);
+        store_x(0, X);
+        store_s(0, seg_order<true>(sa, osa, U), seg_order<true>(sb, osb, U));
     }
     __syncthreads();
+    const int rd = c * 128 + 16 * (q ^ ((c >> 1) & 7));         // step 0's chunk of lane (c, q); step 1: ^ 64
     // LAST 0: slabs j and j + 1 are not the last; 1: slab j + 1 is; 2: slab j is
     auto slab = [&](int j, auto LAST) {
         constexpr int last = decltype(LAST)::value;
-        const uint8_t *const xb = lx + (j & 1) * (4 * CT * 1024) + 16 * lane;
         const uint8_t *const sc = ls + (j & 1) * (NS * 16) + c * 16 + 4 * q;
-        ScaleSeg sg;
-        u32x4 X[XP];
-        if constexpr (last < 2) {
-            sg = load_seg<last == 1>(rs, os + 16u * (j + 1));
-            load_x(j + 1, 0, X);
-        }
+        ScaleSeg sa, sb;
         uint32_t ta[RF], tb[CF];
+        auto unit = [&](auto HALF) {
+            constexpr int h = decltype(HALF)::value;            // the unit's vector buffer too
+            constexpr bool more = last < 2 || h == 0;           // another unit follows
+            const int u = 2 * j + h;
+            u32x4 F[2][RF], B[2][CF], X[XU];
+            auto read_b = [&](int s, u32x4 (&b)[CF]) {
 #pragma unroll
-        for (int f = 0; f < RF; ++f) ta[f] = *(const uint32_t *)(sc + seg_of_row(f) * 16);
+                for (int g = 0; g < CF; ++g) b[g] = *(const u32x4 *)(lx + h * XB + g * 2048 + (rd ^ (64 * s)));
+            };
+            if constexpr (h == 0) {
 #pragma unroll
-        for (int g = 0; g < CF; ++g) tb[g] = *(const uint32_t *)(sc + (BR + 16 * (wc * CF + g)) * 16);
-        // (step, GB column fragments) at a time; the next ones are read from
-        // LDS while these multiply
-        constexpr int H = CF / GB;
-        u32x4 B[2][GB];
-        auto read_b = [&](int i, u32x4 (&b)[GB]) {
+                for (int f = 0; f < RF; ++f) ta[f] = *(const uint32_t *)(sc + seg_of_row(f) * 16);
 #pragma unroll
-            for (int g = 0; g < GB; ++g)
-                b[g] = *(const u32x4 *)(xb + ((i / H) * CT + wc * CF + (i % H) * GB + g) * 1024);
-        };
-        read_b(0, B[0]);
-        auto part = [&](auto IDX) {
-            constexpr int i = decltype(IDX)::value;
-            constexpr int s = i / H, g0 = (i % H) * GB;
-            __builtin_amdgcn_sched_barrier(0);
-            if constexpr (i + 1 < 4 * H) read_b(i + 1, B[(i + 1) & 1]);
-#pragma unroll
-            for (int g = 0; g < GB; ++g)
-#pragma unroll
-                for (int f = 0; f < RF; ++f)
-                    acc[f][g0 + g] = mfma_mx4_op<s>(A[s % AD][f], B[i & 1][g], acc[f][g0 + g], ta[f], tb[g0 + g]);
-            // (the compiler would move the products past the barrier to their
-            // last use, with all their operands held until then)
-#pragma unroll
-            for (int g = 0; g < GB; ++g)
-#pragma unroll
-                for (int f = 0; f < RF; ++f) asm volatile("" : "+v"(acc[f][g0 + g]));
-            __builtin_amdgcn_sched_barrier(0);
-            if constexpr (i % H == H - 1 && last < 2) load_a(4 * j + s + AD, A[s % AD]);
-            if constexpr (i % H == H - 1 && last == 2 && s + AD < 4) load_a(4 * j + s + AD, A[s % AD]);
-        };
-        auto step = [&](auto SIDX) {
-            constexpr int s = decltype(SIDX)::value;
-            part(std::integral_constant<int, s * H>{});
-            if constexpr (H > 1) part(std::integral_constant<int, s * H + 1>{});
-        };
-        // with four portions each is loaded before a step and stored after it
-        auto next = [&](int p) {
-            if constexpr (NP == 4 && last < 2) {
-                store_x(j + 1, p - 1, X);
-                load_x(j + 1, p, X);
+                for (int g = 0; g < CF; ++g) tb[g] = *(const uint32_t *)(sc + (BR + 16 * g) * 16);
             }
+#pragma unroll
+            for (int f = 0; f < RF; ++f) F[0][f] = *(const u32x4 *)(la + f * 2048 + rd);
+            read_b(0, B[0]);
+#pragma unroll
+            for (int f = 0; f < RF; ++f) F[1][f] = *(const u32x4 *)(la + f * 2048 + (rd ^ 64));
+            if constexpr (more) load_x(u + 1, X);
+            if constexpr (h == 0 && last < 2) {
+                sa = load_seg<last == 1>(rsa, osa + 16u * (j + 1));
+                sb = load_seg<last == 1>(rsb, osb + 16u * (j + 1));
+            }
+            asm volatile("" ::: "memory");                      // (the next unit's codes go where these were)
+            if constexpr (more) {
+                store_a(A[(h ^ 1) % NA]);
+                if constexpr (last < 2 || NA == 1) load_a(u + 1 + NA, A[(h ^ 1) % NA]);
+            }
+            auto step = [&](auto SIDX) {
+                constexpr int s = decltype(SIDX)::value;
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (s == 0) read_b(1, B[1]);
+#pragma unroll
+                for (int g = 0; g < CF; ++g)
+#pragma unroll
+                    for (int f = 0; f < RF; ++f)
+                        acc[f][g] = mfma_mx4_op<2 * h + s>(F[s][f], B[s][g], acc[f][g], ta[f], tb[g]);
+                // (the compiler would move the products past the barrier to
+                // their last use, with all their operands held until then)
+#pragma unroll
+                for (int g = 0; g < CF; ++g)
+#pragma unroll
+                    for (int f = 0; f < RF; ++f) asm volatile("" : "+v"(acc[f][g]));
+            };
+            step(std::integral_constant<int, 0>{});
+            step(std::integral_constant<int, 1>{});
+            if constexpr (more) store_x(h ^ 1, X);
+            if constexpr (h == 1 && last < 2)
+                store_s((j + 1) & 1, seg_order<last == 1>(sa, osa, U - 16 * (j + 1)),
+                        seg_order<last == 1>(sb, osb, U - 16 * (j + 1)));
+            __syncthreads();
         };
-        step(std::integral_constant<int, 0>{});
-        next(1);
-        step(std::integral_constant<int, 1>{});
-        next(2);
-        step(std::integral_constant<int, 2>{});
-        next(3);
-        step(std::integral_constant<int, 3>{});
-        if constexpr (last < 2) {
-            store_x(j + 1, NP - 1, X);
-            *(u32x4 *)(ls + ((j + 1) & 1) * (NS * 16) + tid * 16) = seg_order<last == 1>(sg, os, U - 16 * (j + 1));
-        }
-        __syncthreads();
+        unit(std::integral_constant<int, 0>{});
+        unit(std::integral_constant<int, 1>{});
     };
     int j = 0;
     for (; j + 2 < J; ++j) slab(j, std::integral_constant<int, 0>{});
@@ -441,12 +542,12 @@ __device__ __forceinline__ void mx4_tile_chunk(const Args &a, uint8_t *lds, int 
     const bool vec4 = (a.N & 3) == 0 && ((uintptr_t)a.y & 15) == 0;
 #pragma unroll
     for (int g = 0; g < CF; ++g) {
-        const int v = 16 * (wc * CF + g) + c;
+        const int v = 16 * g + c;
         if (v < nv) {
             float *const yr = a.y + (size_t)(gather ? (int)vecs[v] : vstart + v) * a.N;
 #pragma unroll
             for (int f = 0; f < RH; ++f) {
-                const int n0 = row_base + 16 * RH * wr + 16 * f + 4 * q;
+                const int n0 = row_base + 16 * RH * w + 16 * f + 4 * q;
                 float r[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
@@ -465,79 +566,74 @@ __device__ __forceinline__ void mx4_tile_chunk(const Args &a, uint8_t *lds, int 
     }
 }
 
-// The tile's expert and vectors, then its chunks.  CMAX: column fragments per
-// wave of the largest chunk.
-// DENSE: no routed calls.
-template <int MODE, bool DENSE, int RF, int NWR, int NWC, int AD, int CMIN, int CMAX, int WPE>
-__global__ __launch_bounds__(64 * NWR * NWC, WPE) void qmv_mx4_tile_kernel(const Args a)
+// Workgroup b runs on XCD b % 8; the call's tiles (item-major) are dealt to
+// the XCDs in contiguous runs, so that an XCD's L2 holds the vectors of a few
+// experts, and an expert's second chunk finds its weights there.
+#ifndef XRF
+#define XRF 4
+#define XNA 2
+#define XWPE 2
+#endif
+template <int MODE>
+__global__ __launch_bounds__(256, XWPE) void qmv_mx4_tile_kernel(const Args a)
 {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    constexpr int THREADS = 64 * NWR * NWC;
-    constexpr int TR = 16 * RF * NWR / (MODE == 1 ? 2 : 1);
-    constexpr int VCAP = 16 * CMAX * NWC;
+    constexpr int RF = XRF, NW = 4, NA = XNA;
+    constexpr int TR = 16 * RF * NW / (MODE == 1 ? 2 : 1);
+    uint16_t *const list = (uint16_t *)lds;           // [kMx4Chunk]
+    uint8_t *const buf = lds + 2 * kMx4Chunk;
     const int b = blockIdx.x;
-    const int t = (b & 7) * a.bt_per_xcd + (b >> 3);
-    if (t >= a.bt_tiles) return;
-    const bool gather = !DENSE && a.ids != nullptr;
-    int e = 0, cnt = 0, vstart = 0, rt;
-    const uint16_t *vecs = nullptr;
+    int tile = -1;
+    auto pick = [&](int items) {
+        const int tiles = items * a.bt_row_tiles, per_xcd = (tiles + 7) / 8;
+        const int i = b >> 3;
+        if (i < per_xcd) tile = (b & 7) * per_xcd + i;
+        if (tile >= tiles) tile = -1;
+        return tile < 0 ? -1 : tile / a.bt_row_tiles;
+    };
+    int e = 0, nv, vstart = 0, item;
+    const bool gather = a.ids != nullptr;
     if (gather) {
-        const int bucket = t / a.bt_row_tiles;
-        rt = t - bucket * a.bt_row_tiles;
-        const int row_base = rt * TR;
-        PairList L;
-        L.cnt = (int *)(lds + a.lds_vec_bytes);       // behind the staging buffers
-        L.perm = (uint16_t *)(L.cnt + kMaxCounts + 4);
-        const Ids8 id0 = load_ids8<THREADS>(a.ids, a.M * a.top_k, a.E, 0);
-        if (bucket == 0) {
-            // the tiles of expert 0 also write the zero rows of ids outside [0, E)
-            const int ci = list_pairs<THREADS>(a.ids, a.M * a.top_k, a.E, -1, L, id0);
-            const int rows = min(TR, a.N - row_base);
-            for (int o = threadIdx.x; o < ci * rows; o += THREADS)
-                a.y[(size_t)L.perm[o / rows] * a.N + row_base + o % rows] = 0.0f;
-            __syncthreads();
+        // (a call without any id in [0, E) still has its zero rows: one item)
+        const int P = a.M * a.top_k;
+        const Mx4Item it = mx4_item(a.ids, P, a.E, (int *)buf, list, [&](int items) { return pick(max(items, 1)); });
+        if (tile < 0) return;
+        item = tile / a.bt_row_tiles;
+        e = it.e;
+        nv = it.nv;
+        // the rows of ids outside [0, E) are zeros: item i takes the pairs
+        // i, i + items, ... for its rows
+        const int items = max(it.items, 1), row_base = (tile - item * a.bt_row_tiles) * TR;
+        const int rows = min(TR, a.N - row_base), lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+        for (int p0 = item + items * 16 * w; p0 < P; p0 += items * 16 * NW) {
+            const int p = p0 + items * (lane & 15);
+            const bool bad = lane < 16 && p < P && (unsigned)a.ids[min(p, P - 1)] >= (unsigned)a.E;
+            for (unsigned long long m = __ballot(bad); m; m &= m - 1) {
+                float *const yr = a.y + (size_t)(p0 + items * (__ffsll((long long)m) - 1)) * a.N + row_base;
+                for (int o = lane; o < rows; o += 64) yr[o] = 0.0f;
+            }
         }
-        e = bucket;
-        cnt = list_pairs<THREADS>(a.ids, a.M * a.top_k, a.E, bucket, L, id0);
-        if (cnt == 0) return;
-        vecs = L.perm;
+        if (nv == 0) return;
     } else {
-        // dense: groups of bt_vmax vector chunks, chunk-fastest inside, so that
-        // the tiles an XCD runs at a time share both operands
-        const int chunks = (a.M + VCAP - 1) / VCAP;
-        const int per = a.bt_vmax * a.bt_row_tiles;
-        const int grp = t / per;
-        const int in = t - grp * per;
-        const int gw = min(a.bt_vmax, chunks - grp * a.bt_vmax);
-        rt = in / gw;
-        vstart = (grp * a.bt_vmax + in - rt * gw) * VCAP;
-        cnt = min(VCAP, a.M - vstart);
+        item = pick((a.M + kMx4Chunk - 1) / kMx4Chunk);
+        if (item < 0) return;
+        vstart = item * kMx4Chunk;
+        nv = min(kMx4Chunk, a.M - vstart);
     }
-    const int row_base = rt * TR;
-    const int nch = (cnt + VCAP - 1) / VCAP;
-    const int cs = (cnt + nch - 1) / nch;             // equal chunks
-    for (int ch = 0; ch < nch; ++ch) {
-        const int nv = min(cs, cnt - ch * cs);
-        const uint16_t *const cv = vecs ? vecs + ch * cs : nullptr;
-        const int vs = vstart + ch * cs;
-        if (CMIN <= 1 && nv <= 16 * NWC)
-            mx4_tile_chunk<MODE, DENSE, RF, CMIN <= 1 ? 1 : CMAX, NWR, NWC, AD>(a, lds, e, row_base, cv, vs, nv);
-        else if (CMIN <= 2 && CMAX >= 2 && nv <= 32 * NWC)
-            mx4_tile_chunk<MODE, DENSE, RF, CMIN <= 2 && CMAX >= 2 ? 2 : CMAX, NWR, NWC, AD>(a, lds, e, row_base, cv, vs, nv);
-        else if (CMIN <= 4 && CMAX >= 4 && nv <= 64 * NWC)
-            mx4_tile_chunk<MODE, DENSE, RF, CMIN <= 4 && CMAX >= 4 ? 4 : CMAX, NWR, NWC, AD>(a, lds, e, row_base, cv, vs, nv);
-        else
-            mx4_tile_chunk<MODE, DENSE, RF, CMAX, NWR, NWC, AD>(a, lds, e, row_base, cv, vs, nv);
-        __syncthreads();                              // (the next chunk stages over this one's buffers)
-    }
+    const int row_base = (tile - item * a.bt_row_tiles) * TR;
+    const uint16_t *const vecs = gather ? list : nullptr;
+    if (nv <= 16)
+        mx4_tile_chunk<MODE, RF, 1, NW, NA>(a, buf, e, row_base, vecs, vstart, nv);
+    else if (nv <= 32)
+        mx4_tile_chunk<MODE, RF, 2, NW, NA>(a, buf, e, row_base, vecs, vstart, nv);
+    else
+        mx4_tile_chunk<MODE, RF, 4, NW, NA>(a, buf, e, row_base, vecs, vstart, nv);
 }
 
-// [plain, gate/up], then [plain] for wide dense calls
-extern const void *const kTableMx4Tile[3];
-const void *const kTableMx4Tile[3] = {
-    (const void *)&qmv_mx4_tile_kernel<0, false, 2, 8, 1, 2, 1, 4, 4>,
-    (const void *)&qmv_mx4_tile_kernel<1, false, 2, 8, 1, 2, 1, 4, 4>,
-    (const void *)&qmv_mx4_tile_kernel<0, true, 4, 4, 2, 2, 8, 8, 2>,
+extern const void *const kTableMx4Tile[2];
+const void *const kTableMx4Tile[2] = {
+    (const void *)&qmv_mx4_tile_kernel<0>,
+    (const void *)&qmv_mx4_tile_kernel<1>,
 };
 
 }  // namespace qmv
