@@ -585,13 +585,14 @@ std::once_flag g_mx4_once[2];
 hipError_t g_mx4_err[2];
 
 // LDS of a tile workgroup: the chunk's list, two buffers of vector codes (64
-// vectors x 128 bytes) and of scale bytes (256 rows and 64 vectors x 16), the
-// waves' weight pieces (256 rows x 128 bytes).
-#ifndef XRF
-#define XRF 4
-#endif
-constexpr int kMx4RF = XRF;
-constexpr int kMx4TileLds = 128 + 2 * 64 * 128 + 2 * (64 * kMx4RF + 64) * 16 + 64 * kMx4RF * 128;
+// vectors x 128 bytes), the waves' weight pieces (rows x 128 bytes), and the
+// scale bytes of the rows and the vectors (an odd number of 16-byte slabs
+// from row to row); with room for the counts per expert.
+int mx4_tile_lds(int K)
+{
+    const int J = (K + 511) / 512;
+    return 128 + 2 * 64 * 128 + 128 * 128 + (128 + 64) * 16 * (J | 1);
+}
 
 // MXFP4 x MXFP4.  route_w non-null: the combine of up to 4 tokens.
 qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes2, const void *scales2, int E,
@@ -608,21 +609,29 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
     const int mode = route_w ? 2 : codes2 ? 1 : 0;
     const int pairs = gather ? M * top_k : M;
     if (mode != 2 && pairs >= (gather ? 2 * E : 17)) {
-        const int rows = (mode == 1 ? 32 : 64) * kMx4RF;
+        const int rows = mode == 1 ? 64 : 128;
         a.bt_row_tiles = (N + rows - 1) / rows;
         // items at most: a chunk per 64 pairs and a rest per expert
         const long long items = gather ? (pairs < E ? pairs : E) + pairs / 64 : (M + 63) / 64;
-        const long long tiles = items * a.bt_row_tiles;
+        // runs of row tiles: about 8 workgroups for each that the chip holds at
+        // a time (fewer, longer runs scan the ids less often but end unevenly:
+        // 1024 tokens x top-8 of 256, 7168 -> 2048: 570 us at 1, 417 at 4, 376
+        // at 8; 512 x top-4 of 32, gate/up 2880 -> 2880: 110, 112, 112 us)
+        const int lds = mx4_tile_lds(K);
+        const long long slots = (long long)cu_count() * (lds * 2 <= kLdsPerCU ? 2 : 1);
+        const long long run = items * a.bt_row_tiles / (8 * slots);
+        a.bt_chunk = run < 1 ? 1 : run > a.bt_row_tiles ? a.bt_row_tiles : (int)run;
+        const long long groups = items * ((a.bt_row_tiles + a.bt_chunk - 1) / a.bt_chunk);
         const int fn = mode;
         std::call_once(g_mx4_once[fn], [&] {
             g_mx4_err[fn] = hipFuncSetAttribute(kTableMx4Tile[fn], hipFuncAttributeMaxDynamicSharedMemorySize,
-                                                kMx4TileLds);
+                                                mx4_tile_lds(kMaxK));
         });
         if (g_mx4_err[fn] != hipSuccess)
             return QMV_EHIP;
         void *kargs[] = {&a};
-        return hipLaunchKernel(kTableMx4Tile[fn], dim3((unsigned)(8 * ((tiles + 7) / 8))), dim3(256), kargs,
-                               kMx4TileLds, stream) == hipSuccess ? QMV_OK : QMV_EHIP;
+        return hipLaunchKernel(kTableMx4Tile[fn], dim3((unsigned)(8 * ((groups + 7) / 8))), dim3(256), kargs,
+                               lds, stream) == hipSuccess ? QMV_OK : QMV_EHIP;
     }
     const dim3 grid((unsigned)((N + 15) / 16), (unsigned)(route_w ? M : gather ? (pairs < E ? pairs : E) : (M + 15) / 16));
     const size_t lds = 4 * (mode == 1 ? 2 : 1) * 1024 + kPairCountBytes + (((size_t)2 * pairs + 15) & ~(size_t)15);

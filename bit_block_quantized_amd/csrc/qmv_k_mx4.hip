@@ -182,8 +182,8 @@ const void *const kTableMx4Few[3] = {
 };
 
 // ------------------------------------------------------------- many vectors
-// A tile is (expert, 16 RF NW weight rows) against a chunk of its vectors, NW
-// waves of RF x CF fragments each.  K goes in slabs of 512 weights (4 MFMA
+// A tile is (expert, 128 weight rows) against a chunk of its vectors, 4 waves
+// of 2 x CF fragments each (RF = 2).  K goes in slabs of 512 weights (4 MFMA
 // steps) of two units (2 steps, 128 code bytes a row).
 //
 // The MFMA wants lane (c, q) = lane 16 q + c to hold 16 bytes of row c, but a
@@ -198,7 +198,7 @@ const void *const kTableMx4Few[3] = {
 //                       wave's accesses in order: no barrier), two units ahead
 //                       in registers
 //   codes of the vectors  staged by all waves, double-buffered, one unit ahead
-//   scale bytes         staged per slab, one row's 16 bytes a thread,
+//   scale bytes         staged for the whole tile, 16 bytes (a slab) at a time
 //                       transposed so that lane (c, q) reads its four steps'
 //                       bytes as one dword, which the instruction indexes
 // One barrier per unit; two workgroups of 4 waves share a CU.
@@ -254,6 +254,8 @@ __device__ __forceinline__ u32x4 seg_order(const ScaleSeg &s, uint32_t o, int n)
 // numbers: the same counts everywhere), so the grid needs no device-wide
 // knowledge: item i is the i-th (expert, chunk) of the experts in order.
 constexpr int kMx4Chunk = 64;
+constexpr int kMx4Waves = 4;
+constexpr int kMx4RF = 2;            // 16-row fragments per wave of a tile
 
 struct Mx4Item {
     int e;               // expert
@@ -261,20 +263,34 @@ struct Mx4Item {
     int items;           // items of the call
 };
 
+// Inclusive sum over the lanes of a wave.
+__device__ __forceinline__ int wave_scan(int v)
+{
+    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr 1, 2, 4, 8: within 16 lanes
+    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // lane 15 of rows 0, 2 to rows 1, 3
+    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // lane 31 to rows 2, 3
+    return v;
+}
+
 // cnt: 1024 + 8 words of LDS.  `pick` maps the number of items to this
 // workgroup's item (or -1); the chunk's pairs go to list.  ids: thread t
-// looks at ids t, t + 256, ...
+// looks at ids t, t + 256, ...  Every wave finds the item by itself.
 template <class Pick>
 __device__ __forceinline__ Mx4Item mx4_item(const int32_t *ids, int P, int E, int *cnt, uint16_t *list, Pick pick)
 {
-    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    const int lane = tid & 63, w = tid >> 6;
     int *const info = cnt + 1024;
     int idv[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j)
         if (j * 256 < P) idv[j] = ids[min(tid + j * 256, P - 1)];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) cnt[tid + 256 * i] = 0;
+    *(int4 *)(cnt + 4 * tid) = make_int4(0, 0, 0, 0);
+    if (tid == 0) info[4] = 0;
     __syncthreads();
 #pragma unroll
     for (int j = 0; j < 32; ++j)
@@ -282,110 +298,105 @@ __device__ __forceinline__ Mx4Item mx4_item(const int32_t *ids, int P, int E, in
             if (tid + j * 256 < P && (unsigned)idv[j] < (unsigned)E) atomicAdd(&cnt[idv[j]], 1);
         }
     __syncthreads();
-    // thread t: experts 4 t .. 4 t + 3; items before them
-    int c[4], n = 0;
+    // lane l: experts 16 l .. 16 l + 15 (those past E have no pairs)
+    int c[16], n = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        c[i] = 4 * tid + i < E ? cnt[4 * tid + i] : 0;
-        n += (c[i] + kMx4Chunk - 1) / kMx4Chunk;
+        const int4 v = *(const int4 *)(cnt + 16 * lane + 4 * i);
+        c[4 * i] = v.x, c[4 * i + 1] = v.y, c[4 * i + 2] = v.z, c[4 * i + 3] = v.w;
     }
-    int before = n;
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int t = __shfl_up(before, d);
-        if (lane >= d) before += t;
-    }
-    if (lane == 63) info[w] = before;
-    __syncthreads();
-    int items = 0;
-    for (int i = 0; i < 4; ++i) {
-        if (i < w) before += info[i];
-        items += info[i];
-    }
+    for (int i = 0; i < 16; ++i) n += (c[i] + kMx4Chunk - 1) / kMx4Chunk;
+    int before = wave_scan(n);
+    const int items = __builtin_amdgcn_readlane(before, 63);
     before -= n;
     const int item = pick(items);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int k = (c[i] + kMx4Chunk - 1) / kMx4Chunk;
-        if (item >= before && item < before + k) {
-            info[4] = 4 * tid + i;
-            info[5] = item - before;
-        }
-        before += k;
-    }
-    __syncthreads();
     Mx4Item it = {0, 0, items};
     if (item < 0 || item >= items) return it;
-    it.e = info[4];
-    const int chunk = info[5], total = cnt[it.e];
+    const unsigned long long owner = __ballot(item >= before && item < before + n);
+    int e = 0, chunk = 0, total = 0;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int k = (c[i] + kMx4Chunk - 1) / kMx4Chunk;
+        if (item >= before && item < before + k) e = 16 * lane + i, chunk = item - before, total = c[i];
+        before += k;
+    }
+    const int o = __ffsll((long long)owner) - 1;
+    it.e = __builtin_amdgcn_readlane(e, o);
+    chunk = __builtin_amdgcn_readlane(chunk, o);
+    total = __builtin_amdgcn_readlane(total, o);
     const int nch = (total + kMx4Chunk - 1) / kMx4Chunk;
     const int cs = (total + nch - 1) / nch;           // equal chunks
     it.nv = min(cs, total - chunk * cs);
-    // the pairs of e in (thread, round) order: this chunk's ranks
     uint32_t m = 0;
 #pragma unroll
     for (int j = 0; j < 32; ++j)
         if (j * 256 < P) m |= (uint32_t)(idv[j] == it.e && tid + j * 256 < P) << j;
-    n = __popc(m);
-    int rank = n;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int t = __shfl_up(rank, d);
-        if (lane >= d) rank += t;
+    if (nch == 1) {
+        // one chunk: the order of its pairs changes no result
+        for (; m; m &= m - 1) list[atomicAdd(&info[4], 1)] = (uint16_t)(tid + 256 * (__ffs(m) - 1));
+    } else {
+        // the pairs of e in (thread, round) order, the same in every
+        // workgroup: this chunk's ranks
+        n = __popc(m);
+        int rank = wave_scan(n);
+        if (lane == 63) info[w] = rank;
+        __syncthreads();
+        for (int i = 0; i < 4; ++i)
+            if (i < w) rank += info[i];
+        rank -= n + chunk * cs;
+        for (; m; m &= m - 1, ++rank)
+            if (rank >= 0 && rank < it.nv) list[rank] = (uint16_t)(tid + 256 * (__ffs(m) - 1));
     }
-    __syncthreads();                                  // (info is read above)
-    if (lane == 63) info[w] = rank;
-    __syncthreads();
-    for (int i = 0; i < 4; ++i)
-        if (i < w) rank += info[i];
-    rank -= n + chunk * cs;
-    for (; m; m &= m - 1, ++rank)
-        if (rank >= 0 && rank < it.nv) list[rank] = (uint16_t)(tid + 256 * (__ffs(m) - 1));
     __syncthreads();
     return it;
 }
 
-template <int MODE, int RF, int CF, int NW, int NA>
-__device__ __forceinline__ void mx4_tile_chunk(const Args &a, uint8_t *lds, int e, int row_base,
-                                               const uint16_t *vecs, int vstart, int nv)
+// Bytes from row to row of the staged scales of J slabs.
+__host__ __device__ constexpr int mx4_scale_pitch(int J) { return 16 * (J | 1); }
+
+// Row tiles rt0 .. rt1 - 1 of expert e against nv vectors: pairs vecs[0..nv)
+// of a routed call, vectors vstart .. of a dense one (vecs null).
+template <int MODE, int CF>
+__device__ __forceinline__ void mx4_tile_run(const Args &a, uint8_t *lds, int e, int rt0, int rt1,
+                                             const uint16_t *vecs, int vstart, int nv)
 {
-    constexpr int BR = 16 * RF * NW;                 // weight rows of the tile (gate/up: of both)
+    constexpr int NW = kMx4Waves, RF = kMx4RF;
+    constexpr int BR = 16 * RF * NW;                 // weight rows of a tile (gate/up: of both)
     constexpr int RH = MODE == 1 ? RF / 2 : RF;      // output row fragments per wave
+    constexpr int TR = 16 * RH * NW;                 // output rows of a tile
     constexpr int XU = (2 * CF + NW - 1) / NW;       // staged pieces (8 vectors x 128 bytes) per wave and unit
-    constexpr int NS = BR + 64;                      // staged scale rows
     constexpr int XB = CF * 2048;                    // bytes of one vector buffer
-    static_assert(64 * NW % BR == 0 && NW == 4 && CF <= 4 && RF % 2 == 0, "one scale row a thread, 16 vectors a wave");
-    uint8_t *const lx = lds;                         // [2][CF][16 rows x 128 bytes]
-    uint8_t *const ls = lx + 2 * XB;                 // [2][NS] x 16 bytes
-    const int tid = threadIdx.x;
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));                    // (keeps the offsets below out of the caller's loop head)
     const int lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    uint8_t *const la = ls + 2 * NS * 16 + w * (RF * 2048);   // [RF][16 rows x 128 bytes], this wave's
+    uint8_t *const lx = lds;                                      // [2][CF][16 vectors x 128 bytes]
+    uint8_t *const la = lds + 4 * 4096 + w * (RF * 2048);         // [RF][16 rows x 128 bytes], this wave's
+    uint8_t *const ls = lds + 4 * 4096 + NW * RF * 2048;          // [BR + 16 CF] rows of SP bytes
     const int c = lane & 15, q = lane >> 4;
     const int lr = lane >> 3, lc = lane & 7;         // row and chunk of a load
     const bool gather = vecs != nullptr;
+    const int N = a.N;
     const int U = a.units;
     const int S = (U + 3) >> 2;                      // steps
     const int J = (S + 3) >> 2;                      // slabs
+    const int SP = mx4_scale_pitch(J);
+    const uint32_t rsb = (uint32_t)a.rsb;
 
-    f32x4 acc[RF][CF];
-#pragma unroll
-    for (int f = 0; f < RF; ++f)
-#pragma unroll
-        for (int g = 0; g < CF; ++g) acc[f][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
+    const __amdgpu_buffer_rsrc_t rc0 = buffer_rsrc(a.codes + e * a.expert_cb, a.expert_cb);
+    const __amdgpu_buffer_rsrc_t rc1 = buffer_rsrc((MODE == 1 ? a.codes2 : a.codes) + e * a.expert_cb, a.expert_cb);
     // rows past N repeat the last one and are not stored
-    const long long eo = e;
-    const __amdgpu_buffer_rsrc_t rc0 = buffer_rsrc(a.codes + eo * a.expert_cb, a.expert_cb);
-    const __amdgpu_buffer_rsrc_t rc1 = buffer_rsrc((MODE == 1 ? a.codes2 : a.codes) + eo * a.expert_cb, a.expert_cb);
     uint32_t oc[RF][2];
+    auto set_rows = [&](int row_base) {
 #pragma unroll
-    for (int f = 0; f < RF; ++f)
+        for (int f = 0; f < RF; ++f)
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int n = min(row_base + 16 * RH * w + 16 * (MODE == 1 ? f % RH : f) + 8 * i + lr, a.N - 1);
-            oc[f][i] = (uint32_t)n * (uint32_t)a.rcb + 16u * lc;
-        }
+            for (int i = 0; i < 2; ++i) {
+                const int n = min(row_base + 16 * RH * w + 16 * (MODE == 1 ? f % RH : f) + 8 * i + lr, N - 1);
+                oc[f][i] = (uint32_t)n * (uint32_t)a.rcb + 16u * lc;
+            }
+    };
     auto load_a = [&](int u, u32x4 (&A)[RF][2]) {
         const uint32_t so = 2 * u < S ? 128u * u : kXPast;      // (oc < 2^31: the sum does not wrap)
 #pragma unroll
@@ -434,131 +445,155 @@ __device__ __forceinline__ void mx4_tile_chunk(const Args &a, uint8_t *lds, int 
         }
     };
 
-    // staged scales: thread t takes row t % BR of the tile (gate/up: the gate's
-    // rows, then the up's -- the same tensor for all lanes of a wave), and
-    // wave w's lanes vectors 16 w .. 16 w + 15 of the chunk, four lanes each
-    // (what several lanes take they all write)
-    const int sr = tid & (BR - 1);
-    const bool up = MODE == 1 && (64 * w & (BR - 1)) >= BR / 2;
-    const uintptr_t pa = (uintptr_t)((up ? a.scales2 : a.scales) + eo * a.expert_sb), pb = (uintptr_t)a.xs;
-    const __amdgpu_buffer_rsrc_t rsa =
-        buffer_rsrc((const void *)(pa & ~(uintptr_t)3), ((long long)(pa & 3) + a.expert_sb + 3) & ~3ll);
-    const __amdgpu_buffer_rsrc_t rsb =
-        buffer_rsrc((const void *)(pb & ~(uintptr_t)3), ((long long)(pb & 3) + (long long)x_rows * a.rsb + 3) & ~3ll);
-    const int vs = 16 * w + c;
-    const uint32_t osa = (uint32_t)(pa & 3) +
-                         (uint32_t)min(row_base + (MODE == 1 ? tid & (BR / 2 - 1) : sr), a.N - 1) * (uint32_t)a.rsb;
-    const uint32_t osb = (uint32_t)(pb & 3) + vec_row(vs < nv ? vs : 0) * (uint32_t)a.rsb;
+    // Scales: whole rows at once -- a row's 16 bytes of a slab alone would
+    // fetch their 128-byte line anew for every slab.  Neighbouring lanes take
+    // neighbouring slabs of a row; an odd number of 16-byte segments from row
+    // to row (bank conflicts).
+    auto stage_s = [&](const uint8_t *base, long long bytes, int rows, auto row_of, uint8_t *dst) {
+        const uintptr_t p0 = (uintptr_t)base;
+        const __amdgpu_buffer_rsrc_t r =
+            buffer_rsrc((const void *)(p0 & ~(uintptr_t)3), ((long long)(p0 & 3) + bytes + 3) & ~3ll);
+        int t0 = tid;
+        asm volatile("" : "+v"(t0));
+        const int all = rows * J;
+        constexpr int SB = 4;                                       // segments in flight (the last one again past the end)
+#pragma unroll 1
+        for (; t0 < all; t0 += SB * 64 * NW) {
+            ScaleSeg sg[SB];
+            uint32_t o[SB];
+            int at[SB], n[SB];
+#pragma unroll
+            for (int k = 0; k < SB; ++k) {
+                const int t = min(t0 + k * 64 * NW, all - 1), row = t / J, j = t - row * J;
+                o[k] = (uint32_t)(p0 & 3) + row_of(row) * rsb + 16u * j;
+                at[k] = row * SP + 16 * j;
+                n[k] = U - 16 * j;
+                sg[k] = load_seg<true>(r, o[k]);
+            }
+#pragma unroll
+            for (int k = 0; k < SB; ++k) *(u32x4 *)(dst + at[k]) = seg_order<true>(sg[k], o[k], n[k]);
+        }
+    };
+    auto stage_rows = [&](int row_base) {
+        auto tile_row = [&](int row) { return (uint32_t)min(row_base + row, N - 1); };
+        stage_s(a.scales + e * a.expert_sb, a.expert_sb, TR, tile_row, ls);
+        if constexpr (MODE == 1) stage_s(a.scales2 + e * a.expert_sb, a.expert_sb, TR, tile_row, ls + TR * SP);
+    };
     // where the wave's fragments' scales stand
-    auto seg_of_row = [&](int f) { return MODE == 1 ? (f >= RH ? BR / 2 : 0) + 16 * (w * RH + f % RH) : 16 * (w * RF + f); };
-    auto store_s = [&](int buf, const u32x4 &ra, const u32x4 &rb) {
-        *(u32x4 *)(ls + buf * (NS * 16) + sr * 16) = ra;
-        *(u32x4 *)(ls + buf * (NS * 16) + (BR + vs) * 16) = rb;
-    };
-
-    u32x4 A[NA][RF][2];
-    {
-        u32x4 X[XU], A0[RF][2];
-        load_a(0, A0);
-        load_x(0, X);
-        const ScaleSeg sa = load_seg<true>(rsa, osa), sb = load_seg<true>(rsb, osb);
-        load_a(1, A[NA - 1]);
-        if constexpr (NA == 2) load_a(2, A[0]);
-        store_a(A0);
-        store_x(0, X);
-        store_s(0, seg_order<true>(sa, osa, U), seg_order<true>(sb, osb, U));
-    }
-    __syncthreads();
+    auto seg_of_row = [&](int f) { return MODE == 1 ? (f >= RH ? TR : 0) + 16 * (w * RH + f % RH) : 16 * (w * RF + f); };
     const int rd = c * 128 + 16 * (q ^ ((c >> 1) & 7));         // step 0's chunk of lane (c, q); step 1: ^ 64
-    // LAST 0: slabs j and j + 1 are not the last; 1: slab j + 1 is; 2: slab j is
-    auto slab = [&](int j, auto LAST) {
-        constexpr int last = decltype(LAST)::value;
-        const uint8_t *const sc = ls + (j & 1) * (NS * 16) + c * 16 + 4 * q;
-        ScaleSeg sa, sb;
-        uint32_t ta[RF], tb[CF];
-        auto unit = [&](auto HALF) {
-            constexpr int h = decltype(HALF)::value;            // the unit's vector buffer too
-            constexpr bool more = last < 2 || h == 0;           // another unit follows
-            const int u = 2 * j + h;
-            u32x4 F[2][RF], B[2][CF], X[XU];
-            auto read_b = [&](int s, u32x4 (&b)[CF]) {
-#pragma unroll
-                for (int g = 0; g < CF; ++g) b[g] = *(const u32x4 *)(lx + h * XB + g * 2048 + (rd ^ (64 * s)));
-            };
-            if constexpr (h == 0) {
-#pragma unroll
-                for (int f = 0; f < RF; ++f) ta[f] = *(const uint32_t *)(sc + seg_of_row(f) * 16);
-#pragma unroll
-                for (int g = 0; g < CF; ++g) tb[g] = *(const uint32_t *)(sc + (BR + 16 * g) * 16);
-            }
-#pragma unroll
-            for (int f = 0; f < RF; ++f) F[0][f] = *(const u32x4 *)(la + f * 2048 + rd);
-            read_b(0, B[0]);
-#pragma unroll
-            for (int f = 0; f < RF; ++f) F[1][f] = *(const u32x4 *)(la + f * 2048 + (rd ^ 64));
-            if constexpr (more) load_x(u + 1, X);
-            if constexpr (h == 0 && last < 2) {
-                sa = load_seg<last == 1>(rsa, osa + 16u * (j + 1));
-                sb = load_seg<last == 1>(rsb, osb + 16u * (j + 1));
-            }
-            asm volatile("" ::: "memory");                      // (the next unit's codes go where these were)
-            if constexpr (more) {
-                store_a(A[(h ^ 1) % NA]);
-                if constexpr (last < 2 || NA == 1) load_a(u + 1 + NA, A[(h ^ 1) % NA]);
-            }
-            auto step = [&](auto SIDX) {
-                constexpr int s = decltype(SIDX)::value;
-                __builtin_amdgcn_sched_barrier(0);
-                if constexpr (s == 0) read_b(1, B[1]);
-#pragma unroll
-                for (int g = 0; g < CF; ++g)
-#pragma unroll
-                    for (int f = 0; f < RF; ++f)
-                        acc[f][g] = mfma_mx4_op<2 * h + s>(F[s][f], B[s][g], acc[f][g], ta[f], tb[g]);
-                // (the compiler would move the products past the barrier to
-                // their last use, with all their operands held until then)
-#pragma unroll
-                for (int g = 0; g < CF; ++g)
-#pragma unroll
-                    for (int f = 0; f < RF; ++f) asm volatile("" : "+v"(acc[f][g]));
-            };
-            step(std::integral_constant<int, 0>{});
-            step(std::integral_constant<int, 1>{});
-            if constexpr (more) store_x(h ^ 1, X);
-            if constexpr (h == 1 && last < 2)
-                store_s((j + 1) & 1, seg_order<last == 1>(sa, osa, U - 16 * (j + 1)),
-                        seg_order<last == 1>(sb, osb, U - 16 * (j + 1)));
-            __syncthreads();
-        };
-        unit(std::integral_constant<int, 0>{});
-        unit(std::integral_constant<int, 1>{});
-    };
-    int j = 0;
-    for (; j + 2 < J; ++j) slab(j, std::integral_constant<int, 0>{});
-    if (j + 1 < J) slab(j++, std::integral_constant<int, 1>{});
-    slab(j, std::integral_constant<int, 2>{});
+    const bool vec4 = (N & 3) == 0 && ((uintptr_t)a.y & 15) == 0;
 
-    // lane (c, q) holds rows 4 q .. 4 q + 3 of vector c of each fragment
-    const bool vec4 = (a.N & 3) == 0 && ((uintptr_t)a.y & 15) == 0;
+    // While unit u multiplies, its codes stand in LDS and those of units u + 1
+    // and u + 2 are on their way to A[(u + 1) % 2], A[u % 2] and X likewise:
+    // every load has a whole unit's time before its registers are needed.
+    // (Loads return in the order of issue: a wait for the vectors alone, one
+    // unit ahead, would wait for the weights issued before them too.)
+    u32x4 A0[RF][2], A[2][RF][2], X0[XU], X[2][XU];
+    auto first_loads = [&](int row_base) {
+        set_rows(row_base);
+        load_a(0, A0);
+        load_x(0, X0);
+        load_x(1, X[1]);
+        load_a(1, A[1]);
+        load_a(2, A[0]);
+    };
+    first_loads(rt0 * TR);
+    stage_s((const uint8_t *)a.xs, (long long)x_rows * rsb, 16 * CF, [&](int v) { return vec_row(v < nv ? v : 0); },
+            ls + BR * SP);
+    for (int rt = rt0; rt < rt1; ++rt) {
+        const int row_base = rt * TR;
+        stage_rows(row_base);
+        store_a(A0);
+        store_x(0, X0);
+        f32x4 acc[RF][CF];
 #pragma unroll
-    for (int g = 0; g < CF; ++g) {
-        const int v = 16 * g + c;
-        if (v < nv) {
-            float *const yr = a.y + (size_t)(gather ? (int)vecs[v] : vstart + v) * a.N;
+        for (int f = 0; f < RF; ++f)
 #pragma unroll
-            for (int f = 0; f < RH; ++f) {
-                const int n0 = row_base + 16 * RH * w + 16 * f + 4 * q;
-                float r[4];
+            for (int g = 0; g < CF; ++g) acc[f][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        __syncthreads();
+        auto slab = [&](int j, auto LAST) {
+            constexpr bool last = decltype(LAST)::value;
+            const uint8_t *const sc = ls + c * SP + 16 * j + 4 * q;
+            uint32_t ta[RF], tb[CF];
+            auto unit = [&](auto HALF) {
+                constexpr int h = decltype(HALF)::value;            // the unit's vector buffer too
+                constexpr bool more = !last || h == 0;              // another unit follows
+                const int u = 2 * j + h;
+                u32x4 F[2][RF], B[2][CF];
+                auto read_b = [&](int s, u32x4 (&b)[CF]) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    r[k] = MODE == 1 ? swiglu(acc[f][g][k], acc[f + RF - RH][g][k]) : acc[f][g][k];
-                if (n0 < a.N) {
-                    if (vec4) {
-                        *(float4 *)(yr + n0) = make_float4(r[0], r[1], r[2], r[3]);
-                    } else {
+                    for (int g = 0; g < CF; ++g) b[g] = *(const u32x4 *)(lx + h * XB + g * 2048 + (rd ^ (64 * s)));
+                };
+                if constexpr (h == 0) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            if (n0 + k < a.N) yr[n0 + k] = r[k];
+                    for (int f = 0; f < RF; ++f) ta[f] = *(const uint32_t *)(sc + seg_of_row(f) * SP);
+#pragma unroll
+                    for (int g = 0; g < CF; ++g) tb[g] = *(const uint32_t *)(sc + (BR + 16 * g) * SP);
+                }
+#pragma unroll
+                for (int f = 0; f < RF; ++f) F[0][f] = *(const u32x4 *)(la + f * 2048 + rd);
+                read_b(0, B[0]);
+#pragma unroll
+                for (int f = 0; f < RF; ++f) F[1][f] = *(const u32x4 *)(la + f * 2048 + (rd ^ 64));
+                if constexpr (!last) load_x(u + 2, X[h]);
+                asm volatile("" ::: "memory");                      // (the next unit's codes go where these were)
+                if constexpr (more) {
+                    store_a(A[h ^ 1]);
+                    if constexpr (!last) load_a(u + 3, A[h ^ 1]);
+                }
+                auto step = [&](auto SIDX) {
+                    constexpr int s = decltype(SIDX)::value;
+                    __builtin_amdgcn_sched_barrier(0);
+                    if constexpr (s == 0) read_b(1, B[1]);
+#pragma unroll
+                    for (int g = 0; g < CF; ++g)
+#pragma unroll
+                        for (int f = 0; f < RF; ++f)
+                            acc[f][g] = mfma_mx4_op<2 * h + s>(F[s][f], B[s][g], acc[f][g], ta[f], tb[g]);
+                    // (the compiler would move the products past the barrier to
+                    // their last use, with all their operands held until then)
+#pragma unroll
+                    for (int g = 0; g < CF; ++g)
+#pragma unroll
+                        for (int f = 0; f < RF; ++f) asm volatile("" : "+v"(acc[f][g]));
+                };
+                step(std::integral_constant<int, 0>{});
+                step(std::integral_constant<int, 1>{});
+                if constexpr (more) store_x(h ^ 1, X[h ^ 1]);
+                __syncthreads();
+            };
+            unit(std::integral_constant<int, 0>{});
+            unit(std::integral_constant<int, 1>{});
+        };
+        for (int j = 0; j + 1 < J; ++j) slab(j, std::false_type{});
+        slab(J - 1, std::true_type{});
+
+        // the next tile's first loads go out before this tile's results
+        if (rt + 1 < rt1) first_loads(row_base + TR);
+        // lane (c, q) holds rows 4 q .. 4 q + 3 of vector c of each fragment
+        int vc = c;
+        asm volatile("" : "+v"(vc));                                // (the rows' addresses are formed here, not kept)
+#pragma unroll
+        for (int g = 0; g < CF; ++g) {
+            const int v = 16 * g + vc;
+            if (v < nv) {
+                float *const yr = a.y + (size_t)(gather ? (int)vecs[v] : vstart + v) * N;
+#pragma unroll
+                for (int f = 0; f < RH; ++f) {
+                    const int n0 = row_base + 16 * RH * w + 16 * f + 4 * q;
+                    float r[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        r[k] = MODE == 1 ? swiglu(acc[f][g][k], acc[f + RF - RH][g][k]) : acc[f][g][k];
+                    if (n0 < N) {
+                        if (vec4) {
+                            *(float4 *)(yr + n0) = make_float4(r[0], r[1], r[2], r[3]);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (n0 + k < N) yr[n0 + k] = r[k];
+                        }
                     }
                 }
             }
@@ -566,68 +601,65 @@ __device__ __forceinline__ void mx4_tile_chunk(const Args &a, uint8_t *lds, int 
     }
 }
 
-// Workgroup b runs on XCD b % 8; the call's tiles (item-major) are dealt to
-// the XCDs in contiguous runs, so that an XCD's L2 holds the vectors of a few
-// experts, and an expert's second chunk finds its weights there.
-#ifndef XRF
-#define XRF 4
-#define XNA 2
-#define XWPE 2
-#endif
+// A workgroup takes a run of up to bt_chunk row tiles of one item.  Workgroup
+// b runs on XCD b % 8; the runs (item-major) are dealt to the XCDs in
+// contiguous parts, so that an XCD's L2 holds the vectors of a few experts,
+// and an expert's second chunk finds its weights there.
 template <int MODE>
-__global__ __launch_bounds__(256, XWPE) void qmv_mx4_tile_kernel(const Args a)
+__global__ __launch_bounds__(64 * kMx4Waves, 2) void qmv_mx4_tile_kernel(const Args a)
 {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    constexpr int RF = XRF, NW = 4, NA = XNA;
-    constexpr int TR = 16 * RF * NW / (MODE == 1 ? 2 : 1);
+    constexpr int TR = 16 * kMx4RF * kMx4Waves / (MODE == 1 ? 2 : 1);
     uint16_t *const list = (uint16_t *)lds;           // [kMx4Chunk]
     uint8_t *const buf = lds + 2 * kMx4Chunk;
-    const int b = blockIdx.x;
-    int tile = -1;
+    const int runs = (a.bt_row_tiles + a.bt_chunk - 1) / a.bt_chunk;   // per item
+    int item = -1, rt0 = 0, rt1 = 0;
     auto pick = [&](int items) {
-        const int tiles = items * a.bt_row_tiles, per_xcd = (tiles + 7) / 8;
-        const int i = b >> 3;
-        if (i < per_xcd) tile = (b & 7) * per_xcd + i;
-        if (tile >= tiles) tile = -1;
-        return tile < 0 ? -1 : tile / a.bt_row_tiles;
+        const int all = items * runs, per_xcd = (all + 7) / 8, i = blockIdx.x >> 3;
+        const int r = i < per_xcd ? (int)(blockIdx.x & 7) * per_xcd + i : all;
+        if (r < all) {
+            item = r / runs;
+            rt0 = (r - item * runs) * a.bt_chunk;
+            rt1 = min(rt0 + a.bt_chunk, a.bt_row_tiles);
+        }
+        return item;
     };
-    int e = 0, nv, vstart = 0, item;
+    int e = 0, nv, vstart = 0;
     const bool gather = a.ids != nullptr;
     if (gather) {
         // (a call without any id in [0, E) still has its zero rows: one item)
         const int P = a.M * a.top_k;
         const Mx4Item it = mx4_item(a.ids, P, a.E, (int *)buf, list, [&](int items) { return pick(max(items, 1)); });
-        if (tile < 0) return;
-        item = tile / a.bt_row_tiles;
+        if (item < 0) return;
         e = it.e;
         nv = it.nv;
         // the rows of ids outside [0, E) are zeros: item i takes the pairs
-        // i, i + items, ... for its rows
-        const int items = max(it.items, 1), row_base = (tile - item * a.bt_row_tiles) * TR;
-        const int rows = min(TR, a.N - row_base), lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-        for (int p0 = item + items * 16 * w; p0 < P; p0 += items * 16 * NW) {
+        // i, i + items, ... for its tiles' rows
+        int tid = threadIdx.x;
+        asm volatile("" : "+v"(tid));
+        const int items = max(it.items, 1), n0 = rt0 * TR, rows = min(rt1 * TR, a.N) - n0;
+        const int lane = tid & 63, w = tid >> 6;
+        for (int p0 = item + items * 16 * w; p0 < P; p0 += items * 16 * kMx4Waves) {
             const int p = p0 + items * (lane & 15);
             const bool bad = lane < 16 && p < P && (unsigned)a.ids[min(p, P - 1)] >= (unsigned)a.E;
             for (unsigned long long m = __ballot(bad); m; m &= m - 1) {
-                float *const yr = a.y + (size_t)(p0 + items * (__ffsll((long long)m) - 1)) * a.N + row_base;
+                float *const yr = a.y + (size_t)(p0 + items * (__ffsll((long long)m) - 1)) * a.N + n0;
                 for (int o = lane; o < rows; o += 64) yr[o] = 0.0f;
             }
         }
         if (nv == 0) return;
     } else {
-        item = pick((a.M + kMx4Chunk - 1) / kMx4Chunk);
-        if (item < 0) return;
+        if (pick((a.M + kMx4Chunk - 1) / kMx4Chunk) < 0) return;
         vstart = item * kMx4Chunk;
         nv = min(kMx4Chunk, a.M - vstart);
     }
-    const int row_base = (tile - item * a.bt_row_tiles) * TR;
     const uint16_t *const vecs = gather ? list : nullptr;
-    if (nv <= 16)
-        mx4_tile_chunk<MODE, RF, 1, NW, NA>(a, buf, e, row_base, vecs, vstart, nv);
-    else if (nv <= 32)
-        mx4_tile_chunk<MODE, RF, 2, NW, NA>(a, buf, e, row_base, vecs, vstart, nv);
+    if (nv > 32)
+        mx4_tile_run<MODE, 4>(a, buf, e, rt0, rt1, vecs, vstart, nv);
+    else if (nv > 16)
+        mx4_tile_run<MODE, 2>(a, buf, e, rt0, rt1, vecs, vstart, nv);
     else
-        mx4_tile_chunk<MODE, RF, 4, NW, NA>(a, buf, e, row_base, vecs, vstart, nv);
+        mx4_tile_run<MODE, 1>(a, buf, e, rt0, rt1, vecs, vstart, nv);
 }
 
 extern const void *const kTableMx4Tile[2];
