@@ -109,6 +109,22 @@ def _dev_ptr(t, name, dtypes, device):
     return t.data_ptr()
 
 
+# the current stream's handle without a Stream object around it (0.1 against
+# 1.9 us a call)
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _on_device(fn, device, stream, *args):
+    """fn(*args, stream handle) with the tensors' GPU as the current one: the
+    library launches on the current device's default stream for handle 0."""
+    handle = _current_raw_stream(device.index) if stream is None else stream.cuda_stream
+    if torch.cuda.current_device() == device.index:
+        return fn(*args, handle)
+    with torch.cuda.device(device):
+        return fn(*args, handle)
+
+
 def _stream(device, stream):
     if stream is None:
         stream = torch.cuda.current_stream(device)
@@ -150,11 +166,6 @@ def _nbytes(t):
     return t.numel() * t.element_size()
 
 
-def _need(cond, msg):
-    if not cond:
-        raise ValueError(msg)
-
-
 def _check_weights(w, codes, scales, lead, K, what=("w_codes", "w_scales")):
     """codes/scales hold exactly the rows the kernel will address: leading
     dimensions ``lead`` ((E, N) or (N,)) and the row bytes of K weights."""
@@ -162,13 +173,14 @@ def _check_weights(w, codes, scales, lead, K, what=("w_codes", "w_scales")):
     rows = 1
     for d in lead:
         rows *= d
+    n = len(lead)
     for t, name, per_row in ((codes, what[0], rcb), (scales, what[1], rsb)):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
-        _need(tuple(t.shape[:len(lead)]) == tuple(lead) and _nbytes(t) == rows * per_row,
-              f"{name} has shape {tuple(t.shape)} ({_nbytes(t)} bytes), expected leading "
-              f"dimensions {tuple(lead)} and {per_row} bytes per row for K={K} "
-              f"({rows * per_row} bytes)")
+        if t.shape[:n] != lead or _nbytes(t) != rows * per_row:
+            raise ValueError(f"{name} has shape {tuple(t.shape)} ({_nbytes(t)} bytes), expected leading "
+                             f"dimensions {tuple(lead)} and {per_row} bytes per row for K={K} "
+                             f"({rows * per_row} bytes)")
 
 
 def _check_x(x, x_scales, vectors, K, a):
@@ -177,19 +189,18 @@ def _check_x(x, x_scales, vectors, K, a):
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
     held = K // 2 if a == A_MXFP4 else K
-    _need(x.dim() >= 1 and x.shape[-1] == held and x.numel() == vectors * held,
-          f"x has shape {tuple(x.shape)}, expected {vectors} vectors of K={K}")
-    if a == A_MXFP4:
-        _need(isinstance(x_scales, torch.Tensor), "MXFP4 activations need x_scales (uint8, one per 32)")
-        _need(x_scales.numel() == vectors * (K // 32),
-              f"x_scales has shape {tuple(x_scales.shape)}, expected {vectors} x {K // 32} E8M0 scales")
-        return
-    if a == A_Q8B32:
-        _need(isinstance(x_scales, torch.Tensor), "int8 activations need x_scales (float16, one per 32)")
-        _need(x_scales.numel() == vectors * (K // 32),
-              f"x_scales has shape {tuple(x_scales.shape)}, expected {vectors} x {K // 32} fp16 scales")
-    else:
-        _need(x_scales is None, "x_scales is only used with int8 activations")
+    if not (x.dim() >= 1 and x.shape[-1] == held and x.numel() == vectors * held):
+        raise ValueError(f"x has shape {tuple(x.shape)}, expected {vectors} vectors of K={K}")
+    if a == A_Q8B32 or a == A_MXFP4:
+        kind, scale = ("int8", "fp16") if a == A_Q8B32 else ("MXFP4", "E8M0")
+        if not isinstance(x_scales, torch.Tensor):
+            raise ValueError(f"{kind} activations need x_scales "
+                             f"({'float16' if a == A_Q8B32 else 'uint8'}, one per 32)")
+        if x_scales.numel() != vectors * (K // 32):
+            raise ValueError(f"x_scales has shape {tuple(x_scales.shape)}, expected {vectors} x {K // 32} "
+                             f"{scale} scales")
+    elif x_scales is not None:
+        raise ValueError("x_scales is only used with int8 or MXFP4 activations")
 
 
 def _k_of(w, x):
@@ -205,15 +216,16 @@ def _check_y(y, shape):
     n = 1
     for d in shape:
         n *= d
-    _need(isinstance(y, torch.Tensor) and y.numel() == n and y.dtype == torch.float32,
-          f"y has shape {tuple(y.shape)} and dtype {y.dtype}, expected float32 {tuple(shape)}")
+    if not (isinstance(y, torch.Tensor) and y.numel() == n and y.dtype == torch.float32):
+        raise ValueError(f"y has shape {tuple(y.shape)} and dtype {y.dtype}, expected float32 {tuple(shape)}")
 
 
 def _check_ids(expert_ids):
     if not isinstance(expert_ids, torch.Tensor):
         raise TypeError("expert_ids must be a torch.Tensor")
-    _need(expert_ids.dim() == 2, f"expert_ids has shape {tuple(expert_ids.shape)}, expected [M][top_k]")
-    return expert_ids.shape[0], expert_ids.shape[1]
+    if expert_ids.dim() != 2:
+        raise ValueError(f"expert_ids has shape {tuple(expert_ids.shape)}, expected [M][top_k]")
+    return expert_ids.shape
 
 
 def _per_slot(x, x_per_slot, M, top_k):
@@ -221,9 +233,8 @@ def _per_slot(x, x_per_slot, M, top_k):
     if x_per_slot is None:
         return isinstance(x, torch.Tensor) and x.dim() == 3
     x_per_slot = bool(x_per_slot)
-    if isinstance(x, torch.Tensor) and x.dim() == 3:
-        _need(x_per_slot and tuple(x.shape[:2]) == (M, top_k),
-              f"x has shape {tuple(x.shape)}: a 3-D x is [M][top_k][K] per-slot activations")
+    if isinstance(x, torch.Tensor) and x.dim() == 3 and not (x_per_slot and x.shape[:2] == (M, top_k)):
+        raise ValueError(f"x has shape {tuple(x.shape)}: a 3-D x is [M][top_k][K] per-slot activations")
     return x_per_slot
 
 
@@ -236,7 +247,8 @@ def qmv_dense(wfmt, w_codes, w_scales, x, x_scales=None, y=None, stream=None):
     """Dense GEMV: y[m][n] = sum_k w(n,k) x(m,k); returns y (float32 [M][N]).
     ``x`` is [M][K]."""
     w = _wfmt(wfmt)
-    _need(isinstance(x, torch.Tensor) and x.dim() == 2, "x must be a 2-D tensor [M][K]")
+    if not (isinstance(x, torch.Tensor) and x.dim() == 2):
+        raise ValueError("x must be a 2-D tensor [M][K]")
     M, K = x.shape[0], _k_of(w, x)
     N = w_codes.shape[0]
     a, xd = _afmt(w, x)
@@ -248,11 +260,11 @@ def qmv_dense(wfmt, w_codes, w_scales, x, x_scales=None, y=None, stream=None):
     _gpu(dev, "qmv_dense")
     if y is None:
         y = torch.empty((M, N), dtype=torch.float32, device=dev)
-    s = lib().qmv_dense(w, _dev_ptr(w_codes, "w_codes", (torch.uint8,), dev),
+    s = _on_device(lib().qmv_dense, dev, stream, w, _dev_ptr(w_codes, "w_codes", (torch.uint8,), dev),
                         _dev_ptr(w_scales, "w_scales", _SCALE_DT, dev), a,
                         _dev_ptr(x, "x", xd, dev),
                         _dev_ptr(x_scales, "x_scales", _xs_dtypes(a), dev),
-                        _dev_ptr(y, "y", (torch.float32,), dev), M, N, K, _stream(dev, stream))
+                        _dev_ptr(y, "y", (torch.float32,), dev), M, N, K)
     _check(s)
     return y
 
@@ -278,13 +290,13 @@ def qmv_gather_moe(wfmt, w_codes, w_scales, expert_ids, x, x_scales=None, x_per_
     _gpu(dev, "qmv_gather_moe")
     if y is None:
         y = torch.empty((M, top_k, N), dtype=torch.float32, device=dev)
-    s = lib().qmv_gather_moe(w, _dev_ptr(w_codes, "w_codes", (torch.uint8,), dev),
+    s = _on_device(lib().qmv_gather_moe, dev, stream, w, _dev_ptr(w_codes, "w_codes", (torch.uint8,), dev),
                              _dev_ptr(w_scales, "w_scales", _SCALE_DT, dev), E,
                              _dev_ptr(expert_ids, "expert_ids", (torch.int32,), dev), M, top_k, a,
                              _dev_ptr(x, "x", xd, dev),
                              _dev_ptr(x_scales, "x_scales", _xs_dtypes(a), dev),
                              int(per_slot),
-                             _dev_ptr(y, "y", (torch.float32,), dev), N, K, _stream(dev, stream))
+                             _dev_ptr(y, "y", (torch.float32,), dev), N, K)
     _check(s)
     return y
 
@@ -307,14 +319,14 @@ def qmv_gather_moe_swiglu(wfmt, gate_codes, gate_scales, up_codes, up_scales, ex
     _gpu(dev, "qmv_gather_moe_swiglu")
     if y is None:
         y = torch.empty((M, top_k, N), dtype=torch.float32, device=dev)
-    s = lib().qmv_gather_moe_swiglu(
-        w, _dev_ptr(gate_codes, "gate_codes", (torch.uint8,), dev),
+    s = _on_device(
+        lib().qmv_gather_moe_swiglu, dev, stream, w, _dev_ptr(gate_codes, "gate_codes", (torch.uint8,), dev),
         _dev_ptr(gate_scales, "gate_scales", _SCALE_DT, dev),
         _dev_ptr(up_codes, "up_codes", (torch.uint8,), dev),
         _dev_ptr(up_scales, "up_scales", _SCALE_DT, dev), E,
         _dev_ptr(expert_ids, "expert_ids", (torch.int32,), dev), M, top_k, a,
         _dev_ptr(x, "x", xd, dev), _dev_ptr(x_scales, "x_scales", _xs_dtypes(a), dev),
-        _dev_ptr(y, "y", (torch.float32,), dev), N, K, _stream(dev, stream))
+        _dev_ptr(y, "y", (torch.float32,), dev), N, K)
     _check(s)
     return y
 
@@ -350,8 +362,8 @@ def _combine(entry, wfmt, w_codes, w_scales, expert_ids, route_weights, x, x_sca
     E, N = w_codes.shape[0], w_codes.shape[1]
     if not isinstance(route_weights, torch.Tensor):
         raise TypeError("route_weights must be a torch.Tensor")
-    _need(tuple(route_weights.shape) == (M, top_k),
-          f"route_weights has shape {tuple(route_weights.shape)}, expected {(M, top_k)}")
+    if route_weights.shape != (M, top_k):
+        raise ValueError(f"route_weights has shape {tuple(route_weights.shape)}, expected {(M, top_k)}")
     K = _k_of(w, x)
     per_slot = _per_slot(x, x_per_slot, M, top_k)
     a, xd = _afmt(w, x)
@@ -363,14 +375,13 @@ def _combine(entry, wfmt, w_codes, w_scales, expert_ids, route_weights, x, x_sca
     _gpu(dev, entry)
     if y is None:
         y = torch.empty((M, N), dtype=torch.float32, device=dev)
-    s = getattr(lib(), entry)(
-        w, _dev_ptr(w_codes, "w_codes", (torch.uint8,), dev),
+    s = _on_device(
+        getattr(lib(), entry), dev, stream, w, _dev_ptr(w_codes, "w_codes", (torch.uint8,), dev),
         _dev_ptr(w_scales, "w_scales", _SCALE_DT, dev), E,
         _dev_ptr(expert_ids, "expert_ids", (torch.int32,), dev),
         _dev_ptr(route_weights, "route_weights", (torch.float32,), dev), M, top_k, a,
         _dev_ptr(x, "x", xd, dev), _dev_ptr(x_scales, "x_scales", _xs_dtypes(a), dev),
-        int(per_slot), _dev_ptr(y, "y", (torch.float32,), dev), N, K,
-        _stream(dev, stream))
+        int(per_slot), _dev_ptr(y, "y", (torch.float32,), dev), N, K)
     _check(s)
     return y
 

@@ -22,6 +22,8 @@ import os
 
 import torch
 
+import bit_block_quantized_amd as _q
+
 __all__ = ["qmx_rmsnorm", "qmx_router", "qmx_quantize", "qmx_dequantize", "qmx_strerror", "qmx_lib",
            "QMX_LIB_PATH"]
 
@@ -103,22 +105,15 @@ def _out(t, name, spec, device):
     """The caller's output, checked, or a new one."""
     if t is None:
         return torch.empty(spec[1], dtype=spec[0], device=device)
-    _tensor(t, name, (spec[0],), device, torch.Size(spec[1]))
+    _tensor(t, name, (spec[0],), device, spec[1])
     return t
 
 
 def _run(entry, device, stream, *args):
-    """Call a library entry on the tensors' GPU (made current for the call)."""
-    s = torch.cuda.current_stream(device) if stream is None else stream
-    fn = getattr(qmx_lib(), entry)
-    if torch.cuda.current_device() == device.index:
-        status = fn(*args, s.cuda_stream)
-    else:
-        with torch.cuda.device(device):
-            status = fn(*args, s.cuda_stream)
+    """Call a library entry on the tensors' GPU and stream."""
+    status = _q._on_device(getattr(_lib or qmx_lib(), entry), device, stream, *args)
     if status != 0:
-        from . import QmvError
-        raise QmvError(status, qmx_strerror(status))
+        raise _q.QmvError(status, qmx_strerror(status))
 
 
 def _gpu(t, entry):
@@ -218,7 +213,7 @@ def qmx_dequantize(codes, scales, fmt="mxfp4", dtype=torch.bfloat16, y=None, str
     K = 2 * n if fmt == "mxfp4" else n
     _blocks(K, "codes")
     _, ss = _code_spec(fmt, tuple(codes.shape[:-1]), K)
-    _tensor(scales, "scales", (ss[0],), codes.device, torch.Size(ss[1]))
+    _tensor(scales, "scales", (ss[0],), codes.device, ss[1])
     _gpu(codes, "qmx_dequantize")
     y = _out(y, "y", (dtype, tuple(codes.shape[:-1]) + (K,)), codes.device)
     _run("qmx_dequantize", codes.device, stream, _FMT[fmt], codes.data_ptr(), scales.data_ptr(), _TYPE[dtype],
