@@ -583,6 +583,8 @@ qmv_status_t launch_dense4(const void *codes, const void *scales, const void *x,
 
 std::once_flag g_mx4_once[2];
 hipError_t g_mx4_err[2];
+std::once_flag g_mx4_few_once[3];
+hipError_t g_mx4_few_err[3];
 
 // LDS of a tile workgroup: the chunk's list, two buffers of vector codes (64
 // vectors x 128 bytes), the waves' weight pieces (rows x 128 bytes), and the
@@ -608,7 +610,11 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
     a.x_vec_bytes = K / 2;
     const int mode = route_w ? 2 : codes2 ? 1 : 0;
     const int pairs = gather ? M * top_k : M;
-    if (mode != 2 && pairs >= (gather ? 2 * E : 17)) {
+    // the few kernel's LDS: weight pieces, the vectors (codes and scales), the rows' scales
+    const int U = K / 32, J = (U + 15) / 16, h = mode == 1 ? 2 : 1;
+    const int xp = (U + 7) / 8 * 128 + 16, sp = 16 * (J | 1), most = pairs < 16 ? pairs : 16;
+    size_t lds_few = 64 + 4 * h * 2048 + (size_t)most * (xp + sp) + (size_t)h * 16 * sp;
+    if (mode != 2 && (pairs >= (gather ? 2 * E : 17) || lds_few > kLdsPerCU)) {
         const int rows = mode == 1 ? 64 : 128;
         a.bt_row_tiles = (N + rows - 1) / rows;
         // items at most: a chunk per 64 pairs and a rest per expert
@@ -633,8 +639,38 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
         return hipLaunchKernel(kTableMx4Tile[fn], dim3((unsigned)(8 * ((groups + 7) / 8))), dim3(256), kargs,
                                lds, stream) == hipSuccess ? QMV_OK : QMV_EHIP;
     }
-    const dim3 grid((unsigned)((N + 15) / 16), (unsigned)(route_w ? M : gather ? (pairs < E ? pairs : E) : (M + 15) / 16));
-    const size_t lds = 4 * (mode == 1 ? 2 : 1) * 1024 + kPairCountBytes + (((size_t)2 * pairs + 15) & ~(size_t)15);
+    // few vectors: 16-row tiles, K split over the waves
+    a.bt_row_tiles = (N + 15) / 16;
+    a.bt_chunk = 1;
+    size_t lds = lds_few;
+    dim3 grid((unsigned)a.bt_row_tiles, 1);
+    if (mode == 2) {
+        // as many slots staged at a time as 64 KB hold
+        const int per_slot = xp + sp + 16 * sp, fit = 64 * 1024 / per_slot;
+        a.bt_vmax = fit < 1 ? 1 : fit < top_k ? fit : top_k;
+        lds = 64 + 4 * 2048 + (size_t)a.bt_vmax * per_slot;
+        grid.y = (unsigned)M;
+    } else {
+        a.bt_vmax = most;
+        if (gather && pairs > 64) {
+            if (lds < 64 + 4 * 1032) lds = 64 + 4 * 1032;      // the counts per expert
+            const long long items = (pairs < E ? pairs : E) + pairs / 16;
+            const long long run = items * a.bt_row_tiles / (16 * cu_count());
+            a.bt_chunk = run < 1 ? 1 : run > a.bt_row_tiles ? a.bt_row_tiles : (int)run;
+            const long long groups = items * ((a.bt_row_tiles + a.bt_chunk - 1) / a.bt_chunk);
+            grid.x = (unsigned)(8 * ((groups + 7) / 8));
+        } else if (gather) {
+            grid.y = (unsigned)(pairs * ((pairs + 15) / 16));
+        } else {
+            grid.y = (unsigned)((M + 15) / 16);
+        }
+    }
+    std::call_once(g_mx4_few_once[mode], [&] {
+        g_mx4_few_err[mode] = hipFuncSetAttribute(kTableMx4Few[mode], hipFuncAttributeMaxDynamicSharedMemorySize,
+                                                  kLdsPerCU);
+    });
+    if (g_mx4_few_err[mode] != hipSuccess)
+        return QMV_EHIP;
     void *kargs[] = {&a};
     return hipLaunchKernel(kTableMx4Few[mode], grid, dim3(256), kargs, lds, stream) == hipSuccess ? QMV_OK
                                                                                                   : QMV_EHIP;

@@ -29,158 +29,6 @@ __device__ __forceinline__ f32x4 mfma_mx4_op(u32x4 a, u32x4 b, f32x4 c, uint32_t
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, c, 4, 4, OP, (int)sa, OP, (int)sb);
 }
 
-// One 16 x 128 x 16 product; sa, sb: the lane's scale bytes in bits 0-7.
-__device__ __forceinline__ f32x4 mfma_mx4(u32x4 a, u32x4 b, f32x4 c, uint32_t sa, uint32_t sb)
-{
-    const i32x8 A = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
-    const i32x8 B = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(A, B, c, 4, 4, 0, (int)sa, 0, (int)sb);
-}
-
-// Items: 16 rows of one expert (a dense matrix, a token of a combine) and 16
-// of its vectors; the NW waves of a workgroup split K, wave w taking the
-// 128-weight steps w, w + NW, ..., and the waves' partial tiles are summed
-// in wave order.
-template <int MODE, int NW>
-__global__ __launch_bounds__(64 * NW) void qmv_mx4_few_kernel(const Args a)
-{
-    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    constexpr int H = MODE == 1 ? 2 : 1;            // weight tensors
-    constexpr int D = 4;                            // steps in flight
-    const int lane = threadIdx.x & 63;
-    const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int c = lane & 15, q = lane >> 4;
-    const int row0 = blockIdx.x * 16;
-    const int U = a.units;
-    const int S = (U + 3) >> 2;
-    const bool gather = a.ids != nullptr;
-    const int P = gather ? a.M * a.top_k : a.M;
-    f32x4 *const part = (f32x4 *)lds;               // [NW][H][64]
-    PairList L;
-    L.cnt = (int *)(lds + NW * H * 1024);
-    L.perm = (uint16_t *)(L.cnt + kMaxCounts + 4);
-
-    int e = 0, count = P, slots = 1;
-    int ids_lane = 0;                               // combine: lane j holds the id of slot j
-    if constexpr (MODE == 2) {
-        slots = a.top_k;
-        count = 1;
-        if (lane < a.top_k) ids_lane = a.ids[blockIdx.y * a.top_k + lane];
-    } else if (gather) {
-        // grid.y: one per expert, or with fewer pairs than experts one per
-        // pair (the first pair of an expert takes it)
-        const Ids8 id0 = load_ids8<64 * NW>(a.ids, P, a.E, 0);
-        const bool by_pair = P < a.E;
-        if (by_pair ? (unsigned)a.ids[blockIdx.y] >= (unsigned)a.E : blockIdx.y == 0) {
-            // the rows of ids outside [0, E) are zeros (by pair: this one's)
-            const int ci = by_pair ? 1 : list_pairs<64 * NW>(a.ids, P, a.E, -1, L, id0);
-            for (int o = threadIdx.x; o < ci * 16; o += 64 * NW) {
-                const int pz = by_pair ? (int)blockIdx.y : (int)L.perm[o >> 4];
-                if (row0 + (o & 15) < a.N) a.y[(size_t)pz * a.N + row0 + (o & 15)] = 0.0f;
-            }
-            if (by_pair) return;
-            __syncthreads();
-        }
-        e = by_pair ? a.ids[blockIdx.y] : (int)blockIdx.y;
-        count = list_pairs<64 * NW>(a.ids, P, a.E, e, L, id0);
-        if (count == 0 || (by_pair && (int)L.perm[0] != (int)blockIdx.y)) return;
-    }
-    const int rowc = row0 + c;
-    const int x_bytes = (MODE == 2 || gather ? (a.x_per_slot ? a.M * a.top_k : a.M) : a.M) * a.x_vec_bytes;
-    const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(a.x, x_bytes);
-    const __amdgpu_buffer_rsrc_t rxs = buffer_rsrc(a.xs, x_bytes / 16);
-    const int vfirst = MODE == 2 || gather ? 0 : blockIdx.y * 16;
-    const int vlast = MODE == 2 || gather ? count : min(P, vfirst + 16);
-    for (int v0 = vfirst; v0 < vlast; v0 += 16) {
-        const int nv = min(16, vlast - v0);
-        // this lane's column: a vector of the chunk (columns past nv repeat the first)
-        const int vi = c < nv ? v0 + c : v0;
-        const int pair = MODE == 2 ? blockIdx.y * a.top_k : gather ? (int)L.perm[vi] : vi;
-        int vec = pair;
-        if (MODE == 2 || gather) vec = a.x_per_slot ? pair : pair / a.top_k;
-        f32x4 acc[H], tot = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int h = 0; h < H; ++h) acc[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        // (slot, step) of this wave: slot-major, every NW-th one
-        const int total = slots * S;
-        for (int g0 = w; g0 < total; g0 += NW * D) {
-            u32x4 A[D][H], B[D];
-            uint32_t sa[D][H], sb[D];
-#pragma unroll
-            for (int d = 0; d < D; ++d) {
-                const int g = g0 + NW * d;
-                const int slot = MODE == 2 ? g / S : 0;
-                const int s = g - slot * S;
-                const int blk = 4 * s + q;
-                const bool in = g < total && blk < U;
-                int ee = e;
-                bool ok = in && rowc < a.N;
-                if constexpr (MODE == 2) {
-                    ee = __builtin_amdgcn_readlane(ids_lane, slot < slots ? slot : 0);
-                    ok = ok && (unsigned)ee < (unsigned)a.E;
-                    if ((unsigned)ee >= (unsigned)a.E) ee = 0;
-                }
-                const uint32_t oc = ok ? (uint32_t)rowc * (uint32_t)a.rcb + 16u * blk : kXPast;
-                const uint32_t os = ok ? (uint32_t)rowc * (uint32_t)a.rsb + blk : kXPast;
-#pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    const __amdgpu_buffer_rsrc_t rc =
-                        buffer_rsrc((h ? a.codes2 : a.codes) + (long long)ee * a.expert_cb, a.expert_cb);
-                    const __amdgpu_buffer_rsrc_t rs =
-                        buffer_rsrc((h ? a.scales2 : a.scales) + (long long)ee * a.expert_sb, a.expert_sb);
-                    A[d][h] = __builtin_amdgcn_raw_buffer_load_b128(rc, oc, 0, 0);
-                    sa[d][h] = __builtin_amdgcn_raw_buffer_load_b8(rs, os, 0, 0);
-                }
-                const int xv = vec + (MODE == 2 && a.x_per_slot ? slot : 0);
-                B[d] = __builtin_amdgcn_raw_buffer_load_b128(
-                    rx, in ? (uint32_t)xv * (uint32_t)a.x_vec_bytes + 16u * blk : kXPast, 0, 0);
-                sb[d] = __builtin_amdgcn_raw_buffer_load_b8(
-                    rxs, in ? (uint32_t)xv * (uint32_t)a.rsb + blk : kXPast, 0, 0);
-            }
-#pragma unroll
-            for (int d = 0; d < D; ++d) {
-                const int g = g0 + NW * d;
-#pragma unroll
-                for (int h = 0; h < H; ++h) acc[h] = mfma_mx4(A[d][h], B[d], acc[h], sa[d][h], sb[d]);
-                if constexpr (MODE == 2) {
-                    if (g < total && (g + NW) / S != g / S) {
-                        const float rw = a.route_w[blockIdx.y * a.top_k + g / S];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) tot[k] = __builtin_fmaf(rw, acc[0][k], tot[k]);
-                        acc[0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                    }
-                }
-            }
-        }
-        if constexpr (MODE == 2) acc[0] = tot;
-#pragma unroll
-        for (int h = 0; h < H; ++h) part[(w * H + h) * 64 + lane] = acc[h];
-        __syncthreads();
-        if (threadIdx.x < 64 && c < nv) {
-            f32x4 r[H];
-#pragma unroll
-            for (int h = 0; h < H; ++h) {
-                r[h] = part[h * 64 + lane];
-                for (int i = 1; i < NW; ++i) r[h] += part[(i * H + h) * 64 + lane];
-            }
-            float *const yr = a.y + (size_t)(MODE == 2 ? blockIdx.y : pair) * a.N;
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int n = row0 + 4 * q + k;
-                if (n < a.N) yr[n] = MODE == 1 ? swiglu(r[0][k], r[H - 1][k]) : r[0][k];
-            }
-        }
-        __syncthreads();
-    }
-}
-
-extern const void *const kTableMx4Few[3];
-const void *const kTableMx4Few[3] = {
-    (const void *)&qmv_mx4_few_kernel<0, 4>,
-    (const void *)&qmv_mx4_few_kernel<1, 4>,
-    (const void *)&qmv_mx4_few_kernel<2, 4>,
-};
-
 // ------------------------------------------------------------- many vectors
 // A tile is (expert, 128 weight rows) against a chunk of its vectors, 4 waves
 // of 2 x CF fragments each (RF = 2).  K goes in slabs of 512 weights (4 MFMA
@@ -249,11 +97,12 @@ __device__ __forceinline__ u32x4 seg_order(const ScaleSeg &s, uint32_t o, int n)
                  perm(h23, h01, 0x07060302u)};
 }
 
-// The routed calls' work: an expert's pairs in chunks of at most kMx4Chunk.
+// The routed calls' work: an expert's pairs in chunks of at most CHUNK.
 // Every workgroup counts the pairs per expert itself (LDS atomics on whole
 // numbers: the same counts everywhere), so the grid needs no device-wide
 // knowledge: item i is the i-th (expert, chunk) of the experts in order.
-constexpr int kMx4Chunk = 64;
+constexpr int kMx4Chunk = 64;        // tile kernel
+constexpr int kMx4Few = 16;          // few kernel
 constexpr int kMx4Waves = 4;
 constexpr int kMx4RF = 2;            // 16-row fragments per wave of a tile
 
@@ -278,7 +127,7 @@ __device__ __forceinline__ int wave_scan(int v)
 // cnt: 1024 + 8 words of LDS.  `pick` maps the number of items to this
 // workgroup's item (or -1); the chunk's pairs go to list.  ids: thread t
 // looks at ids t, t + 256, ...  Every wave finds the item by itself.
-template <class Pick>
+template <int CHUNK, class Pick>
 __device__ __forceinline__ Mx4Item mx4_item(const int32_t *ids, int P, int E, int *cnt, uint16_t *list, Pick pick)
 {
     int tid = threadIdx.x;
@@ -306,7 +155,7 @@ __device__ __forceinline__ Mx4Item mx4_item(const int32_t *ids, int P, int E, in
         c[4 * i] = v.x, c[4 * i + 1] = v.y, c[4 * i + 2] = v.z, c[4 * i + 3] = v.w;
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) n += (c[i] + kMx4Chunk - 1) / kMx4Chunk;
+    for (int i = 0; i < 16; ++i) n += (c[i] + CHUNK - 1) / CHUNK;
     int before = wave_scan(n);
     const int items = __builtin_amdgcn_readlane(before, 63);
     before -= n;
@@ -317,7 +166,7 @@ __device__ __forceinline__ Mx4Item mx4_item(const int32_t *ids, int P, int E, in
     int e = 0, chunk = 0, total = 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
-        const int k = (c[i] + kMx4Chunk - 1) / kMx4Chunk;
+        const int k = (c[i] + CHUNK - 1) / CHUNK;
         if (item >= before && item < before + k) e = 16 * lane + i, chunk = item - before, total = c[i];
         before += k;
     }
@@ -325,7 +174,7 @@ __device__ __forceinline__ Mx4Item mx4_item(const int32_t *ids, int P, int E, in
     it.e = __builtin_amdgcn_readlane(e, o);
     chunk = __builtin_amdgcn_readlane(chunk, o);
     total = __builtin_amdgcn_readlane(total, o);
-    const int nch = (total + kMx4Chunk - 1) / kMx4Chunk;
+    const int nch = (total + CHUNK - 1) / CHUNK;
     const int cs = (total + nch - 1) / nch;           // equal chunks
     it.nv = min(cs, total - chunk * cs);
     uint32_t m = 0;
@@ -338,7 +187,7 @@ __device__ __forceinline__ Mx4Item mx4_item(const int32_t *ids, int P, int E, in
     } else {
         // the pairs of e in (thread, round) order, the same in every
         // workgroup: this chunk's ranks
-        n = __popc(m);
+        n = (int)__popc(m);
         int rank = wave_scan(n);
         if (lane == 63) info[w] = rank;
         __syncthreads();
@@ -350,6 +199,23 @@ __device__ __forceinline__ Mx4Item mx4_item(const int32_t *ids, int P, int E, in
     }
     __syncthreads();
     return it;
+}
+
+// The rows [n0, n1) of pairs whose id is outside [0, E) are zeros: of `items`
+// items, item i takes the pairs i, i + items, ...
+__device__ __forceinline__ void mx4_zero_rows(const Args &a, int item, int items, int n0, int n1)
+{
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));
+    const int lane = tid & 63, w = tid >> 6, P = a.M * a.top_k;
+    for (int p0 = item + items * 16 * w; p0 < P; p0 += items * 16 * kMx4Waves) {
+        const int p = p0 + items * (lane & 15);
+        const bool bad = lane < 16 && p < P && (unsigned)a.ids[min(p, P - 1)] >= (unsigned)a.E;
+        for (unsigned long long m = __ballot(bad); m; m &= m - 1) {
+            float *const yr = a.y + (size_t)(p0 + items * (__ffsll((long long)m) - 1)) * a.N;
+            for (int n = n0 + lane; n < n1; n += 64) yr[n] = 0.0f;
+        }
+    }
 }
 
 // Bytes from row to row of the staged scales of J slabs.
@@ -629,24 +495,11 @@ __global__ __launch_bounds__(64 * kMx4Waves, 2) void qmv_mx4_tile_kernel(const A
     if (gather) {
         // (a call without any id in [0, E) still has its zero rows: one item)
         const int P = a.M * a.top_k;
-        const Mx4Item it = mx4_item(a.ids, P, a.E, (int *)buf, list, [&](int items) { return pick(max(items, 1)); });
+        const Mx4Item it = mx4_item<kMx4Chunk>(a.ids, P, a.E, (int *)buf, list, [&](int items) { return pick(max(items, 1)); });
         if (item < 0) return;
         e = it.e;
         nv = it.nv;
-        // the rows of ids outside [0, E) are zeros: item i takes the pairs
-        // i, i + items, ... for its tiles' rows
-        int tid = threadIdx.x;
-        asm volatile("" : "+v"(tid));
-        const int items = max(it.items, 1), n0 = rt0 * TR, rows = min(rt1 * TR, a.N) - n0;
-        const int lane = tid & 63, w = tid >> 6;
-        for (int p0 = item + items * 16 * w; p0 < P; p0 += items * 16 * kMx4Waves) {
-            const int p = p0 + items * (lane & 15);
-            const bool bad = lane < 16 && p < P && (unsigned)a.ids[min(p, P - 1)] >= (unsigned)a.E;
-            for (unsigned long long m = __ballot(bad); m; m &= m - 1) {
-                float *const yr = a.y + (size_t)(p0 + items * (__ffsll((long long)m) - 1)) * a.N + n0;
-                for (int o = lane; o < rows; o += 64) yr[o] = 0.0f;
-            }
-        }
+        mx4_zero_rows(a, item, max(it.items, 1), rt0 * TR, min(rt1 * TR, a.N));
         if (nv == 0) return;
     } else {
         if (pick((a.M + kMx4Chunk - 1) / kMx4Chunk) < 0) return;
@@ -661,6 +514,260 @@ __global__ __launch_bounds__(64 * kMx4Waves, 2) void qmv_mx4_tile_kernel(const A
     else
         mx4_tile_run<MODE, 1>(a, buf, e, rt0, rt1, vecs, vstart, nv);
 }
+
+// -------------------------------------------------------------- few vectors
+// Up to 16 vectors of an expert (a dense matrix) against a run of 16-row
+// tiles, or (MODE 2, the combine) a token's slots, each with its expert,
+// against one 16-row tile.  The call waits for its weight bytes, so the 4
+// waves of a workgroup split K -- wave w takes units (256 weights) w, w + 4,
+// ... -- and each has up to kFewAhead units of its rows on their way from the
+// start; the vectors and the scale bytes are staged in LDS once.  The waves'
+// partial tiles are summed in wave order.  Columns past the last vector
+// repeat one (nothing of them is stored).
+constexpr int kFewAhead = 4;
+
+// Bytes from vector to vector of the staged codes: whole units, and 16 more
+// so that the 16 vectors of a read lie in different bank groups.
+__host__ __device__ constexpr int mx4_x_pitch(int U) { return (U + 7) / 8 * 128 + 16; }
+
+template <int MODE>
+__global__ __launch_bounds__(64 * kMx4Waves) void qmv_mx4_few_kernel(const Args a)
+{
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    constexpr int NW = kMx4Waves, H = MODE == 1 ? 2 : 1, D = kFewAhead;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = lane & 15, q = lane >> 4, lr = lane >> 3, lc = lane & 7;
+    const int U = a.units, J = (U + 15) >> 4, NU = (U + 7) >> 3;
+    const int SP = mx4_scale_pitch(J), XP = mx4_x_pitch(U);
+    const int N = a.N;
+    const uint32_t rsb = (uint32_t)a.rsb;
+    const bool gather = MODE != 2 && a.ids != nullptr;
+    const int P = gather ? a.M * a.top_k : a.M;
+
+    uint16_t *const list = (uint16_t *)lds;                    // [kMx4Few]
+    uint8_t *const la = lds + 64 + w * (H * 2048);             // this wave's weight pieces; its partial sums
+    uint8_t *const lx = lds + 64 + NW * H * 2048;              // [vectors] x XP
+    uint8_t *const lxs = lx + a.bt_vmax * XP;                  // [vectors] x SP
+    uint8_t *const ls = lxs + a.bt_vmax * SP;                  // [H or slots][16 rows] x SP
+
+    // ---- which expert, vectors and row tiles
+    int e = 0, nv = 1, v0 = 0, rt0 = blockIdx.x * a.bt_chunk, rt1;
+    int ids_lane = 0;
+    float rw_lane = 0.0f;
+    if constexpr (MODE == 2) {
+        // lane j holds slot j's expert and weight
+        if (lane < a.top_k) {
+            ids_lane = a.ids[blockIdx.y * a.top_k + lane];
+            rw_lane = a.route_w[blockIdx.y * a.top_k + lane];
+        }
+        rt1 = rt0 + 1;
+    } else if (!gather) {
+        rt1 = min(rt0 + a.bt_chunk, a.bt_row_tiles);
+        v0 = blockIdx.y * kMx4Few;
+        nv = min(kMx4Few, a.M - v0);
+    } else if (P <= 64) {
+        // workgroup row blockIdx.y: pair blockIdx.y's expert, if no earlier
+        // pair has it (up to 64 pairs: one lane each)
+        rt1 = min(rt0 + a.bt_chunk, a.bt_row_tiles);
+        const int id = lane < P ? a.ids[lane] : -1, y = blockIdx.y % P;
+        const int chunk = blockIdx.y / P;                      // of 16 pairs of the expert
+        e = __builtin_amdgcn_readlane(id, y);
+        if ((unsigned)e >= (unsigned)a.E) {
+            if (chunk == 0)
+                for (int n = rt0 * 16 + tid; n < min(rt1 * 16, N); n += 64 * NW) a.y[(size_t)y * N + n] = 0.0f;
+            return;
+        }
+        const unsigned long long m = __ballot(id == e);
+        if (__ffsll((long long)m) - 1 != y) return;
+        // (bit counts are unsigned: as int before anything is subtracted)
+        const int r = (int)__popcll(m & ((1ull << lane) - 1ull)) - chunk * kMx4Few;
+        const int left = (int)__popcll(m) - chunk * kMx4Few;
+        if (left <= 0) return;
+        nv = min(left, kMx4Few);
+        if ((m >> lane & 1) && r >= 0 && r < kMx4Few) list[r] = (uint16_t)lane;    // (every wave the same)
+    } else {
+        const int runs = (a.bt_row_tiles + a.bt_chunk - 1) / a.bt_chunk;
+        int item = -1;
+        rt1 = 0;
+        const Mx4Item it = mx4_item<kMx4Few>(a.ids, P, a.E, (int *)(lds + 64), list, [&](int items) {
+            const int all = max(items, 1) * runs, per_xcd = (all + 7) / 8, i = blockIdx.x >> 3;
+            const int r = i < per_xcd ? (int)(blockIdx.x & 7) * per_xcd + i : all;
+            if (r < all) {
+                item = r / runs;
+                rt0 = (r - item * runs) * a.bt_chunk;
+                rt1 = min(rt0 + a.bt_chunk, a.bt_row_tiles);
+            }
+            return item;
+        });
+        if (item < 0) return;
+        e = it.e;
+        nv = it.nv;
+        mx4_zero_rows(a, item, max(it.items, 1), rt0 * 16, min(rt1 * 16, N));
+        if (nv == 0) return;
+        __syncthreads();                                       // (the counts lie where the staging goes)
+    }
+    const bool routed = MODE == 2 || gather;
+    const int vmask = nv - 1;                                  // columns past nv repeat
+    const int top_k = a.top_k;
+    const int x_rows = routed && a.x_per_slot ? a.M * top_k : a.M;
+    auto pair_of = [&](int v) { return MODE == 2 ? (int)blockIdx.y * top_k + v : gather ? (int)list[v] : v0 + v; };
+    auto vec_row = [&](int v) -> uint32_t {
+        const int p = pair_of(v);
+        return (uint32_t)(routed && !a.x_per_slot ? p / top_k : p);
+    };
+
+    // ---- groups of slots (MODE 2: bt_vmax at a time; else one pass a row tile)
+    const int slots = MODE == 2 ? top_k : 1, per = MODE == 2 ? a.bt_vmax : 1;
+    const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(a.x, (long long)x_rows * a.x_vec_bytes);
+    f32x4 tot = {0.0f, 0.0f, 0.0f, 0.0f};
+    u32x4 A[D][H][2];
+    for (int rt = rt0; rt < rt1; ++rt) {
+        const int row0 = rt * 16;
+        uint32_t oc[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) oc[i] = (uint32_t)min(row0 + 8 * i + lr, N - 1) * (uint32_t)a.rcb + 16u * lc;
+        for (int s0 = 0; s0 < slots; s0 += per) {
+            const int ns = min(per, slots - s0), total = ns * NU;
+            auto load_a = [&](int i, u32x4 (&R)[H][2]) {
+                const int g = w + NW * i;
+                const int slot = MODE == 2 ? g / NU : 0, u = g - slot * NU;
+                int ee = e;
+                long long size = a.expert_cb;
+                if constexpr (MODE == 2) {
+                    ee = __builtin_amdgcn_readlane(ids_lane, g < total ? s0 + slot : 0);
+                    if ((unsigned)ee >= (unsigned)a.E) ee = 0, size = 0;           // reads zeros
+                }
+                const uint32_t so = g < total ? 128u * u : kXPast;
+#pragma unroll
+                for (int h = 0; h < H; ++h) {                                      // (nt: read once)
+                    const __amdgpu_buffer_rsrc_t rc = buffer_rsrc((h ? a.codes2 : a.codes) + ee * a.expert_cb, size);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) R[h][k] = __builtin_amdgcn_raw_buffer_load_b128(rc, oc[k] + so, 0, 2);
+                }
+            };
+            auto stage_s = [&](const uint8_t *base, long long bytes, int rows, auto row_of, uint8_t *dst) {
+                const uintptr_t p0 = (uintptr_t)base;
+                const __amdgpu_buffer_rsrc_t r =
+                    buffer_rsrc((const void *)(p0 & ~(uintptr_t)3), ((long long)(p0 & 3) + bytes + 3) & ~3ll);
+                for (int t = tid; t < rows * J; t += 64 * NW) {
+                    const int row = t / J, j = t - row * J;
+                    const uint32_t o = (uint32_t)(p0 & 3) + row_of(row) * rsb + 16u * j;
+                    *(u32x4 *)(dst + row * SP + 16 * j) = seg_order<true>(load_seg<true>(r, o), o, U - 16 * j);
+                }
+            };
+            auto tile_row = [&](int row) { return (uint32_t)min(row0 + row, N - 1); };
+#pragma unroll
+            for (int i = 0; i < D; ++i) load_a(i, A[i]);
+            if (rt == rt0) {
+                // the vectors (MODE 2: those of the group's slots)
+                const int vecs = MODE == 2 ? (a.x_per_slot ? ns : 1) : nv;
+                for (int t = tid; t < vecs * 8 * NU; t += 64 * NW) {
+                    const int v = t / (8 * NU), b = t - v * 8 * NU;
+                    const uint32_t o = vec_row(MODE == 2 ? s0 + v : v) * (uint32_t)a.x_vec_bytes + 16u * b;
+                    *(u32x4 *)(lx + v * XP + 16 * b) =
+                        __builtin_amdgcn_raw_buffer_load_b128(rx, b < U ? o : kXPast, 0, 0);
+                }
+                stage_s((const uint8_t *)a.xs, (long long)x_rows * rsb, vecs,
+                        [&](int v) { return vec_row(MODE == 2 ? s0 + v : v); }, lxs);
+            }
+            if constexpr (MODE == 2) {
+                for (int k = 0; k < ns; ++k) {
+                    int ee = __builtin_amdgcn_readlane(ids_lane, s0 + k);
+                    if ((unsigned)ee >= (unsigned)a.E) ee = 0;                     // (times zero codes)
+                    stage_s(a.scales + ee * a.expert_sb, a.expert_sb, 16, tile_row, ls + k * 16 * SP);
+                }
+            } else {
+                stage_s(a.scales + e * a.expert_sb, a.expert_sb, 16, tile_row, ls);
+                if constexpr (H == 2) stage_s(a.scales2 + e * a.expert_sb, a.expert_sb, 16, tile_row, ls + 16 * SP);
+            }
+            __syncthreads();
+
+            f32x4 acc[H];
+#pragma unroll
+            for (int h = 0; h < H; ++h) acc[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            const int wst = swz_chunk(lr, lc), rd = c * 128 + 16 * (q ^ ((c >> 1) & 7));
+            const int vc = MODE == 2 ? 0 : (c < nv ? c : vmask);
+            const int mine = total > w ? (total - w + NW - 1) / NW : 0;            // this wave's units
+            for (int i0 = 0; i0 < mine; i0 += D) {
+#pragma unroll
+                for (int d = 0; d < D; ++d) {
+                    const int i = i0 + d;
+                    if (i < mine) {
+                        const int g = w + NW * i;
+                        const int slot = MODE == 2 ? g / NU : 0, u = g - slot * NU;
+                        const int v = MODE == 2 ? (a.x_per_slot ? slot : 0) : vc;
+                        // slab u / 2's bytes of this unit's two steps in bits 0-15
+                        const int sh = 16 * (u & 1), so = 16 * (u >> 1) + 4 * q;
+                        const uint32_t tb = *(const uint32_t *)(lxs + v * SP + so) >> sh;
+                        const u32x4 B0 = *(const u32x4 *)(lx + v * XP + 128 * u + 16 * q);
+                        const u32x4 B1 = *(const u32x4 *)(lx + v * XP + 128 * u + 64 + 16 * q);
+#pragma unroll
+                        for (int h = 0; h < H; ++h) {
+                            *(u32x4 *)(la + h * 2048 + wst) = A[d][h][0];
+                            *(u32x4 *)(la + h * 2048 + 1024 + (wst ^ 64)) = A[d][h][1];
+                        }
+                        asm volatile("" ::: "memory");                             // (written before read: one wave's LDS)
+                        load_a(i + D, A[d]);
+#pragma unroll
+                        for (int h = 0; h < H; ++h) {
+                            const uint32_t ta =
+                                *(const uint32_t *)(ls + ((MODE == 2 ? slot : h) * 16 + c) * SP + so) >> sh;
+                            const u32x4 F0 = *(const u32x4 *)(la + h * 2048 + rd);
+                            const u32x4 F1 = *(const u32x4 *)(la + h * 2048 + (rd ^ 64));
+                            acc[h] = mfma_mx4_op<0>(F0, B0, acc[h], ta, tb);
+                            acc[h] = mfma_mx4_op<1>(F1, B1, acc[h], ta, tb);
+                        }
+                        asm volatile("" ::: "memory");
+                        if constexpr (MODE == 2) {
+                            if ((g + NW) / NU != slot || i + 1 == mine) {          // this wave's last unit of the slot
+                                const float rw = __uint_as_float(
+                                    __builtin_amdgcn_readlane(__float_as_uint(rw_lane), s0 + slot));
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) tot[k] = __builtin_fmaf(rw, acc[0][k], tot[k]);
+                                acc[0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                            }
+                        }
+                    }
+                }
+            }
+            if constexpr (MODE == 2) {
+                if (s0 + per < slots) {
+                    __syncthreads();                           // (the next group's staging)
+                    continue;
+                }
+                acc[0] = tot;
+            }
+#pragma unroll
+            for (int h = 0; h < H; ++h) *(f32x4 *)(la + h * 2048 + 16 * lane) = acc[h];
+            __syncthreads();
+            // lane (c, q): rows 4 q .. 4 q + 3 of vector c, summed over the waves
+            if (w == 0 && c < nv) {
+                f32x4 r[H];
+#pragma unroll
+                for (int h = 0; h < H; ++h) {
+                    r[h] = acc[h];
+#pragma unroll
+                    for (int i = 1; i < NW; ++i) r[h] += *(const f32x4 *)(la + (i * H + h) * 2048 + 16 * lane);
+                }
+                float *const yr = a.y + (size_t)(MODE == 2 ? (int)blockIdx.y : pair_of(c)) * N;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int n = row0 + 4 * q + k;
+                    if (n < N) yr[n] = MODE == 1 ? swiglu(r[0][k], r[H - 1][k]) : r[0][k];
+                }
+            }
+            if (rt + 1 < rt1) __syncthreads();                 // (the next tile's pieces and scales)
+        }
+    }
+}
+
+extern const void *const kTableMx4Few[3];
+const void *const kTableMx4Few[3] = {
+    (const void *)&qmv_mx4_few_kernel<0>,
+    (const void *)&qmv_mx4_few_kernel<1>,
+    (const void *)&qmv_mx4_few_kernel<2>,
+};
 
 extern const void *const kTableMx4Tile[2];
 const void *const kTableMx4Tile[2] = {

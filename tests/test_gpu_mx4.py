@@ -281,3 +281,40 @@ def test_rows_behind_the_output_stay():
         q.qmv_gather_moe("mxfp4", dev(wc), dev(ws), dev(make_ids(rng, M, 2, 4)), dev(xc), dev(xs),
                          y=buf[:M * 2 * 33].view(M, 2, 33))
         assert (buf[M * 2 * 33:] == 7.0).all()
+
+
+@pytest.mark.parametrize("M,E,top_k,N,K", [(16, 64, 2, 20, 16384), (3, 500, 16, 33, 8192), (20, 300, 2, 100, 1088)])
+def test_long_rows_with_few_pairs(M, E, top_k, N, K):
+    """The widest vectors that a workgroup stages at once, gate/up and plain."""
+    rng = np.random.default_rng(M + K)
+    used = np.sort(rng.permutation(E)[:12]).astype(np.int32)
+    codes = torch.zeros((E, N, K // 2), dtype=torch.uint8, device="cuda")
+    scales = torch.full((E, N, K // 32), 255, dtype=torch.uint8, device="cuda")
+    wc, ws = make(rng, (12, N), K, 116, 120)
+    codes[torch.from_numpy(used).long()], scales[torch.from_numpy(used).long()] = dev(wc), dev(ws)
+    xc, xs = make(rng, (M,), K, 122, 124)
+    small = rng.integers(0, 12, (M, top_k)).astype(np.int32)
+    ids = dev(used[small])
+    x, w = R.values(xc, xs), R.values(wc, ws)
+    g, A = R.gather(small, w, x, False)
+    close(q.qmv_gather_moe("mxfp4", codes, scales, ids, dev(xc), dev(xs)), g, K * U * A, "long rows")
+    y = q.qmv_gather_moe_swiglu("mxfp4", codes, scales, codes, scales, ids, dev(xc), dev(xs))
+    silu = g / (1 + np.exp(-g))
+    tol = 1.1 * K * U * A * (np.abs(g) + K * U * A) + np.abs(silu) * K * U * A + (np.abs(g) + 8) * 2 * U * np.abs(silu * g)
+    close(y, silu * g, tol, "long rows, gate/up")
+
+
+@pytest.mark.parametrize("M,top_k,E", [(10, 4, 100), (16, 4, 40), (40, 2, 200), (3, 6, 50), (64, 1, 64), (200, 3, 1000)])
+def test_many_pairs_of_one_expert_among_few_pairs(M, top_k, E):
+    """More than 16 pairs of one expert where the call has fewer than two
+    pairs per expert (chunks of 16 of the expert's pairs)."""
+    rng = np.random.default_rng(M)
+    N, K = 40, 288
+    wc, ws = make(rng, (E, N), K)
+    xc, xs = make(rng, (M,), K)
+    for ids in (np.full((M, top_k), 7, np.int32), np.where(rng.random((M, top_k)) < 0.7, 7, -1).astype(np.int32),
+                rng.integers(0, 2, (M, top_k)).astype(np.int32)):
+        out = torch.full((M, top_k, N), float("nan"), device="cuda")
+        y = q.qmv_gather_moe("mxfp4", dev(wc), dev(ws), dev(ids), dev(xc), dev(xs), y=out)
+        want, A = R.gather(ids, R.values(wc, ws), R.values(xc, xs), False)
+        close(y, want, K * U * A, f"one expert {M} {top_k}")
