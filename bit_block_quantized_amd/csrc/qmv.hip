@@ -70,6 +70,7 @@ extern const void *const kTableBatchedKS[3];
 namespace qmv {
 extern const void *const kTableMx4Few[3];
 extern const void *const kTableMx4Tile[2];
+extern const void *const kTableMx4Wide[1];
 }
 
 namespace qmv {
@@ -583,6 +584,8 @@ qmv_status_t launch_dense4(const void *codes, const void *scales, const void *x,
 
 std::once_flag g_mx4_once[2];
 hipError_t g_mx4_err[2];
+std::once_flag g_mx4_wide_once;
+hipError_t g_mx4_wide_err;
 std::once_flag g_mx4_few_once[3];
 hipError_t g_mx4_few_err[3];
 
@@ -614,7 +617,32 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
     const int U = K / 32, J = (U + 15) / 16, h = mode == 1 ? 2 : 1;
     const int xp = (U + 7) / 8 * 128 + 16, sp = 16 * (J | 1), most = pairs < 16 ? pairs : 16;
     size_t lds_few = 64 + 4 * h * 2048 + (size_t)most * (xp + sp) + (size_t)h * 16 * sp;
-    if (mode != 2 && (pairs >= (gather ? 2 * E : 17) || lds_few > kLdsPerCU)) {
+    // 256 x 256 tiles once they fill half of the chip (us, against the tile
+    // kernel's 128 x 64: 56 tiles 60 and 38; 96 60 and 59, 33 and 32; 108 33 and
+    // 28; 112 63 and 74, 26 and 29; 192 36 and 50; 224 70 and 136; 896 275 and 493)
+    const long long wide_tiles = (long long)((N + 255) / 256) * ((M + 255) / 256);
+    if (!gather && mode == 0 && 2 * wide_tiles >= cu_count()) {
+        const int lds = 4 * 256 * 128 + 4 * 256 * 16;
+        a.bt_row_tiles = (N + 255) / 256;
+        a.bt_vmax = 4;
+        a.bt_tiles = (int)wide_tiles;
+        a.bt_per_xcd = (a.bt_tiles + 7) / 8;
+        std::call_once(g_mx4_wide_once, [&] {
+            g_mx4_wide_err = hipFuncSetAttribute(kTableMx4Wide[0], hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        });
+        if (g_mx4_wide_err != hipSuccess)
+            return QMV_EHIP;
+        void *kargs[] = {&a};
+        return hipLaunchKernel(kTableMx4Wide[0], dim3((unsigned)(8 * a.bt_per_xcd)), dim3(512), kargs, lds, stream) == hipSuccess
+                   ? QMV_OK
+                   : QMV_EHIP;
+    }
+    // dense: a workgroup per 16 rows and 16 vectors until there are three per CU
+    // (7168 -> 2048: 32 vectors 10 us against the tile kernel's 15, 64 9.4 and
+    // 18.5; 2880 -> 2880: 64 8.9 and 11.5, 128 14 and 11.5; 7168 -> 7168: 16 11.5
+    // and 17, 32 19 and 18, 64 35 and 20)
+    const bool many = gather ? pairs >= 2 * E : M > 16 && (long long)((M + 15) / 16) * ((N + 15) / 16) > 3 * cu_count();
+    if (mode != 2 && (many || lds_few > kLdsPerCU)) {
         const int rows = mode == 1 ? 64 : 128;
         a.bt_row_tiles = (N + rows - 1) / rows;
         // items at most: a chunk per 64 pairs and a rest per expert

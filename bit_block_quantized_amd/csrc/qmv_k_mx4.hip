@@ -762,6 +762,221 @@ __global__ __launch_bounds__(64 * kMx4Waves) void qmv_mx4_few_kernel(const Args 
     }
 }
 
+// ------------------------------------------------------------- wide dense
+// A dense matrix against thousands of vectors is bound by the matrix cores
+// and by LDS.  256 x 256 tiles, 4 x 2 waves of 64 rows x 128 vectors: a wave's
+// step reads 12 fragments from LDS for 32 products.  Both operands are staged
+// for a unit (256 weights, 2 steps) at a time, double-buffered, half of a
+// unit's loads in flight during each step.  The vectors' fragments are read in
+// two groups of 4, each group while the other is multiplied, and a row's
+// fragment as soon as its last product of the step is given out, so a step
+// enters with its operands read.  One barrier a unit, in the middle of its
+// second step, where every fragment of the unit is read.
+// 8192 vectors, 7168 -> 7168: 275 us, 3.06 PFLOP/s (128 x 128 tiles of 4 waves
+// 398, the tile kernel's 128 x 64 493).  Half a round of its 3.5 rounds of
+// workgroups is lost at the end; all-zero operands take 227 us, which the
+// chip's power limit explains (2.1 GHz against 2.4).  With zero operands the
+// products alone take 145 us, LDS reads add 20, the staging stores 30, the
+// loads 30; loads two steps ahead, or written between other products, change
+// nothing.
+__global__ __launch_bounds__(512, 2) void qmv_mx4_wide_kernel(const Args a)
+{
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    constexpr int RF = 4, CF = 8, NWR = 4, NWC = 2, NW = NWR * NWC;
+    constexpr int BR = 16 * RF * NWR, BC = 16 * CF * NWC;   // tile: rows, vectors
+    constexpr int AB = BR * 128, XB = BC * 128;       // bytes of a unit's codes
+    constexpr int NS = BR + BC;                       // staged scale rows, one a thread
+    constexpr int KA = BR / 8 / NW, KX = BC / 8 / NW; // staged pieces (8 rows x 128 bytes) per wave and unit
+    constexpr int GB = CF / 2;                        // column fragments read at a time
+    static_assert(NS == 64 * NW && BR % 64 == 0 && KA % 2 == 0 && KX % 2 == 0 && NW % 2 == 0, "staging split");
+    uint8_t *const ld = lds;                          // [2][AB + XB]
+    uint8_t *const ls = lds + 2 * (AB + XB);          // [2][NS] x 16 bytes
+    // groups of bt_vmax vector chunks, chunk-fastest inside, dealt to the XCDs
+    // in contiguous parts: the tiles an XCD runs at a time share both operands
+    const int tile = (blockIdx.x & 7) * a.bt_per_xcd + (blockIdx.x >> 3);
+    if (tile >= a.bt_tiles) return;
+    const int chunks = (a.M + BC - 1) / BC, group = a.bt_vmax * a.bt_row_tiles;
+    const int gi = tile / group, in = tile - gi * group, gw = min(a.bt_vmax, chunks - gi * a.bt_vmax);
+    const int row0 = in / gw * BR, vec0 = (gi * a.bt_vmax + in % gw) * BC;
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wr = w / NWC, wc = w % NWC;
+    const int c = lane & 15, q = lane >> 4, lr = lane >> 3, lc = lane & 7;
+    const int U = a.units, J = (U + 15) >> 4;
+
+    f32x4 acc[RF][CF];
+#pragma unroll
+    for (int f = 0; f < RF; ++f)
+#pragma unroll
+        for (int g = 0; g < CF; ++g) acc[f][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    // wave w stages pieces w, w + NW, ... of each operand; rows past N and
+    // vectors past M lie past the buffers' ends and read zeros
+    const __amdgpu_buffer_rsrc_t rc = buffer_rsrc(a.codes, a.expert_cb);
+    const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(a.x, (long long)a.M * a.x_vec_bytes);
+    const uint32_t oa = (uint32_t)(row0 + 8 * w + lr) * (uint32_t)a.rcb + 16u * lc;
+    const uint32_t ox = (uint32_t)(vec0 + 8 * w + lr) * (uint32_t)a.x_vec_bytes + 16u * lc;
+    const uint32_t pa = 8u * NW * (uint32_t)a.rcb, px = 8u * NW * (uint32_t)a.x_vec_bytes;
+    u32x4 ga[KA / 2], gx[KX / 2];                     // half a unit's pieces
+    auto load_half = [&](int u, int half) {
+        // (a row's blocks past its end: zeros; the pieces' offsets are built
+        // anew each time: registers are scarcer than additions)
+        const bool ok = 8 * u + lc < U;
+        uint32_t ta = oa, tx = ox;
+        asm volatile("" : "+v"(ta), "+v"(tx));
+#pragma unroll
+        for (int k = 0; k < KA / 2; ++k)
+            ga[k] = __builtin_amdgcn_raw_buffer_load_b128(rc, ok ? ta + ((half * (KA / 2) + k) * pa + 128u * u) : kXPast, 0, 0);
+#pragma unroll
+        for (int k = 0; k < KX / 2; ++k)
+            gx[k] = __builtin_amdgcn_raw_buffer_load_b128(rx, ok ? tx + ((half * (KX / 2) + k) * px + 128u * u) : kXPast, 0, 0);
+    };
+    // piece p stands in fragment p / 2, rows 8 (p % 2) ..; p has the wave's parity
+    const int wst = (w >> 1) * 2048 + (w & 1) * 1024 + (swz_chunk(lr, lc) ^ ((w & 1) << 6));
+    auto store_half = [&](int buf, int half) {
+        uint8_t *const d = ld + buf * (AB + XB) + wst;
+#pragma unroll
+        for (int k = 0; k < KA / 2; ++k) *(u32x4 *)(d + (half * (KA / 2) + k) * (NW * 1024)) = ga[k];
+#pragma unroll
+        for (int k = 0; k < KX / 2; ++k) *(u32x4 *)(d + AB + (half * (KX / 2) + k) * (NW * 1024)) = gx[k];
+    };
+
+    // scale bytes: thread t takes 16 bytes (a slab, two units) of row t of the
+    // tile or of vector t - BR, the same tensor for a whole wave
+    const bool vecs = w >= BR / 64;
+    const uintptr_t p0 = (uintptr_t)(vecs ? (const uint8_t *)a.xs : a.scales);
+    const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(
+        (const void *)(p0 & ~(uintptr_t)3), ((long long)(p0 & 3) + (long long)(vecs ? a.M : a.N) * a.rsb + 3) & ~3ll);
+    const uint32_t os = (uint32_t)(p0 & 3) +
+                        (uint32_t)(vecs ? min(vec0 + tid - BR, a.M - 1) : min(row0 + tid, a.N - 1)) * (uint32_t)a.rsb;
+    auto put_s = [&](int j, u32x4 v) { *(u32x4 *)(ls + (j & 1) * (NS * 16) + tid * 16) = v; };
+    const int rd = c * 128 + 16 * (q ^ ((c >> 1) & 7));
+
+    u32x4 F[RF], B[2][GB];                            // fragments: rows; two groups of vectors
+    uint32_t ta[RF], tb[2][GB];                       // their scale bytes, a slab's dword each
+    const uint8_t *const fa = ld + wr * RF * 2048, *const fb = ld + AB + wc * CF * 2048;
+    // step s of the unit in buffer h
+    auto read_f = [&](int h, int s, int f) {
+        uint32_t o = rd ^ (64 * s);
+        asm volatile("" : "+v"(o));
+        F[f] = *(const u32x4 *)(fa + h * (AB + XB) + f * 2048 + o);
+    };
+    auto read_b = [&](int h, int s, int grp) {
+        uint32_t o = rd ^ (64 * s);
+        asm volatile("" : "+v"(o));
+#pragma unroll
+        for (int g = 0; g < GB; ++g) B[grp][g] = *(const u32x4 *)(fb + h * (AB + XB) + (grp * GB + g) * 2048 + o);
+    };
+    const uint8_t *const fs = ls + c * 16 + 4 * q;
+    auto read_ta = [&](int j, int f) { ta[f] = *(const uint32_t *)(fs + (j & 1) * (NS * 16) + 256 * (wr * RF + f)); };
+    auto read_tb = [&](int j, int grp) {
+#pragma unroll
+        for (int g = 0; g < GB; ++g)
+            tb[grp][g] = *(const uint32_t *)(fs + (j & 1) * (NS * 16) + BR * 16 + 256 * (wc * CF + grp * GB + g));
+    };
+
+    {
+        const ScaleSeg sg = load_seg<true>(rs, os);
+        load_half(0, 0);
+        store_half(0, 0);
+        load_half(0, 1);
+        store_half(0, 1);
+        load_half(1, 0);
+        put_s(0, seg_order<true>(sg, os, U));
+    }
+    __syncthreads();
+    read_b(0, 0, 0);
+    read_tb(0, 0);
+#pragma unroll
+    for (int f = 0; f < RF; ++f) {
+        read_f(0, 0, f);
+        read_ta(0, f);
+    }
+    // a slab: LAST 0: two more follow; 1: one more; 2: none
+    auto slab = [&](int j, auto LAST) {
+        constexpr int last = decltype(LAST)::value;
+        ScaleSeg sg;
+        read_tb(j, 1);
+        auto step = [&](auto HALF, auto SIDX) {
+            constexpr int h = decltype(HALF)::value;  // the unit's buffer too
+            constexpr int s = decltype(SIDX)::value;
+            constexpr bool more = last < 2 || h == 0; // another unit follows
+            if constexpr (h == 1 && s == 0 && last < 2) sg = load_seg<last == 1>(rs, os + 16u * (j + 1));
+            read_b(h, s, 1);
+            __builtin_amdgcn_s_setprio(1);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int g = 0; g < GB; ++g)
+#pragma unroll
+                for (int f = 0; f < RF; ++f)
+                    acc[f][g] = mfma_mx4_op<2 * h + s>(F[f], B[0][g], acc[f][g], ta[f], tb[0][g]);
+            // (keeps the products here)
+#pragma unroll
+            for (int g = 0; g < GB; ++g)
+#pragma unroll
+                for (int f = 0; f < RF; ++f) asm volatile("" : "+v"(acc[f][g]));
+            __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_s_setprio(0);
+            if constexpr (more) store_half(h ^ 1, s);
+            if constexpr (h == 1 && s == 1 && last < 2) put_s(j + 1, seg_order<last == 1>(sg, os, U - 16 * (j + 1)));
+            // every fragment of this unit is read, and the next unit is staged
+            if constexpr (s == 1 && more) __syncthreads();
+            if constexpr (s == 0 && more) load_half(2 * j + h + 1, 1);
+            if constexpr (s == 1 && last < 2) load_half(2 * j + h + 2, 0);
+            if constexpr (s == 0 || more) read_b(s ? h ^ 1 : h, s ^ 1, 0);
+            if constexpr (h == 1 && s == 1 && last < 2) read_tb(j + 1, 0);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int f = 0; f < RF; ++f) {
+#pragma unroll
+                for (int g = 0; g < GB; ++g)
+                    acc[f][GB + g] = mfma_mx4_op<2 * h + s>(F[f], B[1][g], acc[f][GB + g], ta[f], tb[1][g]);
+#pragma unroll
+                for (int g = 0; g < GB; ++g) asm volatile("" : "+v"(acc[f][GB + g]));
+                if constexpr (s == 0 || more) read_f(s ? h ^ 1 : h, s ^ 1, f);
+                if constexpr (h == 1 && s == 1 && last < 2) read_ta(j + 1, f);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        step(std::integral_constant<int, 0>{}, std::integral_constant<int, 0>{});
+        step(std::integral_constant<int, 0>{}, std::integral_constant<int, 1>{});
+        step(std::integral_constant<int, 1>{}, std::integral_constant<int, 0>{});
+        step(std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
+    };
+    int j = 0;
+    for (; j + 2 < J; ++j) slab(j, std::integral_constant<int, 0>{});
+    if (j + 1 < J) slab(j++, std::integral_constant<int, 1>{});
+    slab(j, std::integral_constant<int, 2>{});
+
+    const bool vec4 = (a.N & 3) == 0 && ((uintptr_t)a.y & 15) == 0;
+#pragma unroll
+    for (int g = 0; g < CF; ++g) {
+        const int v = vec0 + 16 * (wc * CF + g) + c;
+        if (v < a.M) {
+            float *const yr = a.y + (size_t)v * a.N;
+#pragma unroll
+            for (int f = 0; f < RF; ++f) {
+                const int n0 = row0 + 16 * (wr * RF + f) + 4 * q;
+                if (n0 < a.N) {
+                    if (vec4) {
+                        *(float4 *)(yr + n0) = make_float4(acc[f][g][0], acc[f][g][1], acc[f][g][2], acc[f][g][3]);
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            if (n0 + k < a.N) yr[n0 + k] = acc[f][g][k];
+                    }
+                }
+            }
+        }
+    }
+}
+
+extern const void *const kTableMx4Wide[1];
+const void *const kTableMx4Wide[1] = {
+    (const void *)&qmv_mx4_wide_kernel,
+};
+
 extern const void *const kTableMx4Few[3];
 const void *const kTableMx4Few[3] = {
     (const void *)&qmv_mx4_few_kernel<0>,

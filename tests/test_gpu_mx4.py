@@ -50,6 +50,13 @@ DENSE = [(1, 1, 32), (1, 17, 64), (1, 2880, 2880), (2, 33, 96), (4, 64, 544), (5
          (1, 40, 16384), (20, 24, 16384), (513, 513, 1024), (1025, 300, 256)]
 
 
+# thousands of vectors: tiles of 256 x 256, odd edges and every tail of K; and
+# tiles of 128 x 64 with few vectors and many rows
+DENSE += [(600, 130, 2880), (520, 70, 32), (777, 260, 544), (512, 256, 1536), (1100, 515, 1056), (2049, 300, 128),
+          (4100, 33, 96), (2050, 3600, 32), (1900, 4097, 160), (4100, 2050, 544), (2049, 3850, 1056), (8192, 900, 96),
+          (1025, 7001, 512), (17, 12400, 64), (70, 2900, 96), (200, 1100, 544), (96, 2700, 2880), (33, 5000, 1056)]
+
+
 @pytest.mark.parametrize("M,N,K", DENSE)
 def test_dense(M, N, K):
     rng = np.random.default_rng(M * 7 + N * 3 + K)
