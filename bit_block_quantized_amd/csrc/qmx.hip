@@ -86,13 +86,35 @@ __device__ __forceinline__ void store8(void *base, size_t i, int type, const flo
     }
 }
 
-// One value of any type (rows whose length is no multiple of 8).
-__device__ __forceinline__ float load1(const void *base, size_t i, int type)
+// Values first, first + step, ... of a row of K values of any type, the last
+// one again past the end (P loads with no branch between them, all in flight
+// at once); a value's bits to its value.
+template <int P>
+__device__ __forceinline__ void load_bits(const void *base, size_t row, int first, int step, int K, int type,
+                                          uint32_t (&v)[P])
 {
-    if (type == QMX_T_F32) return ((const float *)base)[i];
-    const uint16_t h = ((const uint16_t *)base)[i];
-    if (type == QMX_T_BF16) return __uint_as_float((uint32_t)h << 16);
-    return (float)__builtin_bit_cast(_Float16, h);
+    if (type == QMX_T_F32) {
+        const uint32_t *const p = (const uint32_t *)base + row;
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = p[min(first + i * step, K - 1)];
+    } else {
+        const uint16_t *const p = (const uint16_t *)base + row;
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = p[min(first + i * step, K - 1)];
+    }
+}
+
+template <int P>
+__device__ __forceinline__ void bits_to_f32(const uint32_t (&b)[P], int type, float (&v)[P])
+{
+    if (type == QMX_T_F16) {
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = (float)__builtin_bit_cast(_Float16, (uint16_t)b[i]);
+    } else {
+        const int up = type == QMX_T_BF16 ? 16 : 0;
+#pragma unroll
+        for (int i = 0; i < P; ++i) v[i] = __uint_as_float(b[i] << up);
+    }
 }
 
 __device__ __forceinline__ void store1(void *base, size_t i, int type, float v)
@@ -208,7 +230,8 @@ __device__ __forceinline__ void put8(void *y, void *ys, size_t i, const float (&
 // sum(h^2) and the products are formed in fp64: the quantizers round to a
 // border-exact code, and an fp32 norm is off by 1e-7, which moves one code
 // in 1e5 across a border.  The kernel waits for memory, not for the fp64
-// rate.
+// rate: 2048 rows of 7168, bf16 with an fp32 residual, to int8: 32 us for 162 MB,
+// 5.1 TB/s, which is what a copy reaches.
 struct NormArgs {
     const void *x, *res, *w;
     void *res_out, *y, *ys;
@@ -290,7 +313,8 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void qmx_rmsnorm_kernel(const No
 
 // Rows whose length is no multiple of 8 (bf16 output): the same, with thread
 // t of the group taking values t, t + T, ... one at a time, so that a wave's
-// accesses are still consecutive.
+// accesses are still consecutive.  All loads are given out before the first
+// is used (777 rows of 2879: 7.2 us, 8.9 with a wait a value).
 template <int T, int P>
 __global__ __launch_bounds__(T == 64 ? 256 : T) void qmx_rmsnorm_odd_kernel(const NormArgs a)
 {
@@ -300,48 +324,55 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void qmx_rmsnorm_odd_kernel(cons
     const long long row = a.row0 + (long long)blockIdx.x * R + (T == 64 ? threadIdx.x >> 6 : 0);
     if (row >= a.M) return;
     const size_t base = (size_t)row * a.K;
-    float h[P], rv[P], wv[P];
+    uint32_t xb[P], rb[P], wb[P];
+    load_bits<P>(a.x, base, tid, T, a.K, a.xt, xb);
+    if (a.res) load_bits<P>(a.res, base, tid, T, a.K, a.rt, rb);
+    if (a.w) load_bits<P>(a.w, 0, tid, T, a.K, a.wt, wb);
+    float h[P], w[P];
+    bits_to_f32<P>(xb, a.xt, h);
+    if (a.res) {
+        float rv[P];
+        bits_to_f32<P>(rb, a.rt, rv);
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-        const int k = p * T + tid;
-        h[p] = 0.0f;
-        if (k < a.K) {
-            h[p] = load1(a.x, base + k, a.xt);
-            if (a.res) rv[p] = load1(a.res, base + k, a.rt);
-            if (a.w) wv[p] = load1(a.w, k, a.wt);
+        for (int p = 0; p < P; ++p) {
+            h[p] += rv[p];
+            if (p * T + tid < a.K) store1(a.res_out, base + p * T + tid, a.rt, h[p]);
         }
     }
     double s = 0.0;
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-        const int k = p * T + tid;
-        if (k < a.K) {
-            if (a.res) {
-                h[p] += rv[p];
-                store1(a.res_out, base + k, a.rt, h[p]);
-            }
-            s = __builtin_fma((double)h[p], (double)h[p], s);
-        }
-    }
+    for (int p = 0; p < P; ++p)
+        if (p * T + tid < a.K) s = __builtin_fma((double)h[p], (double)h[p], s);
     s = row_sum<T>(s, part);
     const double r = 1.0 / __builtin_sqrt(s / (double)a.K + (double)a.eps);
+    if (a.w) {
+        bits_to_f32<P>(wb, a.wt, w);
+    } else {
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-        const int k = p * T + tid;
-        if (k < a.K)
-            store1(a.y, base + k, QMX_T_BF16, (float)((double)h[p] * r * (a.w ? (double)wv[p] : 1.0)));
+        for (int p = 0; p < P; ++p) w[p] = 1.0f;
     }
+#pragma unroll
+    for (int p = 0; p < P; ++p)
+        if (p * T + tid < a.K)
+            store1(a.y, base + p * T + tid, QMX_T_BF16, (float)((double)h[p] * r * (double)w[p]));
 }
 
+// Threads a row: a step of 8 values each keeps the most bytes in flight
+// (2048 rows of 7168, us: 256 threads 34.8, 512 32.7, 1024 32.1; one row of
+// 7168 5.4, 4.5, 4.2), except where a row of up to 4096 leaves many of 512
+// threads idle and there are rows enough to fill the chip (rows of 2880: 2048
+// of them 13.6 us with 256 threads, 14.9 with 512; one 3.9 and 3.2).
 template <int FMT>
-const void *norm_kernel(int K, int &threads, int &rows)
+const void *norm_kernel(int M, int K, int &threads, int &rows)
 {
     rows = 1;
-    if (K <= 512) { threads = 256; rows = 4; return (const void *)&qmx_rmsnorm_kernel<FMT, 64, 1>; }
-    if (K <= 2048) { threads = 256; return (const void *)&qmx_rmsnorm_kernel<FMT, 256, 1>; }
-    if (K <= 4096) { threads = 256; return (const void *)&qmx_rmsnorm_kernel<FMT, 256, 2>; }
-    if (K <= 8192) { threads = 256; return (const void *)&qmx_rmsnorm_kernel<FMT, 256, 4>; }
+    threads = 256;
+    if (K <= 512) { rows = 4; return (const void *)&qmx_rmsnorm_kernel<FMT, 64, 1>; }
+    if (K <= 2048) return (const void *)&qmx_rmsnorm_kernel<FMT, 256, 1>;
+    if (K <= 4096 && M >= 1024) return (const void *)&qmx_rmsnorm_kernel<FMT, 256, 2>;
+    if (K <= 4096) { threads = 512; return (const void *)&qmx_rmsnorm_kernel<FMT, 512, 1>; }
     threads = 1024;
+    if (K <= 8192) return (const void *)&qmx_rmsnorm_kernel<FMT, 1024, 1>;
     return (const void *)&qmx_rmsnorm_kernel<FMT, 1024, 2>;
 }
 
@@ -440,8 +471,13 @@ __global__ __launch_bounds__(256) void qmx_dequantize_kernel(const void *c, cons
 }
 
 // ------------------------------------------------------------------- router
-// One wave per token, L logits a lane (expert lane + 64 i).  Logits order
-// like these keys; NaN and -infinity get key 0 (masked).
+// One wave per token, L logits a lane (expert lane + 64 i), held in registers;
+// top_k times the largest is taken out.  Logits order like these keys; NaN and
+// -infinity get key 0 (masked).  The instructions of the selection bound it
+// (at 8192 x 256, top 8: 7.6 us, of which 0.43 a selection; the logits alone take about 2): the
+// maximum runs over the lanes with row shifts and broadcasts of the vector
+// ALUs (12.4 us with shuffles through LDS), and the lowest expert that has it
+// comes from ballots in scalar registers, with no second reduction.
 __device__ __forceinline__ uint32_t logit_key(float l)
 {
     const uint32_t b = __float_as_uint(l + 0.0f);             // -0 and 0 are equal
@@ -454,14 +490,22 @@ __device__ __forceinline__ float key_logit(uint32_t k)
     return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
 }
 
+template <int CTRL> __device__ __forceinline__ uint32_t lanes_max(uint32_t v)
+{
+    const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xF, 0xF, false);
+    return v > o ? v : o;                                     // (lanes with no source: 0)
+}
+
+// The wave's largest value, the same in every lane.
 __device__ __forceinline__ uint32_t wave_max(uint32_t v)
 {
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) {
-        const uint32_t o = (uint32_t)__shfl_xor((int)v, d);
-        v = v > o ? v : o;
-    }
-    return v;
+    v = lanes_max<0x111>(v);                                  // from the lane 1, 2, 4, 8 below in the row of 16
+    v = lanes_max<0x112>(v);
+    v = lanes_max<0x114>(v);
+    v = lanes_max<0x118>(v);
+    v = lanes_max<0x142>(v);                                  // a row's last lane to the row after it
+    v = lanes_max<0x143>(v);                                  // lane 31 to the upper half
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
 }
 
 __device__ __forceinline__ float wave_sum(float v)
@@ -487,50 +531,46 @@ __global__ __launch_bounds__(256) void qmx_router_kernel(const RouterArgs a)
     if (t >= a.M) return;
     const size_t base = (size_t)t * a.E;
     uint32_t key[L];
+    float l[L];
+    load_bits<L>(a.logits, base, lane, 64, a.E, a.lt, key);
+    bits_to_f32<L>(key, a.lt, l);
 #pragma unroll
-    for (int i = 0; i < L; ++i) {
-        const int e = lane + 64 * i;
-        key[i] = e < a.E ? logit_key(load1(a.logits, base + e, a.lt)) : 0u;
-    }
+    for (int i = 0; i < L; ++i) key[i] = lane + 64 * i < a.E ? logit_key(l[i]) : 0u;
     // the j-th largest: the wave's largest key, then the lowest expert that
-    // has it; lane j keeps it, its owner clears it
-    float mine = 0.0f;
+    // has it; lane j keeps it, its owner clears it.  (Once only masked experts
+    // are left the key is 0, and clearing a 0 changes nothing.)
+    uint32_t my_key = 0, first = 0;
     int my_id = -1;
-    float top = 0.0f, all = 0.0f;
-    int chosen = 0;
     for (int j = 0; j < a.top_k; ++j) {
         uint32_t m = 0;
 #pragma unroll
         for (int i = 0; i < L; ++i) m = m > key[i] ? m : key[i];
         m = wave_max(m);
-        if (m == 0u) break;                                   // every expert left is masked
-        if (j == 0) {
-            top = key_logit(m);
-            if (a.scoring == QMX_SOFTMAX && !a.normalize) {
+        first = j == 0 ? m : first;
+        int lowest = 0;
 #pragma unroll
-                for (int i = 0; i < L; ++i)
-                    if (key[i]) all += expf(key_logit(key[i]) - top);
-                all = wave_sum(all);
-            }
+        for (int i = L - 1; i >= 0; --i) {
+            const unsigned long long have = __ballot(key[i] == m);
+            lowest = have ? 64 * i + __builtin_ctzll(have) : lowest;
         }
-        int id = 0x7FFFFFFF;
+        my_key = lane == j ? m : my_key;
+        my_id = lane == j ? lowest : my_id;
 #pragma unroll
-        for (int i = L - 1; i >= 0; --i) id = key[i] == m ? lane + 64 * i : id;
-        const uint32_t lowest = 0x7FFFFFFFu - wave_max(0x7FFFFFFFu - (uint32_t)id);
-        if (lane == j) {
-            mine = key_logit(m);
-            my_id = (int)lowest;
-        }
-#pragma unroll
-        for (int i = 0; i < L; ++i) key[i] = (uint32_t)(lane + 64 * i) == lowest ? 0u : key[i];
-        chosen = j + 1;
+        for (int i = 0; i < L; ++i) key[i] = lane + 64 * i == lowest ? 0u : key[i];
     }
-    if (lane >= a.top_k) mine = 0.0f;
-    const bool have = lane < chosen;
+    const bool have = my_key != 0u;
+    if (!have) my_id = -1;
+    const float mine = have ? key_logit(my_key) : 0.0f, top = first ? key_logit(first) : 0.0f;
     float w = 0.0f;
     if (a.scoring == QMX_SOFTMAX) {
         const float e = have ? expf(mine - top) : 0.0f;
-        const float sum = a.normalize ? wave_sum(e) : all;
+        float part = e;                                       // the chosen, and without normalize the rest
+        if (!a.normalize) {
+#pragma unroll
+            for (int i = 0; i < L; ++i)
+                if (key[i]) part += expf(key_logit(key[i]) - top);
+        }
+        const float sum = wave_sum(part);
         w = have ? e / sum : 0.0f;
     } else if (a.normalize) {
         // both sides of the quotient times e^-top where top < 0, so that
@@ -606,9 +646,9 @@ QMX_API qmv_status_t qmx_rmsnorm(qmx_type_t xtype, const void *x, qmx_type_t rty
     NormArgs a = {x, residual, weight, residual_out, y, y_scales, eps, (int)xtype, (int)rtype, (int)wtype, M, K, 0};
     int threads, rows;
     const void *fn = K % 8 != 0          ? norm_odd_kernel(K, threads, rows)
-                     : fmt == QMX_BF16   ? norm_kernel<QMX_BF16>(K, threads, rows)
-                     : fmt == QMX_Q8B32  ? norm_kernel<QMX_Q8B32>(K, threads, rows)
-                                         : norm_kernel<QMX_MXFP4>(K, threads, rows);
+                     : fmt == QMX_BF16   ? norm_kernel<QMX_BF16>(M, K, threads, rows)
+                     : fmt == QMX_Q8B32  ? norm_kernel<QMX_Q8B32>(M, K, threads, rows)
+                                         : norm_kernel<QMX_MXFP4>(M, K, threads, rows);
     return go_rows(fn, a, rows, threads, stream);
 }
 
