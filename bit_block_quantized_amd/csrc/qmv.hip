@@ -69,7 +69,7 @@ extern const void *const kTableBatchedKS[3];
 // gate/up, combine].
 namespace qmv {
 extern const void *const kTableMx4Few[3];
-extern const void *const kTableMx4Tile[2];
+extern const void *const kTableMx4Tile[4];
 extern const void *const kTableMx4Wide[1];
 }
 
@@ -582,21 +582,21 @@ qmv_status_t launch_dense4(const void *codes, const void *scales, const void *x,
     return QMV_OK;
 }
 
-std::once_flag g_mx4_once[2];
-hipError_t g_mx4_err[2];
+std::once_flag g_mx4_once[4];
+hipError_t g_mx4_err[4];
 std::once_flag g_mx4_wide_once;
 hipError_t g_mx4_wide_err;
 std::once_flag g_mx4_few_once[3];
 hipError_t g_mx4_few_err[3];
 
-// LDS of a tile workgroup: the chunk's list, two buffers of vector codes (64
-// vectors x 128 bytes), the waves' weight pieces (rows x 128 bytes), and the
+// LDS of a tile workgroup: the chunk's list, two buffers of vector codes (chunk
+// x 128 bytes), the waves' weight pieces (rows x 128 bytes), and the
 // scale bytes of the rows and the vectors (an odd number of 16-byte slabs
 // from row to row); with room for the counts per expert.
-int mx4_tile_lds(int K)
+int mx4_tile_lds(int K, int chunk)
 {
     const int J = (K + 511) / 512;
-    return 128 + 2 * 64 * 128 + 128 * 128 + (128 + 64) * 16 * (J | 1);
+    return 2 * chunk + 2 * chunk * 128 + 128 * 128 + (128 + chunk) * 16 * (J | 1);
 }
 
 // MXFP4 x MXFP4.  route_w non-null: the combine of up to 4 tokens.
@@ -645,21 +645,28 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
     if (mode != 2 && (many || lds_few > kLdsPerCU)) {
         const int rows = mode == 1 ? 64 : 128;
         a.bt_row_tiles = (N + rows - 1) / rows;
-        // items at most: a chunk per 64 pairs and a rest per expert
-        const long long items = gather ? (pairs < E ? pairs : E) + pairs / 64 : (M + 63) / 64;
+        // chunks of 128 vectors where many experts have more than 64, as long as
+        // the chip holds two workgroups a CU (2880 -> 2880 of 32 experts, us with
+        // 128 and with 64: gate/up 32 pairs an expert 82 and 81, 48 86 and 86, 64
+        // 93 and 117, 96 105 and 148, 256 243 and 323; gather 64 57 and 63; a dense
+        // matrix differs by less than 3%)
+        const bool big = gather && pairs >= 48LL * E && 2 * mx4_tile_lds(K, 128) <= kLdsPerCU;
+        const int chunk = big ? 128 : 64;
+        // items at most: a whole chunk each and a rest per expert
+        const long long items = gather ? (pairs < E ? pairs : E) + pairs / chunk : (M + chunk - 1) / chunk;
         // runs of row tiles: about 8 workgroups for each that the chip holds at
         // a time (fewer, longer runs scan the ids less often but end unevenly:
         // 1024 tokens x top-8 of 256, 7168 -> 2048: 570 us at 1, 417 at 4, 376
         // at 8; 512 x top-4 of 32, gate/up 2880 -> 2880: 110, 112, 112 us)
-        const int lds = mx4_tile_lds(K);
+        const int lds = mx4_tile_lds(K, chunk);
         const long long slots = (long long)cu_count() * (lds * 2 <= kLdsPerCU ? 2 : 1);
         const long long run = items * a.bt_row_tiles / (8 * slots);
         a.bt_chunk = run < 1 ? 1 : run > a.bt_row_tiles ? a.bt_row_tiles : (int)run;
         const long long groups = items * ((a.bt_row_tiles + a.bt_chunk - 1) / a.bt_chunk);
-        const int fn = mode;
+        const int fn = 2 * big + mode;
         std::call_once(g_mx4_once[fn], [&] {
             g_mx4_err[fn] = hipFuncSetAttribute(kTableMx4Tile[fn], hipFuncAttributeMaxDynamicSharedMemorySize,
-                                                mx4_tile_lds(kMaxK));
+                                                big ? kLdsPerCU / 2 : mx4_tile_lds(kMaxK, 64));
         });
         if (g_mx4_err[fn] != hipSuccess)
             return QMV_EHIP;

@@ -101,7 +101,6 @@ __device__ __forceinline__ u32x4 seg_order(const ScaleSeg &s, uint32_t o, int n)
 // Every workgroup counts the pairs per expert itself (LDS atomics on whole
 // numbers: the same counts everywhere), so the grid needs no device-wide
 // knowledge: item i is the i-th (expert, chunk) of the experts in order.
-constexpr int kMx4Chunk = 64;        // tile kernel
 constexpr int kMx4Few = 16;          // few kernel
 constexpr int kMx4Waves = 4;
 constexpr int kMx4RF = 2;            // 16-row fragments per wave of a tile
@@ -223,7 +222,8 @@ __host__ __device__ constexpr int mx4_scale_pitch(int J) { return 16 * (J | 1); 
 
 // Row tiles rt0 .. rt1 - 1 of expert e against nv vectors: pairs vecs[0..nv)
 // of a routed call, vectors vstart .. of a dense one (vecs null).
-template <int MODE, int CF>
+// XR: vectors that the LDS layout has room for.
+template <int MODE, int CF, int XR>
 __device__ __forceinline__ void mx4_tile_run(const Args &a, uint8_t *lds, int e, int rt0, int rt1,
                                              const uint16_t *vecs, int vstart, int nv)
 {
@@ -233,13 +233,14 @@ __device__ __forceinline__ void mx4_tile_run(const Args &a, uint8_t *lds, int e,
     constexpr int TR = 16 * RH * NW;                 // output rows of a tile
     constexpr int XU = (2 * CF + NW - 1) / NW;       // staged pieces (8 vectors x 128 bytes) per wave and unit
     constexpr int XB = CF * 2048;                    // bytes of one vector buffer
+    constexpr int GB = CF < 4 ? CF : 4, HG = CF / GB; // vector fragments read at a time; groups of them
     int tid = threadIdx.x;
     asm volatile("" : "+v"(tid));                    // (keeps the offsets below out of the caller's loop head)
     const int lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     uint8_t *const lx = lds;                                      // [2][CF][16 vectors x 128 bytes]
-    uint8_t *const la = lds + 4 * 4096 + w * (RF * 2048);         // [RF][16 rows x 128 bytes], this wave's
-    uint8_t *const ls = lds + 4 * 4096 + NW * RF * 2048;          // [BR + 16 CF] rows of SP bytes
+    uint8_t *const la = lds + 2 * XR * 128 + w * (RF * 2048);        // [RF][16 rows x 128 bytes], this wave's
+    uint8_t *const ls = lds + 2 * XR * 128 + NW * RF * 2048;        // [BR + 16 CF] rows of SP bytes
     const int c = lane & 15, q = lane >> 4;
     const int lr = lane >> 3, lc = lane & 7;         // row and chunk of a load
     const bool gather = vecs != nullptr;
@@ -386,10 +387,12 @@ __device__ __forceinline__ void mx4_tile_run(const Args &a, uint8_t *lds, int e,
                 constexpr int h = decltype(HALF)::value;            // the unit's vector buffer too
                 constexpr bool more = !last || h == 0;              // another unit follows
                 const int u = 2 * j + h;
-                u32x4 F[2][RF], B[2][CF];
-                auto read_b = [&](int s, u32x4 (&b)[CF]) {
+                u32x4 F[2][RF], B[2][GB];
+                // group i of the unit: step i / HG's vectors i % HG * GB ..
+                auto read_b = [&](int i, u32x4 (&b)[GB]) {
 #pragma unroll
-                    for (int g = 0; g < CF; ++g) b[g] = *(const u32x4 *)(lx + h * XB + g * 2048 + (rd ^ (64 * s)));
+                    for (int g = 0; g < GB; ++g)
+                        b[g] = *(const u32x4 *)(lx + h * XB + (i % HG * GB + g) * 2048 + (rd ^ (64 * (i / HG))));
                 };
                 if constexpr (h == 0) {
 #pragma unroll
@@ -408,24 +411,28 @@ __device__ __forceinline__ void mx4_tile_run(const Args &a, uint8_t *lds, int e,
                     store_a(A[h ^ 1]);
                     if constexpr (!last) load_a(u + 3, A[h ^ 1]);
                 }
-                auto step = [&](auto SIDX) {
-                    constexpr int s = decltype(SIDX)::value;
+                auto part = [&](auto IDX) {
+                    constexpr int i = decltype(IDX)::value, s = i / HG, g0 = i % HG * GB;
                     __builtin_amdgcn_sched_barrier(0);
-                    if constexpr (s == 0) read_b(1, B[1]);
+                    if constexpr (i + 1 < 2 * HG) read_b(i + 1, B[(i + 1) & 1]);
 #pragma unroll
-                    for (int g = 0; g < CF; ++g)
+                    for (int g = 0; g < GB; ++g)
 #pragma unroll
                         for (int f = 0; f < RF; ++f)
-                            acc[f][g] = mfma_mx4_op<2 * h + s>(F[s][f], B[s][g], acc[f][g], ta[f], tb[g]);
+                            acc[f][g0 + g] = mfma_mx4_op<2 * h + s>(F[s][f], B[i & 1][g], acc[f][g0 + g], ta[f], tb[g0 + g]);
                     // (the compiler would move the products past the barrier to
                     // their last use, with all their operands held until then)
 #pragma unroll
-                    for (int g = 0; g < CF; ++g)
+                    for (int g = 0; g < GB; ++g)
 #pragma unroll
-                        for (int f = 0; f < RF; ++f) asm volatile("" : "+v"(acc[f][g]));
+                        for (int f = 0; f < RF; ++f) asm volatile("" : "+v"(acc[f][g0 + g]));
                 };
-                step(std::integral_constant<int, 0>{});
-                step(std::integral_constant<int, 1>{});
+                part(std::integral_constant<int, 0>{});
+                part(std::integral_constant<int, 1>{});
+                if constexpr (HG > 1) {
+                    part(std::integral_constant<int, 2>{});
+                    part(std::integral_constant<int, 3>{});
+                }
                 if constexpr (more) store_x(h ^ 1, X[h ^ 1]);
                 __syncthreads();
             };
@@ -471,13 +478,13 @@ __device__ __forceinline__ void mx4_tile_run(const Args &a, uint8_t *lds, int e,
 // b runs on XCD b % 8; the runs (item-major) are dealt to the XCDs in
 // contiguous parts, so that an XCD's L2 holds the vectors of a few experts,
 // and an expert's second chunk finds its weights there.
-template <int MODE>
+template <int MODE, int CHUNK>
 __global__ __launch_bounds__(64 * kMx4Waves, 2) void qmv_mx4_tile_kernel(const Args a)
 {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     constexpr int TR = 16 * kMx4RF * kMx4Waves / (MODE == 1 ? 2 : 1);
-    uint16_t *const list = (uint16_t *)lds;           // [kMx4Chunk]
-    uint8_t *const buf = lds + 2 * kMx4Chunk;
+    uint16_t *const list = (uint16_t *)lds;           // [CHUNK]
+    uint8_t *const buf = lds + 2 * CHUNK;
     const int runs = (a.bt_row_tiles + a.bt_chunk - 1) / a.bt_chunk;   // per item
     int item = -1, rt0 = 0, rt1 = 0;
     auto pick = [&](int items) {
@@ -495,24 +502,26 @@ __global__ __launch_bounds__(64 * kMx4Waves, 2) void qmv_mx4_tile_kernel(const A
     if (gather) {
         // (a call without any id in [0, E) still has its zero rows: one item)
         const int P = a.M * a.top_k;
-        const Mx4Item it = mx4_item<kMx4Chunk>(a.ids, P, a.E, (int *)buf, list, [&](int items) { return pick(max(items, 1)); });
+        const Mx4Item it = mx4_item<CHUNK>(a.ids, P, a.E, (int *)buf, list, [&](int items) { return pick(max(items, 1)); });
         if (item < 0) return;
         e = it.e;
         nv = it.nv;
         mx4_zero_rows(a, item, max(it.items, 1), rt0 * TR, min(rt1 * TR, a.N));
         if (nv == 0) return;
     } else {
-        if (pick((a.M + kMx4Chunk - 1) / kMx4Chunk) < 0) return;
-        vstart = item * kMx4Chunk;
-        nv = min(kMx4Chunk, a.M - vstart);
+        if (pick((a.M + CHUNK - 1) / CHUNK) < 0) return;
+        vstart = item * CHUNK;
+        nv = min(CHUNK, a.M - vstart);
     }
     const uint16_t *const vecs = gather ? list : nullptr;
-    if (nv > 32)
-        mx4_tile_run<MODE, 4>(a, buf, e, rt0, rt1, vecs, vstart, nv);
+    if (CHUNK > 64 && nv > 64)
+        mx4_tile_run<MODE, CHUNK / 16, CHUNK>(a, buf, e, rt0, rt1, vecs, vstart, nv);
+    else if (nv > 32)
+        mx4_tile_run<MODE, 4, CHUNK>(a, buf, e, rt0, rt1, vecs, vstart, nv);
     else if (nv > 16)
-        mx4_tile_run<MODE, 2>(a, buf, e, rt0, rt1, vecs, vstart, nv);
+        mx4_tile_run<MODE, 2, CHUNK>(a, buf, e, rt0, rt1, vecs, vstart, nv);
     else
-        mx4_tile_run<MODE, 1>(a, buf, e, rt0, rt1, vecs, vstart, nv);
+        mx4_tile_run<MODE, 1, CHUNK>(a, buf, e, rt0, rt1, vecs, vstart, nv);
 }
 
 // -------------------------------------------------------------- few vectors
@@ -984,10 +993,13 @@ const void *const kTableMx4Few[3] = {
     (const void *)&qmv_mx4_few_kernel<2>,
 };
 
-extern const void *const kTableMx4Tile[2];
-const void *const kTableMx4Tile[2] = {
-    (const void *)&qmv_mx4_tile_kernel<0>,
-    (const void *)&qmv_mx4_tile_kernel<1>,
+// [chunks of 64 or 128 vectors][plain, gate/up]
+extern const void *const kTableMx4Tile[4];
+const void *const kTableMx4Tile[4] = {
+    (const void *)&qmv_mx4_tile_kernel<0, 64>,
+    (const void *)&qmv_mx4_tile_kernel<1, 64>,
+    (const void *)&qmv_mx4_tile_kernel<0, 128>,
+    (const void *)&qmv_mx4_tile_kernel<1, 128>,
 };
 
 }  // namespace qmv

@@ -70,7 +70,8 @@ def test_dense(M, N, K):
 GATHER = [(1, 1, 1, 5, 32), (1, 32, 4, 70, 2880), (2, 8, 3, 33, 96), (4, 40, 8, 48, 512), (4, 2, 4, 100, 224),
           (5, 64, 2, 50, 160), (6, 3, 2, 65, 544), (37, 8, 4, 130, 288), (64, 200, 4, 20, 128), (100, 4, 4, 96, 1024),
           (16, 1023, 2, 9, 64), (512, 16, 4, 40, 96), (1, 2000, 16, 24, 256), (4, 70000, 2, 3, 32),
-          (70, 1, 3, 200, 320)]
+          (70, 1, 3, 200, 320), (129, 2, 2, 40, 2880), (65, 1, 1, 130, 3584), (300, 3, 2, 33, 3616),
+         (1000, 8, 2, 20, 64), (96, 2, 1, 129, 1504)]
 
 
 @pytest.mark.parametrize("M,E,top_k,N,K", GATHER)
@@ -91,7 +92,8 @@ def test_gather(M, E, top_k, N, K, per_slot):
 
 
 SWIGLU = [(1, 32, 4, 70, 2880), (4, 6, 2, 33, 96), (5, 64, 2, 50, 160), (37, 8, 4, 130, 288), (150, 4, 4, 96, 1024),
-          (3, 300, 8, 17, 64), (2, 1, 1, 5, 32), (300, 2, 2, 70, 544)]
+          (3, 300, 8, 17, 64), (2, 1, 1, 5, 32), (300, 2, 2, 70, 544), (129, 2, 2, 40, 2880), (65, 1, 1, 66, 3584),
+          (200, 3, 2, 33, 3616)]
 
 
 @pytest.mark.parametrize("M,E,top_k,N,K", SWIGLU)
