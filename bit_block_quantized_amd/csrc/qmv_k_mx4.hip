@@ -316,35 +316,62 @@ __device__ __forceinline__ void mx4_tile_run(const Args &a, uint8_t *lds, int e,
     // fetch their 128-byte line anew for every slab.  Neighbouring lanes take
     // neighbouring slabs of a row; an odd number of 16-byte segments from row
     // to row (bank conflicts).
-    auto stage_s = [&](const uint8_t *base, long long bytes, int rows, auto row_of, uint8_t *dst) {
+    auto scale_rsrc = [&](const uint8_t *base, long long bytes) {
         const uintptr_t p0 = (uintptr_t)base;
-        const __amdgpu_buffer_rsrc_t r =
-            buffer_rsrc((const void *)(p0 & ~(uintptr_t)3), ((long long)(p0 & 3) + bytes + 3) & ~3ll);
-        int t0 = tid;
-        asm volatile("" : "+v"(t0));
-        const int all = rows * J;
-        constexpr int SB = 4;                                       // segments in flight (the last one again past the end)
-#pragma unroll 1
-        for (; t0 < all; t0 += SB * 64 * NW) {
-            ScaleSeg sg[SB];
-            uint32_t o[SB];
-            int at[SB], n[SB];
+        return buffer_rsrc((const void *)(p0 & ~(uintptr_t)3), ((long long)(p0 & 3) + bytes + 3) & ~3ll);
+    };
+    // segments t0, t0 + 256, ... of `rows` rows (the last one again past the end)
+    auto load_s = [&](const uint8_t *base, __amdgpu_buffer_rsrc_t r, int rows, int t0, auto row_of, auto &sg) {
+        constexpr int SB = sizeof(sg) / sizeof(sg[0]);
 #pragma unroll
-            for (int k = 0; k < SB; ++k) {
-                const int t = min(t0 + k * 64 * NW, all - 1), row = t / J, j = t - row * J;
-                o[k] = (uint32_t)(p0 & 3) + row_of(row) * rsb + 16u * j;
-                at[k] = row * SP + 16 * j;
-                n[k] = U - 16 * j;
-                sg[k] = load_seg<true>(r, o[k]);
-            }
-#pragma unroll
-            for (int k = 0; k < SB; ++k) *(u32x4 *)(dst + at[k]) = seg_order<true>(sg[k], o[k], n[k]);
+        for (int k = 0; k < SB; ++k) {
+            const int t = min(t0 + k * 64 * NW, rows * J - 1), row = t / J, j = t - row * J;
+            sg[k].o = (uint32_t)((uintptr_t)base & 3) + row_of(row) * rsb + 16u * j;
+            sg[k].at = row * SP + 16 * j;
+            sg[k].n = U - 16 * j;
+            sg[k].s = load_seg<true>(r, sg[k].o);
         }
     };
-    auto stage_rows = [&](int row_base) {
+    auto store_s = [&](uint8_t *dst, const auto &sg) {
+        constexpr int SB = sizeof(sg) / sizeof(sg[0]);
+#pragma unroll
+        for (int k = 0; k < SB; ++k) *(u32x4 *)(dst + sg[k].at) = seg_order<true>(sg[k].s, sg[k].o, sg[k].n);
+    };
+    struct Seg { ScaleSeg s; uint32_t o; int at, n; };
+    // A tile's scale rows, and (VECS) the vectors' before them: the first
+    // segments of all of them are on their way before one is waited for.
+    auto stage_scales = [&](int row_base, auto VECS) {
+        constexpr bool vecs_too = decltype(VECS)::value;
+        int t0 = tid;
+        asm volatile("" : "+v"(t0));
         auto tile_row = [&](int row) { return (uint32_t)min(row_base + row, N - 1); };
-        stage_s(a.scales + e * a.expert_sb, a.expert_sb, TR, tile_row, ls);
-        if constexpr (MODE == 1) stage_s(a.scales2 + e * a.expert_sb, a.expert_sb, TR, tile_row, ls + TR * SP);
+        auto vec = [&](int v) { return vec_row(v < nv ? v : 0); };
+        const uint8_t *const b0 = a.scales + e * a.expert_sb, *const b1 = (MODE == 1 ? a.scales2 : a.scales) + e * a.expert_sb;
+        const uint8_t *const bx = (const uint8_t *)a.xs;
+        const __amdgpu_buffer_rsrc_t r0 = scale_rsrc(b0, a.expert_sb), r1 = scale_rsrc(b1, a.expert_sb),
+                                     rv = scale_rsrc(bx, (long long)x_rows * rsb);
+        constexpr int SR = MODE == 1 ? 2 : 4, SV = 4;
+        Seg g0[SR], g1[SR], gv[SV];
+        load_s(b0, r0, TR, t0, tile_row, g0);
+        if constexpr (MODE == 1) load_s(b1, r1, TR, t0, tile_row, g1);
+        if constexpr (vecs_too) load_s(bx, rv, 16 * CF, t0, vec, gv);
+        store_s(ls, g0);
+        if constexpr (MODE == 1) store_s(ls + TR * SP, g1);
+        if constexpr (vecs_too) store_s(ls + BR * SP, gv);
+#pragma unroll 1
+        for (int t = t0 + SR * 64 * NW; t < TR * J; t += SR * 64 * NW) {
+            load_s(b0, r0, TR, t, tile_row, g0);
+            if constexpr (MODE == 1) load_s(b1, r1, TR, t, tile_row, g1);
+            store_s(ls, g0);
+            if constexpr (MODE == 1) store_s(ls + TR * SP, g1);
+        }
+        if constexpr (vecs_too) {
+#pragma unroll 1
+            for (int t = t0 + SV * 64 * NW; t < 16 * CF * J; t += SV * 64 * NW) {
+                load_s(bx, rv, 16 * CF, t, vec, gv);
+                store_s(ls + BR * SP, gv);
+            }
+        }
     };
     // where the wave's fragments' scales stand
     auto seg_of_row = [&](int f) { return MODE == 1 ? (f >= RH ? TR : 0) + 16 * (w * RH + f % RH) : 16 * (w * RF + f); };
@@ -356,23 +383,24 @@ __device__ __forceinline__ void mx4_tile_run(const Args &a, uint8_t *lds, int e,
     // every load has a whole unit's time before its registers are needed.
     // (Loads return in the order of issue: a wait for the vectors alone, one
     // unit ahead, would wait for the weights issued before them too.)
-    u32x4 A0[RF][2], A[2][RF][2], X0[XU], X[2][XU];
+    u32x4 A0[RF][2], A[2][RF][2], X[2][XU];
     auto first_loads = [&](int row_base) {
         set_rows(row_base);
         load_a(0, A0);
-        load_x(0, X0);
+        load_x(0, X[0]);
         load_x(1, X[1]);
         load_a(1, A[1]);
         load_a(2, A[0]);
     };
     first_loads(rt0 * TR);
-    stage_s((const uint8_t *)a.xs, (long long)x_rows * rsb, 16 * CF, [&](int v) { return vec_row(v < nv ? v : 0); },
-            ls + BR * SP);
     for (int rt = rt0; rt < rt1; ++rt) {
         const int row_base = rt * TR;
-        stage_rows(row_base);
+        if (rt == rt0)
+            stage_scales(row_base, std::true_type{});
+        else
+            stage_scales(row_base, std::false_type{});
         store_a(A0);
-        store_x(0, X0);
+        store_x(0, X[0]);
         f32x4 acc[RF][CF];
 #pragma unroll
         for (int f = 0; f < RF; ++f)
