@@ -711,7 +711,7 @@ __global__ __launch_bounds__(64 * kMx4Waves) void qmv_mx4_few_kernel(const Args 
             if constexpr (MODE == 2) {
                 for (int k = 0; k < ns; ++k) {
                     int ee = __builtin_amdgcn_readlane(ids_lane, s0 + k);
-                    if ((unsigned)ee >= (unsigned)a.E) ee = 0;                     // (times zero codes)
+                    if ((unsigned)ee >= (unsigned)a.E) ee = 0;                     // (unused)
                     stage_s(a.scales + ee * a.expert_sb, a.expert_sb, 16, tile_row, ls + k * 16 * SP);
                 }
             } else {
@@ -760,8 +760,11 @@ __global__ __launch_bounds__(64 * kMx4Waves) void qmv_mx4_few_kernel(const Args 
                             if ((g + NW) / NU != slot || i + 1 == mine) {          // this wave's last unit of the slot
                                 const float rw = __uint_as_float(
                                     __builtin_amdgcn_readlane(__float_as_uint(rw_lane), s0 + slot));
+                                // (a slot without an expert is 0 whatever scales
+                                // its vector has; zero codes times NaN are not)
+                                const bool have = (unsigned)__builtin_amdgcn_readlane(ids_lane, s0 + slot) < (unsigned)a.E;
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) tot[k] = __builtin_fmaf(rw, acc[0][k], tot[k]);
+                                for (int k = 0; k < 4; ++k) tot[k] = __builtin_fmaf(rw, have ? acc[0][k] : 0.0f, tot[k]);
                                 acc[0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                             }
                         }

@@ -106,10 +106,10 @@
  * untouched.  No check needs a device synchronization.  QMV_EHIP (the
  * runtime refused a launch) can come after earlier launches of the same
  * call have run: a dense (MXFP4, BF16) call with 5 to 8 vectors, and a
- * gather or gate/up call with 5 to 64 tokens and fewer than two (token,
- * slot) pairs per expert (M * top_k < 2 E), are one launch per group of up
- * to 4 vectors or tokens, so y may then hold the rows of the groups before
- * the failing one.  A combine call with more than 4 tokens writes y only in
+ * gather or gate/up call (of another pair than (MXFP4, MXFP4)) with 5 to 64
+ * tokens and fewer than two (token, slot) pairs per expert (M * top_k < 2 E),
+ * are one launch per group of up to 4 vectors or tokens, so y may then hold
+ * the rows of the groups before the failing one.  A combine call with more than 4 tokens writes y only in
  * its last launch.  Every other call is one launch.  An expert
  * id outside [0, E) is not an error: that (token, slot) output row is
  * written with zeros (mlxcel issue #2178, Implementation Notes, Edge cases).
@@ -154,7 +154,9 @@ typedef enum {
  * 32-vector column fragments), and M > 64 on the batched matrix-core kernel
  * described under qmv_gather_moe; 2-bit and 3-bit
  * weights with int8 (or in-kernel quantized bf16) activations and M >= 8 on
- * the int8 matrix-core kernel;
+ * the int8 matrix-core kernel; (MXFP4, MXFP4) with any M on the block-scaled
+ * matrix cores (16 rows and 16 vectors a workgroup with K split over its
+ * waves, 128 x 64 tiles, or 256 x 256 tiles once they fill half of the chip);
  * every other M > 4 call on the grouped kernel.
  */
 qmv_status_t qmv_dense(qmv_wfmt_t wfmt, const void *w_codes, const void *w_scales,
@@ -185,6 +187,10 @@ qmv_status_t qmv_dense(qmv_wfmt_t wfmt, const void *w_codes, const void *w_scale
  *     (2-bit) or 12 (3-bit) vectors per staged chunk (bf16 x quantized
  *     while staged), each workgroup a run of (expert, row tile) items of
  *     equal cost with the experts' vector counts weighed in;
+ *   (MXFP4, MXFP4): an expert's vectors in equal chunks, each chunk reading
+ *     the expert's rows once, on the block-scaled matrix cores; chunks of up
+ *     to 16 with M * top_k < 2 E (with M <= 4 too), else of up to 64, or 128
+ *     from 48 pairs an expert on where K leaves the LDS for them;
  *   at most 64 tokens with fewer than two pairs per expert: groups of up to
  *     4 tokens on the decode kernels, one launch per group;
  *   every other call: the decode kernels' own multiply-adds in one launch,
@@ -209,8 +215,9 @@ qmv_status_t qmv_gather_moe(qmv_wfmt_t wfmt, const void *w_codes, const void *w_
  * computes in one matvec kernel -- and hands the down projection its input
  * directly.  Arguments, limits and errors as qmv_gather_moe (M > 4
  * included: (MXFP4, BF16) with M * top_k >= 2 E on the batched matrix-core
- * kernel with a gate and an up fragment per output fragment, every other
- * call on the grouped kernel); silu is evaluated in fp32.
+ * kernel with a gate and an up fragment per output fragment, (MXFP4, MXFP4)
+ * likewise on the block-scaled ones, every other call on the grouped
+ * kernel); silu is evaluated in fp32.
  */
 qmv_status_t qmv_gather_moe_swiglu(qmv_wfmt_t wfmt, const void *gate_codes, const void *gate_scales,
                                    const void *up_codes, const void *up_scales, int E,
@@ -238,7 +245,9 @@ qmv_status_t qmv_gather_moe_swiglu(qmv_wfmt_t wfmt, const void *gate_codes, cons
  * multiply-add onto a sum that starts at zero; results are bitwise
  * reproducible.  An out-of-range id contributes route_weights[t][j] * 0.
  * Up to 4 tokens: one launch, a workgroup per token and row tile, each lane
- * carrying one row of four of the token's slots.  More than 4 tokens: the
+ * carrying one row of four of the token's slots (with (MXFP4, MXFP4) the
+ * slots one after another on the matrix cores, their partial rows summed in
+ * slot order).  More than 4 tokens: the
  * gather of qmv_gather_moe (same kernels and routing) writes every (token,
  * slot) row to a temporary of M * top_k * N floats from the library's pool
  * (see Ownership; it can be recorded into a HIP graph as the graph's own

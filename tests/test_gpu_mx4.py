@@ -139,6 +139,29 @@ def test_combine(M, E, top_k, N, K, per_slot):
     assert torch.equal(y, z)
 
 
+@pytest.mark.parametrize("M", [1, 4, 5, 40])
+def test_slots_without_an_expert_hide_nan(M):
+    """NaN scales of a slot whose id is outside [0, E), and of the expert that
+    no pair has, reach no output."""
+    E, top_k, N, K = 6, 4, 50, 544
+    rng = np.random.default_rng(M)
+    wc, ws = make(rng, (E, N), K)
+    ws[0] = 255
+    xc, xs = make(rng, (M, top_k), K)
+    ids = rng.integers(1, E, (M, top_k)).astype(np.int32)
+    for t in range(M):
+        ids[t, t % top_k] = (-1, E, -2 ** 31, 2 ** 31 - 1)[t % 4]
+        xs[t, t % top_k] = 255
+    rw = rng.standard_normal((M, top_k)).astype(np.float32)
+    y = q.qmv_gather_moe_combine("mxfp4", dev(wc), dev(ws), dev(ids), dev(rw), dev(xc), dev(xs))
+    rows = q.qmv_gather_moe("mxfp4", dev(wc), dev(ws), dev(ids), dev(xc), dev(xs))
+    ws[0], xs[xs == 255] = 120, 120
+    g, A = R.gather(ids, R.values(wc, ws), R.values(xc, xs), True)
+    close(rows, g, K * U * A, f"gather {M}")
+    want = (rw[:, :, None].astype(np.float64) * g).sum(axis=1)
+    close(y, want, ((K + 2 * top_k) * U * np.abs(rw[:, :, None]) * A).sum(axis=1), f"combine {M}")
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 48, 2880), (4, 100, 512), (40, 70, 1056), (200, 300, 2048)])
 def test_one_scale_is_exact(M, N, K):
     rng = np.random.default_rng(K)
