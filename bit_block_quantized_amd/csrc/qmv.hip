@@ -617,11 +617,14 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
     const int U = K / 32, J = (U + 15) / 16, h = mode == 1 ? 2 : 1;
     const int xp = (U + 7) / 8 * 128 + 16, sp = 16 * (J | 1), most = pairs < 16 ? pairs : 16;
     size_t lds_few = 64 + 4 * h * 2048 + (size_t)most * (xp + sp) + (size_t)h * 16 * sp;
-    // 256 x 256 tiles once they fill half of the chip (us, against the tile
-    // kernel's 128 x 64: 56 tiles 60 and 38; 96 60 and 59, 33 and 32; 108 33 and
-    // 28; 112 63 and 74, 26 and 29; 192 36 and 50; 224 70 and 136; 896 275 and 493)
+    // 256 x 256 tiles once they fill half of the chip and more than half of
+    // their vectors exist (us, against the tile kernel's 128 x 64: 56 tiles 60
+    // and 38; 96 60 and 59, 33 and 32; 108 33 and 28; 112 63 and 74, 26 and 29;
+    // 192 36 and 50; 224 70 and 136; 896 275 and 493.  2880 -> 201088: 64 vectors
+    // 131 and 93, 128 148 and 146, 192 168 and 242; 7168 -> 40960: 128 66 and 57,
+    // 192 70 and 80)
     const long long wide_tiles = (long long)((N + 255) / 256) * ((M + 255) / 256);
-    if (!gather && mode == 0 && 2 * wide_tiles >= cu_count()) {
+    if (!gather && mode == 0 && M > 128 && 2 * wide_tiles >= cu_count()) {
         const int lds = 4 * 256 * 128 + 4 * 256 * 16;
         a.bt_row_tiles = (N + 255) / 256;
         a.bt_vmax = 4;
@@ -640,8 +643,9 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
     // dense: a workgroup per 16 rows and 16 vectors until there are three per CU
     // (7168 -> 2048: 32 vectors 10 us against the tile kernel's 15, 64 9.4 and
     // 18.5; 2880 -> 2880: 64 8.9 and 11.5, 128 14 and 11.5; 7168 -> 7168: 16 11.5
-    // and 17, 32 19 and 18, 64 35 and 20)
-    const bool many = gather ? pairs >= 2 * E : M > 16 && (long long)((M + 15) / 16) * ((N + 15) / 16) > 3 * cu_count();
+    // and 17, 32 19 and 18, 64 35 and 20; 2880 -> 201088: 4 79 and 69, 8 86 and
+    // 73, 16 99 and 76; 7168 -> 40960: 4 29 and 34, 8 38 and 34, 16 49 and 35)
+    const bool many = gather ? pairs >= 2 * E : M > kMaxM && (long long)((M + 15) / 16) * ((N + 15) / 16) > 3 * cu_count();
     if (mode != 2 && (many || lds_few > kLdsPerCU)) {
         const int rows = mode == 1 ? 64 : 128;
         a.bt_row_tiles = (N + rows - 1) / rows;

@@ -54,7 +54,8 @@ DENSE = [(1, 1, 32), (1, 17, 64), (1, 2880, 2880), (2, 33, 96), (4, 64, 544), (5
 # tiles of 128 x 64 with few vectors and many rows
 DENSE += [(600, 130, 2880), (520, 70, 32), (777, 260, 544), (512, 256, 1536), (1100, 515, 1056), (2049, 300, 128),
           (4100, 33, 96), (2050, 3600, 32), (1900, 4097, 160), (4100, 2050, 544), (2049, 3850, 1056), (8192, 900, 96),
-          (1025, 7001, 512), (17, 12400, 64), (70, 2900, 96), (200, 1100, 544), (96, 2700, 2880), (33, 5000, 1056)]
+          (1025, 7001, 512), (17, 12400, 64), (70, 2900, 96), (200, 1100, 544), (96, 2700, 2880), (33, 5000, 1056),
+          (1, 33000, 96), (4, 12320, 64), (5, 12320, 64), (16, 13000, 160), (128, 16500, 64), (129, 16400, 96)]
 
 
 @pytest.mark.parametrize("M,N,K", DENSE)
