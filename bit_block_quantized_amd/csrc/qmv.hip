@@ -615,8 +615,9 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
     const int pairs = gather ? M * top_k : M;
     // the few kernel's LDS: weight pieces, the vectors (codes and scales), the rows' scales
     const int U = K / 32, J = (U + 15) / 16, h = mode == 1 ? 2 : 1;
-    const int xp = (U + 7) / 8 * 128 + 16, sp = 16 * (J | 1), most = pairs < 16 ? pairs : 16;
-    size_t lds_few = 64 + 4 * h * 2048 + (size_t)most * (xp + sp) + (size_t)h * 16 * sp;
+    const int xp = (U + 7) / 8 * 128 + 16, sp = 16 * (J | 1);
+    auto few_lds = [&](int vectors) { return 64 + 4 * h * 2048 + (size_t)vectors * (xp + sp) + (size_t)h * 16 * sp; };
+    int most = pairs < 16 ? pairs : 16;
     // 256 x 256 tiles once they fill half of the chip and more than half of
     // their vectors exist (us, against the tile kernel's 128 x 64: 56 tiles 60
     // and 38; 96 60 and 59, 33 and 32; 108 33 and 28; 112 63 and 74, 26 and 29;
@@ -646,7 +647,8 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
     // and 17, 32 19 and 18, 64 35 and 20; 2880 -> 201088: 4 79 and 69, 8 86 and
     // 73, 16 99 and 76; 7168 -> 40960: 4 29 and 34, 8 38 and 34, 16 49 and 35)
     const bool many = gather ? pairs >= 2 * E : M > kMaxM && (long long)((M + 15) / 16) * ((N + 15) / 16) > 3 * cu_count();
-    if (mode != 2 && (many || lds_few > kLdsPerCU)) {
+    // (the tile kernel counts the pairs of up to 1023 experts)
+    if (mode != 2 && (!gather || E <= kMaxEBatched) && (many || few_lds(most) > kLdsPerCU)) {
         const int rows = mode == 1 ? 64 : 128;
         a.bt_row_tiles = (N + rows - 1) / rows;
         // chunks of 128 vectors where many experts have more than 64, as long as
@@ -681,7 +683,9 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
     // few vectors: 16-row tiles, K split over the waves
     a.bt_row_tiles = (N + 15) / 16;
     a.bt_chunk = 1;
-    size_t lds = lds_few;
+    if (mode != 2 && few_lds(most) > kLdsPerCU)
+        most = 8;                               // (gate/up with the longest rows)
+    size_t lds = few_lds(most);
     dim3 grid((unsigned)a.bt_row_tiles, 1);
     if (mode == 2) {
         // as many slots staged at a time as 64 KB hold
@@ -699,7 +703,7 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
             const long long groups = items * ((a.bt_row_tiles + a.bt_chunk - 1) / a.bt_chunk);
             grid.x = (unsigned)(8 * ((groups + 7) / 8));
         } else if (gather) {
-            grid.y = (unsigned)(pairs * ((pairs + 15) / 16));
+            grid.y = (unsigned)(pairs * ((pairs + most - 1) / most));
         } else {
             grid.y = (unsigned)((M + 15) / 16);
         }

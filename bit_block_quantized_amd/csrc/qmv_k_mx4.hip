@@ -608,7 +608,7 @@ __global__ __launch_bounds__(64 * kMx4Waves) void qmv_mx4_few_kernel(const Args 
         // pair has it (up to 64 pairs: one lane each)
         rt1 = min(rt0 + a.bt_chunk, a.bt_row_tiles);
         const int id = lane < P ? a.ids[lane] : -1, y = blockIdx.y % P;
-        const int chunk = blockIdx.y / P;                      // of 16 pairs of the expert
+        const int chunk = blockIdx.y / P;                      // of bt_vmax pairs of the expert
         e = __builtin_amdgcn_readlane(id, y);
         if ((unsigned)e >= (unsigned)a.E) {
             if (chunk == 0)
@@ -618,11 +618,11 @@ __global__ __launch_bounds__(64 * kMx4Waves) void qmv_mx4_few_kernel(const Args 
         const unsigned long long m = __ballot(id == e);
         if (__ffsll((long long)m) - 1 != y) return;
         // (bit counts are unsigned: as int before anything is subtracted)
-        const int r = (int)__popcll(m & ((1ull << lane) - 1ull)) - chunk * kMx4Few;
-        const int left = (int)__popcll(m) - chunk * kMx4Few;
+        const int r = (int)__popcll(m & ((1ull << lane) - 1ull)) - chunk * a.bt_vmax;
+        const int left = (int)__popcll(m) - chunk * a.bt_vmax;
         if (left <= 0) return;
-        nv = min(left, kMx4Few);
-        if ((m >> lane & 1) && r >= 0 && r < kMx4Few) list[r] = (uint16_t)lane;    // (every wave the same)
+        nv = min(left, a.bt_vmax);
+        if ((m >> lane & 1) && r >= 0 && r < a.bt_vmax) list[r] = (uint16_t)lane;    // (every wave the same)
     } else {
         const int runs = (a.bt_row_tiles + a.bt_chunk - 1) / a.bt_chunk;
         int item = -1;

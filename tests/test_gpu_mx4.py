@@ -94,7 +94,7 @@ def test_gather(M, E, top_k, N, K, per_slot):
 
 SWIGLU = [(1, 32, 4, 70, 2880), (4, 6, 2, 33, 96), (5, 64, 2, 50, 160), (37, 8, 4, 130, 288), (150, 4, 4, 96, 1024),
           (3, 300, 8, 17, 64), (2, 1, 1, 5, 32), (300, 2, 2, 70, 544), (129, 2, 2, 40, 2880), (65, 1, 1, 66, 3584),
-          (200, 3, 2, 33, 3616)]
+          (200, 3, 2, 33, 3616), (4, 1100, 16, 3, 16384), (4, 2, 16, 20, 16384), (1, 1500, 15, 5, 15392)]
 
 
 @pytest.mark.parametrize("M,E,top_k,N,K", SWIGLU)
