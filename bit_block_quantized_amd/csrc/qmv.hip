@@ -641,12 +641,19 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
                    ? QMV_OK
                    : QMV_EHIP;
     }
-    // dense: a workgroup per 16 rows and 16 vectors until there are three per CU
-    // (7168 -> 2048: 32 vectors 10 us against the tile kernel's 15, 64 9.4 and
-    // 18.5; 2880 -> 2880: 64 8.9 and 11.5, 128 14 and 11.5; 7168 -> 7168: 16 11.5
-    // and 17, 32 19 and 18, 64 35 and 20; 2880 -> 201088: 4 79 and 69, 8 86 and
-    // 73, 16 99 and 76; 7168 -> 40960: 4 29 and 34, 8 38 and 34, 16 49 and 35)
-    const bool many = gather ? pairs >= 2 * E : M > kMaxM && (long long)((M + 15) / 16) * ((N + 15) / 16) > 3 * cu_count();
+    // Few vectors: workgroups of 16 rows while the chip is not full of them.
+    // Dense, one per 16 vectors, until there are three per CU (us, against the
+    // tile kernel: 7168 -> 2048: 32 vectors 10 and 15, 64 9.4 and 18.5; 2880 ->
+    // 2880: 64 8.9 and 11.5, 128 14 and 11.5; 7168 -> 7168: 16 11.5 and 17, 32 19
+    // and 18, 64 35 and 20; 2880 -> 201088: 4 79 and 69, 8 86 and 73, 16 99 and
+    // 76; 7168 -> 40960: 4 29 and 34, 8 38 and 34, 16 49 and 35).
+    // Routed, one per pair (of gate and of up), until there are seven per CU
+    // (2880 -> 2880 of 32 experts: 4 pairs 10.5 and 13.6, 8 10.9 and 13, 12 16
+    // and 14, 16 20.9 and 19.5, 32 30 and 22, 128 67 and 41; gate/up 4 pairs 12
+    // and 13, 8 21 and 18.6; 7168 -> 2048 of 256: 8 pairs 15.8 and 16.7, 16 28
+    // and 25, 64 104 and 84; 4096 -> 14336 of 8: 2 pairs 14.8 and 15.9).
+    const long long row_tiles = (N + 15) / 16;
+    const bool many = gather ? pairs * row_tiles * h > 7 * cu_count() : M > kMaxM && (M + 15) / 16 * row_tiles > 3 * cu_count();
     // (the tile kernel counts the pairs of up to 1023 experts)
     if (mode != 2 && (!gather || E <= kMaxEBatched) && (many || few_lds(most) > kLdsPerCU)) {
         const int rows = mode == 1 ? 64 : 128;
@@ -681,8 +688,7 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
                                lds, stream) == hipSuccess ? QMV_OK : QMV_EHIP;
     }
     // few vectors: 16-row tiles, K split over the waves
-    a.bt_row_tiles = (N + 15) / 16;
-    a.bt_chunk = 1;
+    a.bt_row_tiles = (int)row_tiles;
     if (mode != 2 && few_lds(most) > kLdsPerCU)
         most = 8;                               // (gate/up with the longest rows)
     size_t lds = few_lds(most);
@@ -698,10 +704,7 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
         if (gather && pairs > 64) {
             if (lds < 64 + 4 * 1032) lds = 64 + 4 * 1032;      // the counts per expert
             const long long items = (pairs < E ? pairs : E) + pairs / 16;
-            const long long run = items * a.bt_row_tiles / (16 * cu_count());
-            a.bt_chunk = run < 1 ? 1 : run > a.bt_row_tiles ? a.bt_row_tiles : (int)run;
-            const long long groups = items * ((a.bt_row_tiles + a.bt_chunk - 1) / a.bt_chunk);
-            grid.x = (unsigned)(8 * ((groups + 7) / 8));
+            grid.x = (unsigned)(8 * ((items * row_tiles + 7) / 8));
         } else if (gather) {
             grid.y = (unsigned)(pairs * ((pairs + most - 1) / most));
         } else {

@@ -553,9 +553,8 @@ __global__ __launch_bounds__(64 * kMx4Waves, 2) void qmv_mx4_tile_kernel(const A
 }
 
 // -------------------------------------------------------------- few vectors
-// Up to 16 vectors of an expert (a dense matrix) against a run of 16-row
-// tiles, or (MODE 2, the combine) a token's slots, each with its expert,
-// against one 16-row tile.  The call waits for its weight bytes, so the 4
+// Up to 16 vectors of an expert (a dense matrix), or (MODE 2, the combine) a
+// token's slots, each with its expert, against one tile of 16 rows.  The call waits for its weight bytes, so the 4
 // waves of a workgroup split K -- wave w takes units (256 weights) w, w + 4,
 // ... -- and each has up to kFewAhead units of its rows on their way from the
 // start; the vectors and the scale bytes are staged in LDS once.  The waves'
@@ -589,7 +588,7 @@ __global__ __launch_bounds__(64 * kMx4Waves) void qmv_mx4_few_kernel(const Args 
     uint8_t *const ls = lxs + a.bt_vmax * SP;                  // [H or slots][16 rows] x SP
 
     // ---- which expert, vectors and row tiles
-    int e = 0, nv = 1, v0 = 0, rt0 = blockIdx.x * a.bt_chunk, rt1;
+    int e = 0, nv = 1, v0 = 0, rt = blockIdx.x;
     int ids_lane = 0;
     float rw_lane = 0.0f;
     if constexpr (MODE == 2) {
@@ -598,21 +597,18 @@ __global__ __launch_bounds__(64 * kMx4Waves) void qmv_mx4_few_kernel(const Args 
             ids_lane = a.ids[blockIdx.y * a.top_k + lane];
             rw_lane = a.route_w[blockIdx.y * a.top_k + lane];
         }
-        rt1 = rt0 + 1;
     } else if (!gather) {
-        rt1 = min(rt0 + a.bt_chunk, a.bt_row_tiles);
         v0 = blockIdx.y * kMx4Few;
         nv = min(kMx4Few, a.M - v0);
     } else if (P <= 64) {
         // workgroup row blockIdx.y: pair blockIdx.y's expert, if no earlier
         // pair has it (up to 64 pairs: one lane each)
-        rt1 = min(rt0 + a.bt_chunk, a.bt_row_tiles);
         const int id = lane < P ? a.ids[lane] : -1, y = blockIdx.y % P;
         const int chunk = blockIdx.y / P;                      // of bt_vmax pairs of the expert
         e = __builtin_amdgcn_readlane(id, y);
         if ((unsigned)e >= (unsigned)a.E) {
             if (chunk == 0)
-                for (int n = rt0 * 16 + tid; n < min(rt1 * 16, N); n += 64 * NW) a.y[(size_t)y * N + n] = 0.0f;
+                for (int n = rt * 16 + tid; n < min(rt * 16 + 16, N); n += 64 * NW) a.y[(size_t)y * N + n] = 0.0f;
             return;
         }
         const unsigned long long m = __ballot(id == e);
@@ -624,23 +620,20 @@ __global__ __launch_bounds__(64 * kMx4Waves) void qmv_mx4_few_kernel(const Args 
         nv = min(left, a.bt_vmax);
         if ((m >> lane & 1) && r >= 0 && r < a.bt_vmax) list[r] = (uint16_t)lane;    // (every wave the same)
     } else {
-        const int runs = (a.bt_row_tiles + a.bt_chunk - 1) / a.bt_chunk;
         int item = -1;
-        rt1 = 0;
         const Mx4Item it = mx4_item<kMx4Few>(a.ids, P, a.E, (int *)(lds + 64), list, [&](int items) {
-            const int all = max(items, 1) * runs, per_xcd = (all + 7) / 8, i = blockIdx.x >> 3;
+            const int all = max(items, 1) * a.bt_row_tiles, per_xcd = (all + 7) / 8, i = blockIdx.x >> 3;
             const int r = i < per_xcd ? (int)(blockIdx.x & 7) * per_xcd + i : all;
             if (r < all) {
-                item = r / runs;
-                rt0 = (r - item * runs) * a.bt_chunk;
-                rt1 = min(rt0 + a.bt_chunk, a.bt_row_tiles);
+                item = r / a.bt_row_tiles;
+                rt = r - item * a.bt_row_tiles;
             }
             return item;
         });
         if (item < 0) return;
         e = it.e;
         nv = it.nv;
-        mx4_zero_rows(a, item, max(it.items, 1), rt0 * 16, min(rt1 * 16, N));
+        mx4_zero_rows(a, item, max(it.items, 1), rt * 16, min(rt * 16 + 16, N));
         if (nv == 0) return;
         __syncthreads();                                       // (the counts lie where the staging goes)
     }
@@ -654,150 +647,145 @@ __global__ __launch_bounds__(64 * kMx4Waves) void qmv_mx4_few_kernel(const Args 
         return (uint32_t)(routed && !a.x_per_slot ? p / top_k : p);
     };
 
-    // ---- groups of slots (MODE 2: bt_vmax at a time; else one pass a row tile)
+    // ---- groups of slots (MODE 2: bt_vmax at a time; else one pass)
     const int slots = MODE == 2 ? top_k : 1, per = MODE == 2 ? a.bt_vmax : 1;
     const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(a.x, (long long)x_rows * a.x_vec_bytes);
     f32x4 tot = {0.0f, 0.0f, 0.0f, 0.0f};
     u32x4 A[D][H][2];
-    for (int rt = rt0; rt < rt1; ++rt) {
-        const int row0 = rt * 16;
-        uint32_t oc[2];
+    const int row0 = rt * 16;
+    uint32_t oc[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i) oc[i] = (uint32_t)min(row0 + 8 * i + lr, N - 1) * (uint32_t)a.rcb + 16u * lc;
-        for (int s0 = 0; s0 < slots; s0 += per) {
-            const int ns = min(per, slots - s0), total = ns * NU;
-            auto load_a = [&](int i, u32x4 (&R)[H][2]) {
-                const int g = w + NW * i;
-                const int slot = MODE == 2 ? g / NU : 0, u = g - slot * NU;
-                int ee = e;
-                long long size = a.expert_cb;
-                if constexpr (MODE == 2) {
-                    ee = __builtin_amdgcn_readlane(ids_lane, g < total ? s0 + slot : 0);
-                    if ((unsigned)ee >= (unsigned)a.E) ee = 0, size = 0;           // reads zeros
-                }
-                const uint32_t so = g < total ? 128u * u : kXPast;
-#pragma unroll
-                for (int h = 0; h < H; ++h) {                                      // (nt: read once)
-                    const __amdgpu_buffer_rsrc_t rc = buffer_rsrc((h ? a.codes2 : a.codes) + ee * a.expert_cb, size);
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) R[h][k] = __builtin_amdgcn_raw_buffer_load_b128(rc, oc[k] + so, 0, 2);
-                }
-            };
-            auto stage_s = [&](const uint8_t *base, long long bytes, int rows, auto row_of, uint8_t *dst) {
-                const uintptr_t p0 = (uintptr_t)base;
-                const __amdgpu_buffer_rsrc_t r =
-                    buffer_rsrc((const void *)(p0 & ~(uintptr_t)3), ((long long)(p0 & 3) + bytes + 3) & ~3ll);
-                for (int t = tid; t < rows * J; t += 64 * NW) {
-                    const int row = t / J, j = t - row * J;
-                    const uint32_t o = (uint32_t)(p0 & 3) + row_of(row) * rsb + 16u * j;
-                    *(u32x4 *)(dst + row * SP + 16 * j) = seg_order<true>(load_seg<true>(r, o), o, U - 16 * j);
-                }
-            };
-            auto tile_row = [&](int row) { return (uint32_t)min(row0 + row, N - 1); };
-#pragma unroll
-            for (int i = 0; i < D; ++i) load_a(i, A[i]);
-            if (rt == rt0) {
-                // the vectors (MODE 2: those of the group's slots)
-                const int vecs = MODE == 2 ? (a.x_per_slot ? ns : 1) : nv;
-                for (int t = tid; t < vecs * 8 * NU; t += 64 * NW) {
-                    const int v = t / (8 * NU), b = t - v * 8 * NU;
-                    const uint32_t o = vec_row(MODE == 2 ? s0 + v : v) * (uint32_t)a.x_vec_bytes + 16u * b;
-                    *(u32x4 *)(lx + v * XP + 16 * b) =
-                        __builtin_amdgcn_raw_buffer_load_b128(rx, b < U ? o : kXPast, 0, 0);
-                }
-                stage_s((const uint8_t *)a.xs, (long long)x_rows * rsb, vecs,
-                        [&](int v) { return vec_row(MODE == 2 ? s0 + v : v); }, lxs);
-            }
+    for (int i = 0; i < 2; ++i) oc[i] = (uint32_t)min(row0 + 8 * i + lr, N - 1) * (uint32_t)a.rcb + 16u * lc;
+    for (int s0 = 0; s0 < slots; s0 += per) {
+        const int ns = min(per, slots - s0), total = ns * NU;
+        auto load_a = [&](int i, u32x4 (&R)[H][2]) {
+            const int g = w + NW * i;
+            const int slot = MODE == 2 ? g / NU : 0, u = g - slot * NU;
+            int ee = e;
+            long long size = a.expert_cb;
             if constexpr (MODE == 2) {
-                for (int k = 0; k < ns; ++k) {
-                    int ee = __builtin_amdgcn_readlane(ids_lane, s0 + k);
-                    if ((unsigned)ee >= (unsigned)a.E) ee = 0;                     // (unused)
-                    stage_s(a.scales + ee * a.expert_sb, a.expert_sb, 16, tile_row, ls + k * 16 * SP);
-                }
-            } else {
-                stage_s(a.scales + e * a.expert_sb, a.expert_sb, 16, tile_row, ls);
-                if constexpr (H == 2) stage_s(a.scales2 + e * a.expert_sb, a.expert_sb, 16, tile_row, ls + 16 * SP);
+                ee = __builtin_amdgcn_readlane(ids_lane, g < total ? s0 + slot : 0);
+                if ((unsigned)ee >= (unsigned)a.E) ee = 0, size = 0;           // reads zeros
             }
-            __syncthreads();
+            const uint32_t so = g < total ? 128u * u : kXPast;
+#pragma unroll
+            for (int h = 0; h < H; ++h) {                                      // (nt: read once)
+                const __amdgpu_buffer_rsrc_t rc = buffer_rsrc((h ? a.codes2 : a.codes) + ee * a.expert_cb, size);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) R[h][k] = __builtin_amdgcn_raw_buffer_load_b128(rc, oc[k] + so, 0, 2);
+            }
+        };
+        auto stage_s = [&](const uint8_t *base, long long bytes, int rows, auto row_of, uint8_t *dst) {
+            const uintptr_t p0 = (uintptr_t)base;
+            const __amdgpu_buffer_rsrc_t r =
+                buffer_rsrc((const void *)(p0 & ~(uintptr_t)3), ((long long)(p0 & 3) + bytes + 3) & ~3ll);
+            for (int t = tid; t < rows * J; t += 64 * NW) {
+                const int row = t / J, j = t - row * J;
+                const uint32_t o = (uint32_t)(p0 & 3) + row_of(row) * rsb + 16u * j;
+                *(u32x4 *)(dst + row * SP + 16 * j) = seg_order<true>(load_seg<true>(r, o), o, U - 16 * j);
+            }
+        };
+        auto tile_row = [&](int row) { return (uint32_t)min(row0 + row, N - 1); };
+#pragma unroll
+        for (int i = 0; i < D; ++i) load_a(i, A[i]);
+        // the vectors (MODE 2: those of the group's slots)
+        const int vecs = MODE == 2 ? (a.x_per_slot ? ns : 1) : nv;
+        for (int t = tid; t < vecs * 8 * NU; t += 64 * NW) {
+            const int v = t / (8 * NU), b = t - v * 8 * NU;
+            const uint32_t o = vec_row(MODE == 2 ? s0 + v : v) * (uint32_t)a.x_vec_bytes + 16u * b;
+            *(u32x4 *)(lx + v * XP + 16 * b) =
+                __builtin_amdgcn_raw_buffer_load_b128(rx, b < U ? o : kXPast, 0, 0);
+        }
+        stage_s((const uint8_t *)a.xs, (long long)x_rows * rsb, vecs,
+                [&](int v) { return vec_row(MODE == 2 ? s0 + v : v); }, lxs);
+        if constexpr (MODE == 2) {
+            for (int k = 0; k < ns; ++k) {
+                int ee = __builtin_amdgcn_readlane(ids_lane, s0 + k);
+                if ((unsigned)ee >= (unsigned)a.E) ee = 0;                     // (unused)
+                stage_s(a.scales + ee * a.expert_sb, a.expert_sb, 16, tile_row, ls + k * 16 * SP);
+            }
+        } else {
+            stage_s(a.scales + e * a.expert_sb, a.expert_sb, 16, tile_row, ls);
+            if constexpr (H == 2) stage_s(a.scales2 + e * a.expert_sb, a.expert_sb, 16, tile_row, ls + 16 * SP);
+        }
+        __syncthreads();
 
-            f32x4 acc[H];
+        f32x4 acc[H];
 #pragma unroll
-            for (int h = 0; h < H; ++h) acc[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-            const int wst = swz_chunk(lr, lc), rd = c * 128 + 16 * (q ^ ((c >> 1) & 7));
-            const int vc = MODE == 2 ? 0 : (c < nv ? c : vmask);
-            const int mine = total > w ? (total - w + NW - 1) / NW : 0;            // this wave's units
-            for (int i0 = 0; i0 < mine; i0 += D) {
+        for (int h = 0; h < H; ++h) acc[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        const int wst = swz_chunk(lr, lc), rd = c * 128 + 16 * (q ^ ((c >> 1) & 7));
+        const int vc = MODE == 2 ? 0 : (c < nv ? c : vmask);
+        const int mine = total > w ? (total - w + NW - 1) / NW : 0;            // this wave's units
+        for (int i0 = 0; i0 < mine; i0 += D) {
 #pragma unroll
-                for (int d = 0; d < D; ++d) {
-                    const int i = i0 + d;
-                    if (i < mine) {
-                        const int g = w + NW * i;
-                        const int slot = MODE == 2 ? g / NU : 0, u = g - slot * NU;
-                        const int v = MODE == 2 ? (a.x_per_slot ? slot : 0) : vc;
-                        // slab u / 2's bytes of this unit's two steps in bits 0-15
-                        const int sh = 16 * (u & 1), so = 16 * (u >> 1) + 4 * q;
-                        const uint32_t tb = *(const uint32_t *)(lxs + v * SP + so) >> sh;
-                        const u32x4 B0 = *(const u32x4 *)(lx + v * XP + 128 * u + 16 * q);
-                        const u32x4 B1 = *(const u32x4 *)(lx + v * XP + 128 * u + 64 + 16 * q);
+            for (int d = 0; d < D; ++d) {
+                const int i = i0 + d;
+                if (i < mine) {
+                    const int g = w + NW * i;
+                    const int slot = MODE == 2 ? g / NU : 0, u = g - slot * NU;
+                    const int v = MODE == 2 ? (a.x_per_slot ? slot : 0) : vc;
+                    // slab u / 2's bytes of this unit's two steps in bits 0-15
+                    const int sh = 16 * (u & 1), so = 16 * (u >> 1) + 4 * q;
+                    const uint32_t tb = *(const uint32_t *)(lxs + v * SP + so) >> sh;
+                    const u32x4 B0 = *(const u32x4 *)(lx + v * XP + 128 * u + 16 * q);
+                    const u32x4 B1 = *(const u32x4 *)(lx + v * XP + 128 * u + 64 + 16 * q);
 #pragma unroll
-                        for (int h = 0; h < H; ++h) {
-                            *(u32x4 *)(la + h * 2048 + wst) = A[d][h][0];
-                            *(u32x4 *)(la + h * 2048 + 1024 + (wst ^ 64)) = A[d][h][1];
-                        }
-                        asm volatile("" ::: "memory");                             // (written before read: one wave's LDS)
-                        load_a(i + D, A[d]);
+                    for (int h = 0; h < H; ++h) {
+                        *(u32x4 *)(la + h * 2048 + wst) = A[d][h][0];
+                        *(u32x4 *)(la + h * 2048 + 1024 + (wst ^ 64)) = A[d][h][1];
+                    }
+                    asm volatile("" ::: "memory");                             // (written before read: one wave's LDS)
+                    load_a(i + D, A[d]);
 #pragma unroll
-                        for (int h = 0; h < H; ++h) {
-                            const uint32_t ta =
-                                *(const uint32_t *)(ls + ((MODE == 2 ? slot : h) * 16 + c) * SP + so) >> sh;
-                            const u32x4 F0 = *(const u32x4 *)(la + h * 2048 + rd);
-                            const u32x4 F1 = *(const u32x4 *)(la + h * 2048 + (rd ^ 64));
-                            acc[h] = mfma_mx4_op<0>(F0, B0, acc[h], ta, tb);
-                            acc[h] = mfma_mx4_op<1>(F1, B1, acc[h], ta, tb);
-                        }
-                        asm volatile("" ::: "memory");
-                        if constexpr (MODE == 2) {
-                            if ((g + NW) / NU != slot || i + 1 == mine) {          // this wave's last unit of the slot
-                                const float rw = __uint_as_float(
-                                    __builtin_amdgcn_readlane(__float_as_uint(rw_lane), s0 + slot));
-                                // (a slot without an expert is 0 whatever scales
-                                // its vector has; zero codes times NaN are not)
-                                const bool have = (unsigned)__builtin_amdgcn_readlane(ids_lane, s0 + slot) < (unsigned)a.E;
+                    for (int h = 0; h < H; ++h) {
+                        const uint32_t ta =
+                            *(const uint32_t *)(ls + ((MODE == 2 ? slot : h) * 16 + c) * SP + so) >> sh;
+                        const u32x4 F0 = *(const u32x4 *)(la + h * 2048 + rd);
+                        const u32x4 F1 = *(const u32x4 *)(la + h * 2048 + (rd ^ 64));
+                        acc[h] = mfma_mx4_op<0>(F0, B0, acc[h], ta, tb);
+                        acc[h] = mfma_mx4_op<1>(F1, B1, acc[h], ta, tb);
+                    }
+                    asm volatile("" ::: "memory");
+                    if constexpr (MODE == 2) {
+                        if ((g + NW) / NU != slot || i + 1 == mine) {          // this wave's last unit of the slot
+                            const float rw = __uint_as_float(
+                                __builtin_amdgcn_readlane(__float_as_uint(rw_lane), s0 + slot));
+                            // (a slot without an expert is 0 whatever scales
+                            // its vector has; zero codes times NaN are not)
+                            const bool have = (unsigned)__builtin_amdgcn_readlane(ids_lane, s0 + slot) < (unsigned)a.E;
 #pragma unroll
-                                for (int k = 0; k < 4; ++k) tot[k] = __builtin_fmaf(rw, have ? acc[0][k] : 0.0f, tot[k]);
-                                acc[0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-                            }
+                            for (int k = 0; k < 4; ++k) tot[k] = __builtin_fmaf(rw, have ? acc[0][k] : 0.0f, tot[k]);
+                            acc[0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
                         }
                     }
                 }
             }
-            if constexpr (MODE == 2) {
-                if (s0 + per < slots) {
-                    __syncthreads();                           // (the next group's staging)
-                    continue;
-                }
-                acc[0] = tot;
+        }
+        if constexpr (MODE == 2) {
+            if (s0 + per < slots) {
+                __syncthreads();                           // (the next group's staging)
+                continue;
             }
+            acc[0] = tot;
+        }
 #pragma unroll
-            for (int h = 0; h < H; ++h) *(f32x4 *)(la + h * 2048 + 16 * lane) = acc[h];
-            __syncthreads();
-            // lane (c, q): rows 4 q .. 4 q + 3 of vector c, summed over the waves
-            if (w == 0 && c < nv) {
-                f32x4 r[H];
+        for (int h = 0; h < H; ++h) *(f32x4 *)(la + h * 2048 + 16 * lane) = acc[h];
+        __syncthreads();
+        // lane (c, q): rows 4 q .. 4 q + 3 of vector c, summed over the waves
+        if (w == 0 && c < nv) {
+            f32x4 r[H];
 #pragma unroll
-                for (int h = 0; h < H; ++h) {
-                    r[h] = acc[h];
+            for (int h = 0; h < H; ++h) {
+                r[h] = acc[h];
 #pragma unroll
-                    for (int i = 1; i < NW; ++i) r[h] += *(const f32x4 *)(la + (i * H + h) * 2048 + 16 * lane);
-                }
-                float *const yr = a.y + (size_t)(MODE == 2 ? (int)blockIdx.y : pair_of(c)) * N;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int n = row0 + 4 * q + k;
-                    if (n < N) yr[n] = MODE == 1 ? swiglu(r[0][k], r[H - 1][k]) : r[0][k];
-                }
+                for (int i = 1; i < NW; ++i) r[h] += *(const f32x4 *)(la + (i * H + h) * 2048 + 16 * lane);
             }
-            if (rt + 1 < rt1) __syncthreads();                 // (the next tile's pieces and scales)
+            float *const yr = a.y + (size_t)(MODE == 2 ? (int)blockIdx.y : pair_of(c)) * N;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int n = row0 + 4 * q + k;
+                if (n < N) yr[n] = MODE == 1 ? swiglu(r[0][k], r[H - 1][k]) : r[0][k];
+            }
         }
     }
 }

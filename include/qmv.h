@@ -188,9 +188,10 @@ qmv_status_t qmv_dense(qmv_wfmt_t wfmt, const void *w_codes, const void *w_scale
  *     while staged), each workgroup a run of (expert, row tile) items of
  *     equal cost with the experts' vector counts weighed in;
  *   (MXFP4, MXFP4): an expert's vectors in equal chunks, each chunk reading
- *     the expert's rows once, on the block-scaled matrix cores; chunks of up
- *     to 16 with M * top_k < 2 E (with M <= 4 too), else of up to 64, or 128
- *     from 48 pairs an expert on where K leaves the LDS for them;
+ *     the expert's rows once, on the block-scaled matrix cores (with M <= 4
+ *     too); chunks of up to 16 while 16 rows a workgroup do not fill the chip,
+ *     else of up to 64, or 128 from 48 pairs an expert on where K leaves the
+ *     LDS for them;
  *   at most 64 tokens with fewer than two pairs per expert: groups of up to
  *     4 tokens on the decode kernels, one launch per group;
  *   every other call: the decode kernels' own multiply-adds in one launch,

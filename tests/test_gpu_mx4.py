@@ -72,7 +72,8 @@ GATHER = [(1, 1, 1, 5, 32), (1, 32, 4, 70, 2880), (2, 8, 3, 33, 96), (4, 40, 8, 
           (5, 64, 2, 50, 160), (6, 3, 2, 65, 544), (37, 8, 4, 130, 288), (64, 200, 4, 20, 128), (100, 4, 4, 96, 1024),
           (16, 1023, 2, 9, 64), (512, 16, 4, 40, 96), (1, 2000, 16, 24, 256), (4, 70000, 2, 3, 32),
           (70, 1, 3, 200, 320), (129, 2, 2, 40, 2880), (65, 1, 1, 130, 3584), (300, 3, 2, 33, 3616),
-         (1000, 8, 2, 20, 64), (96, 2, 1, 129, 1504)]
+         (1000, 8, 2, 20, 64), (96, 2, 1, 129, 1504), (4, 30, 8, 1000, 288), (3, 1023, 16, 700, 160),
+         (2, 1024, 16, 1000, 64), (9, 5, 3, 2000, 96), (60, 40, 2, 300, 1056)]
 
 
 @pytest.mark.parametrize("M,E,top_k,N,K", GATHER)
@@ -94,7 +95,8 @@ def test_gather(M, E, top_k, N, K, per_slot):
 
 SWIGLU = [(1, 32, 4, 70, 2880), (4, 6, 2, 33, 96), (5, 64, 2, 50, 160), (37, 8, 4, 130, 288), (150, 4, 4, 96, 1024),
           (3, 300, 8, 17, 64), (2, 1, 1, 5, 32), (300, 2, 2, 70, 544), (129, 2, 2, 40, 2880), (65, 1, 1, 66, 3584),
-          (200, 3, 2, 33, 3616), (4, 1100, 16, 3, 16384), (4, 2, 16, 20, 16384), (1, 1500, 15, 5, 15392)]
+          (200, 3, 2, 33, 3616), (4, 1100, 16, 3, 16384), (4, 2, 16, 20, 16384), (1, 1500, 15, 5, 15392), (4, 30, 8, 600, 288), (2, 1024, 16, 500, 64),
+          (9, 5, 3, 1000, 96)]
 
 
 @pytest.mark.parametrize("M,E,top_k,N,K", SWIGLU)
