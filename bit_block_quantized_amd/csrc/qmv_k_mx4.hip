@@ -30,8 +30,8 @@ __device__ __forceinline__ f32x4 mfma_mx4_op(u32x4 a, u32x4 b, f32x4 c, uint32_t
 }
 
 // ------------------------------------------------------------- many vectors
-// A tile is (expert, 128 weight rows) against a chunk of its vectors, 4 waves
-// of 2 x CF fragments each (RF = 2).  K goes in slabs of 512 weights (4 MFMA
+// A tile is (expert, 128 weight rows; gate/up: 64 of each) against a chunk of
+// its vectors (up to 64 or 128), 4 waves of 2 x CF fragments each (RF = 2).  K goes in slabs of 512 weights (4 MFMA
 // steps) of two units (2 steps, 128 code bytes a row).
 //
 // The MFMA wants lane (c, q) = lane 16 q + c to hold 16 bytes of row c, but a
@@ -50,6 +50,12 @@ __device__ __forceinline__ f32x4 mfma_mx4_op(u32x4 a, u32x4 b, f32x4 c, uint32_t
 //                       transposed so that lane (c, q) reads its four steps'
 //                       bytes as one dword, which the instruction indexes
 // One barrier per unit; two workgroups of 4 waves share a CU.
+//
+// Bound by the weight stream: 1024 tokens x top-8 of 256, 7168 -> 2048, reads
+// 2.0 GB in 375 us (5.5 TB/s of the 6.3 that default-policy loads reach).  Short
+// rows leave more of a tile's time to its start (the ids' counts, the vector
+// list, the scales): 512 tokens x top-4 of 32, gate/up 2880 -> 2880, 282 MB in
+// 92 us, 3.1 TB/s (nontemporal loads of the codes: 104 us).
 __device__ __forceinline__ int swz_chunk(int row, int chunk) { return row * 128 + 16 * (chunk ^ ((row >> 1) & 7)); }
 
 // A row's 16 scale bytes of a slab as loaded: five whole dwords around them.
@@ -559,7 +565,10 @@ __global__ __launch_bounds__(64 * kMx4Waves, 2) void qmv_mx4_tile_kernel(const A
 // ... -- and each has up to kFewAhead units of its rows on their way from the
 // start; the vectors and the scale bytes are staged in LDS once.  The waves'
 // partial tiles are summed in wave order.  Columns past the last vector
-// repeat one (nothing of them is stored).
+// repeat one (nothing of them is stored).  One token's top-4 of 32, 2880 ->
+// 2880: 6.8 us for 18 MB (2.6 TB/s: 720 workgroups of a few loads each, most
+// of it the way from the ids to the first codes); the combine of 4 tokens x 8,
+// 2048 -> 7168: 49 us for 250 MB, 5.1 TB/s.
 constexpr int kFewAhead = 4;
 
 // Bytes from vector to vector of the staged codes: whole units, and 16 more

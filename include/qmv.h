@@ -72,7 +72,9 @@
  *                    run on the block-scaled matrix cores, sums in fp32 (an
  *                    output one of whose blocks sums to 2^128 or more need not
  *                    be finite); a NaN scale (255) of either side makes the
- *                    outputs of its row or vector NaN.
+ *                    outputs of its row or vector NaN.  (E8M0 arrays are read
+ *                    in whole aligned 4-byte words: up to 3 bytes before the
+ *                    first and behind the last byte are read with them.)
  * Supported pairs: (MXFP4, BF16), (MXFP4, Q8B32), (MXFP4, MXFP4),
  * (CB2, Q8B32), (CB3, Q8B32), (CB2, BF16_Q8), (CB3, BF16_Q8).  With
  * (MXFP4, Q8B32) every 32-weight block shares one E8M0 weight scale and one activation scale (both are per 32 of

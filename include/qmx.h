@@ -90,7 +90,8 @@ qmv_status_t qmx_rmsnorm(qmx_type_t xtype, const void *x, qmx_type_t rtype, cons
  *   QMX_SIGMOID  w_j = 1 / (1 + exp(-l_j)), divided by their sum over the
  *                chosen experts with normalize
  * times `scale`.  A logit of -infinity or NaN masks its expert: it is never
- * chosen and adds nothing to a sum.  A token with fewer than top_k unmasked
+ * chosen and adds nothing to a sum; +infinity is chosen first, and makes the
+ * softmax weights NaN.  A token with fewer than top_k unmasked
  * experts gets id -1 and weight 0 in its last slots (the gathers write zero
  * rows for such ids).
  *   logits  ltype (QMX_T_F32 or QMX_T_BF16) [M][E]

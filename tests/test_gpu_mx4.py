@@ -353,3 +353,60 @@ def test_many_pairs_of_one_expert_among_few_pairs(M, top_k, E):
         y = q.qmv_gather_moe("mxfp4", dev(wc), dev(ws), dev(ids), dev(xc), dev(xs), y=out)
         want, A = R.gather(ids, R.values(wc, ws), R.values(xc, xs), False)
         close(y, want, K * U * A, f"one expert {M} {top_k}")
+
+
+def test_dense_and_gate_up_replayed_and_on_two_streams_at_once():
+    """Every kernel (few vectors, tiles of 64 and of 128, wide tiles): bit for
+    bit the eager call's, under graph replays and beside each other on two
+    streams."""
+    rng = np.random.default_rng(3)
+    K = 544
+    dense = []
+    for M, N in ((3, 100), (70, 12400), (1100, 6600)):
+        wc, ws = (dev(a) for a in make(rng, (N,), K))
+        xc, xs = (dev(a) for a in make(rng, (M,), K))
+        dense.append((wc, ws, xc, xs, torch.empty(M, N, device="cuda")))
+    routed = []
+    for M, E, top_k, N in ((2, 8, 2, 96), (40, 4, 2, 1000), (150, 4, 2, 1000)):
+        gu = [dev(a) for _ in range(2) for a in make(rng, (E, N), K)]
+        xc, xs = (dev(a) for a in make(rng, (M,), K))
+        routed.append((*gu, dev(make_ids(rng, M, top_k, E)), xc, xs, torch.empty(M, top_k, N, device="cuda")))
+
+    def call():
+        for *a, y in dense:
+            q.qmv_dense("mxfp4", *a, y=y)
+        for *a, y in routed:
+            q.qmv_gather_moe_swiglu("mxfp4", *a, y=y)
+
+    outs = [t[-1] for t in dense + routed]
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for k in range(3):
+        for t in dense + routed:
+            for x in t[-3:-1]:                                   # other codes and scales of the vectors
+                x.copy_(x.flip(0))
+        call()
+        torch.cuda.synchronize()
+        eager = [y.clone() for y in outs]
+        for y in outs:
+            y.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(y, e) for y, e in zip(outs, eager)), k
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for i, st in enumerate(streams):
+        st.wait_stream(torch.cuda.current_stream())
+    for _ in range(3):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got[i].append([q.qmv_dense("mxfp4", *a) for *a, _ in dense] +
+                              [q.qmv_gather_moe_swiglu("mxfp4", *a) for *a, _ in routed])
+    for st in streams:
+        st.synchronize()
+    for rounds in got:
+        for r in rounds:
+            assert all(torch.equal(y, e) for y, e in zip(r, eager))

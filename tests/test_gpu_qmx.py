@@ -62,6 +62,13 @@ def test_rmsnorm_sizes(M, K, fmt):
 
 
 @pytest.mark.parametrize("fmt", ["bf16", "q8", "mxfp4"])
+@pytest.mark.parametrize("M,K", [(1024, 2080), (1030, 4096), (1023, 2880)])
+def test_rmsnorm_many_rows(M, K, fmt):
+    rng = np.random.default_rng(M + K)
+    check_norm(rand(rng, (M, K), "bf16", 3.0), rand(rng, (K,), "bf16"), rand(rng, (M, K), "f32", 20.0), fmt)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "q8", "mxfp4"])
 @pytest.mark.parametrize("xt", list(TYPES))
 @pytest.mark.parametrize("rt", [None, "f32", "bf16", "f16"])
 def test_rmsnorm_types(xt, rt, fmt):
