@@ -618,28 +618,31 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
     const int xp = (U + 7) / 8 * 128 + 16, sp = 16 * (J | 1);
     auto few_lds = [&](int vectors) { return 64 + 4 * h * 2048 + (size_t)vectors * (xp + sp) + (size_t)h * 16 * sp; };
     int most = pairs < 16 ? pairs : 16;
-    // 256 x 256 tiles once they fill half of the chip and more than half of
-    // their vectors exist (us, against the tile kernel's 128 x 64: 56 tiles 60
-    // and 38; 96 60 and 59, 33 and 32; 108 33 and 28; 112 63 and 74, 26 and 29;
-    // 192 36 and 50; 224 70 and 136; 896 275 and 493.  2880 -> 201088: 64 vectors
-    // 131 and 93, 128 148 and 146, 192 168 and 242; 7168 -> 40960: 128 66 and 57,
-    // 192 70 and 80)
+    // 256 x 256 tiles (or halves of them) once there are more than one for four
+    // CUs and more than half of their vectors exist (us, against the tile
+    // kernel's 128 x 64: 56 tiles 42 and 38; 64 41 and 42, 41 and 40, 41 and 31;
+    // 80 43 and 55; 96 24 and 32, 44 and 45; 112 44 and 71; 224 66 and 131; 896
+    // 241 and 493.  2880 -> 201088: 64 vectors 131 and 93, 128 148 and 146, 256
+    // 171 and 268; 7168 -> 40960: 128 66 and 57, 192 59 and 73)
     const long long wide_tiles = (long long)((N + 255) / 256) * ((M + 255) / 256);
-    if (!gather && mode == 0 && M > 128 && 2 * wide_tiles >= cu_count()) {
+    if (!gather && mode == 0 && M > 128 && 4 * wide_tiles > cu_count()) {
         const int lds = 4 * 256 * 128 + 4 * 256 * 16;
         a.bt_row_tiles = (N + 255) / 256;
         a.bt_vmax = 4;
         a.bt_tiles = (int)wide_tiles;
         a.bt_per_xcd = (a.bt_tiles + 7) / 8;
+        // a last round that fills at most half of an XCD's CUs is dealt as half
+        // tiles (896 tiles 241 us, 270 without; 112 tiles 44 and 63)
+        const int cus = cu_count() / 8, rest = cus > 0 ? a.bt_per_xcd % cus : 0, halves = 2 * rest <= cus ? rest : 0;
+        a.bt_chunk = a.bt_per_xcd - halves;
         std::call_once(g_mx4_wide_once, [&] {
             g_mx4_wide_err = hipFuncSetAttribute(kTableMx4Wide[0], hipFuncAttributeMaxDynamicSharedMemorySize, lds);
         });
         if (g_mx4_wide_err != hipSuccess)
             return QMV_EHIP;
         void *kargs[] = {&a};
-        return hipLaunchKernel(kTableMx4Wide[0], dim3((unsigned)(8 * a.bt_per_xcd)), dim3(512), kargs, lds, stream) == hipSuccess
-                   ? QMV_OK
-                   : QMV_EHIP;
+        return hipLaunchKernel(kTableMx4Wide[0], dim3((unsigned)(8 * (a.bt_per_xcd + halves))), dim3(512), kargs, lds,
+                               stream) == hipSuccess ? QMV_OK : QMV_EHIP;
     }
     // Few vectors: workgroups of 16 rows while the chip is not full of them.
     // Dense, one per 16 vectors, until there are three per CU (us, against the

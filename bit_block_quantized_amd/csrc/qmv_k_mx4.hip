@@ -809,32 +809,26 @@ __global__ __launch_bounds__(64 * kMx4Waves) void qmv_mx4_few_kernel(const Args 
 // fragment as soon as its last product of the step is given out, so a step
 // enters with its operands read.  One barrier a unit, in the middle of its
 // second step, where every fragment of the unit is read.
-// 8192 vectors, 7168 -> 7168: 275 us, 3.06 PFLOP/s (128 x 128 tiles of 4 waves
-// 398, the tile kernel's 128 x 64 493).  Half a round of its 3.5 rounds of
-// workgroups is lost at the end; all-zero operands take 227 us, which the
-// chip's power limit explains (2.1 GHz against 2.4).  With zero operands the
-// products alone take 145 us, LDS reads add 20, the staging stores 30, the
+// 8192 vectors, 7168 -> 7168: 241 us, 3.5 PFLOP/s (270 with the last half round
+// of its 3.5 done in whole tiles, 398 in 128 x 128 tiles of 4 waves, 493 in the
+// tile kernel's 128 x 64).  Measured with whole tiles: all-zero operands take
+// 227 us, which the chip's power limit explains (2.1 GHz against 2.4); of them
+// the products alone take 145, LDS reads add 20, the staging stores 30, the
 // loads 30; loads two steps ahead, or written between other products, change
 // nothing.
-__global__ __launch_bounds__(512, 2) void qmv_mx4_wide_kernel(const Args a)
+// RF: 16-row fragments per wave; the tile starts at row0 and vec0.
+template <int RF>
+__device__ __forceinline__ void mx4_wide_tile(const Args &a, uint8_t *lds, int row0, int vec0)
 {
-    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    constexpr int RF = 4, CF = 8, NWR = 4, NWC = 2, NW = NWR * NWC;
+    constexpr int CF = 8, NWR = 4, NWC = 2, NW = NWR * NWC;
     constexpr int BR = 16 * RF * NWR, BC = 16 * CF * NWC;   // tile: rows, vectors
     constexpr int AB = BR * 128, XB = BC * 128;       // bytes of a unit's codes
-    constexpr int NS = BR + BC;                       // staged scale rows, one a thread
+    constexpr int NS = BR + BC;                       // staged scale rows, at most one a thread
     constexpr int KA = BR / 8 / NW, KX = BC / 8 / NW; // staged pieces (8 rows x 128 bytes) per wave and unit
     constexpr int GB = CF / 2;                        // column fragments read at a time
-    static_assert(NS == 64 * NW && BR % 64 == 0 && KA % 2 == 0 && KX % 2 == 0 && NW % 2 == 0, "staging split");
+    static_assert(NS <= 64 * NW && BR % 64 == 0 && KA % 2 == 0 && KX % 2 == 0 && NW % 2 == 0, "staging split");
     uint8_t *const ld = lds;                          // [2][AB + XB]
     uint8_t *const ls = lds + 2 * (AB + XB);          // [2][NS] x 16 bytes
-    // groups of bt_vmax vector chunks, chunk-fastest inside, dealt to the XCDs
-    // in contiguous parts: the tiles an XCD runs at a time share both operands
-    const int tile = (blockIdx.x & 7) * a.bt_per_xcd + (blockIdx.x >> 3);
-    if (tile >= a.bt_tiles) return;
-    const int chunks = (a.M + BC - 1) / BC, group = a.bt_vmax * a.bt_row_tiles;
-    const int gi = tile / group, in = tile - gi * group, gw = min(a.bt_vmax, chunks - gi * a.bt_vmax);
-    const int row0 = in / gw * BR, vec0 = (gi * a.bt_vmax + in % gw) * BC;
 
     const int tid = threadIdx.x, lane = tid & 63;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -887,7 +881,9 @@ __global__ __launch_bounds__(512, 2) void qmv_mx4_wide_kernel(const Args a)
         (const void *)(p0 & ~(uintptr_t)3), ((long long)(p0 & 3) + (long long)(vecs ? a.M : a.N) * a.rsb + 3) & ~3ll);
     const uint32_t os = (uint32_t)(p0 & 3) +
                         (uint32_t)(vecs ? min(vec0 + tid - BR, a.M - 1) : min(row0 + tid, a.N - 1)) * (uint32_t)a.rsb;
-    auto put_s = [&](int j, u32x4 v) { *(u32x4 *)(ls + (j & 1) * (NS * 16) + tid * 16) = v; };
+    auto put_s = [&](int j, u32x4 v) {
+        if (NS == 64 * NW || tid < NS) *(u32x4 *)(ls + (j & 1) * (NS * 16) + tid * 16) = v;
+    };
     const int rd = c * 128 + 16 * (q ^ ((c >> 1) & 7));
 
     u32x4 F[RF], B[2][GB];                            // fragments: rows; two groups of vectors
@@ -1007,6 +1003,25 @@ __global__ __launch_bounds__(512, 2) void qmv_mx4_wide_kernel(const Args a)
             }
         }
     }
+}
+
+// The tiles lie in groups of bt_vmax vector chunks, chunk-fastest inside, and
+// are dealt to the XCDs in contiguous parts: the tiles an XCD runs at a time
+// share both operands.  Of an XCD's bt_per_xcd tiles all from bt_chunk on are
+// done as two halves of 128 rows.
+__global__ __launch_bounds__(512, 2) void qmv_mx4_wide_kernel(const Args a)
+{
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const int i = blockIdx.x >> 3, half = i - a.bt_chunk;
+    const int tile = (blockIdx.x & 7) * a.bt_per_xcd + (half < 0 ? i : a.bt_chunk + half / 2);
+    if (tile >= a.bt_tiles) return;
+    const int chunks = (a.M + 255) / 256, group = a.bt_vmax * a.bt_row_tiles;
+    const int gi = tile / group, in = tile - gi * group, gw = min(a.bt_vmax, chunks - gi * a.bt_vmax);
+    const int row0 = in / gw * 256, vec0 = (gi * a.bt_vmax + in % gw) * 256;
+    if (half < 0)
+        mx4_wide_tile<4>(a, lds, row0, vec0);
+    else if (row0 + 128 * (half & 1) < a.N)
+        mx4_wide_tile<2>(a, lds, row0 + 128 * (half & 1), vec0);
 }
 
 extern const void *const kTableMx4Wide[1];

@@ -158,7 +158,7 @@ typedef enum {
  * weights with int8 (or in-kernel quantized bf16) activations and M >= 8 on
  * the int8 matrix-core kernel; (MXFP4, MXFP4) with any M on the block-scaled
  * matrix cores (16 rows and 16 vectors a workgroup with K split over its
- * waves, 128 x 64 tiles, or 256 x 256 tiles once they fill half of the chip);
+ * waves, 128 x 64 tiles, or 256 x 256 tiles for many);
  * every other M > 4 call on the grouped kernel.
  */
 qmv_status_t qmv_dense(qmv_wfmt_t wfmt, const void *w_codes, const void *w_scales,

@@ -55,7 +55,8 @@ DENSE = [(1, 1, 32), (1, 17, 64), (1, 2880, 2880), (2, 33, 96), (4, 64, 544), (5
 DENSE += [(600, 130, 2880), (520, 70, 32), (777, 260, 544), (512, 256, 1536), (1100, 515, 1056), (2049, 300, 128),
           (4100, 33, 96), (2050, 3600, 32), (1900, 4097, 160), (4100, 2050, 544), (2049, 3850, 1056), (8192, 900, 96),
           (1025, 7001, 512), (17, 12400, 64), (70, 2900, 96), (200, 1100, 544), (96, 2700, 2880), (33, 5000, 1056),
-          (1, 33000, 96), (4, 12320, 64), (5, 12320, 64), (16, 13000, 160), (128, 16500, 64), (129, 16400, 96)]
+          (1, 33000, 96), (4, 12320, 64), (5, 12320, 64), (16, 13000, 160), (128, 16500, 64), (129, 16400, 96),
+          (600, 7000, 544), (700, 7041, 96), (257, 16600, 1056), (4100, 4200, 64), (2300, 7500, 32)]
 
 
 @pytest.mark.parametrize("M,N,K", DENSE)
