@@ -673,7 +673,8 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
         // runs of row tiles: about 8 workgroups for each that the chip holds at
         // a time (fewer, longer runs scan the ids less often but end unevenly:
         // 1024 tokens x top-8 of 256, 7168 -> 2048: 570 us at 1, 417 at 4, 376
-        // at 8; 512 x top-4 of 32, gate/up 2880 -> 2880: 110, 112, 112 us)
+        // at 8; 512 x top-4 of 32, gate/up 2880 -> 2880, chunks of 64: 110, 112,
+        // 112 us)
         const int lds = mx4_tile_lds(K, chunk);
         const long long slots = (long long)cu_count() * (lds * 2 <= kLdsPerCU ? 2 : 1);
         const long long run = items * a.bt_row_tiles / (8 * slots);

@@ -73,8 +73,9 @@ struct Args {
     int bt_row_tiles;        // row tiles per expert
     int bt_tiles;            // tiles in the call
     int bt_per_xcd;          // tiles per XCD (ceil(bt_tiles / 8))
-    int bt_chunk;            // dense: vectors per tile
-    int bt_vmax;             // vectors the activation ring holds (32, 64 or 128)
+    int bt_chunk;            // dense: vectors per tile; MXFP4 x MXFP4: row tiles per run, or whole tiles per XCD
+    int bt_vmax;             // vectors the activation ring holds (32, 64 or 128); MXFP4 x MXFP4: vectors
+                             // or slots staged at a time, or vector tiles of a group
     // grouped kernel: work items (expert slot, row tile), slot-major
     int gr_tiles;            // row tiles per expert
 };

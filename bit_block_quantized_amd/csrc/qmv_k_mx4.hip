@@ -816,6 +816,7 @@ __global__ __launch_bounds__(64 * kMx4Waves) void qmv_mx4_few_kernel(const Args 
 // the products alone take 145, LDS reads add 20, the staging stores 30, the
 // loads 30; loads two steps ahead, or written between other products, change
 // nothing.
+//
 // RF: 16-row fragments per wave; the tile starts at row0 and vec0.
 template <int RF>
 __device__ __forceinline__ void mx4_wide_tile(const Args &a, uint8_t *lds, int row0, int vec0)
