@@ -30,7 +30,7 @@ for line in sys.stdin:
     rec.rec_clear()
     fn = next(getattr(l, name) for l in libs if hasattr(l, name))
     put = [ctypes.c_void_p(None) if a is None else ctypes.c_void_p(int(a[1:])) if isinstance(a, str) else
-           ctypes.c_float(a) if isinstance(a, float) else ctypes.c_int(a) for a in args]
+           ctypes.c_float(a) if isinstance(a, float) else ctypes.c_longlong(a) for a in args]
     print(json.dumps([fn(*put), rec.rec_lines().decode()]), flush=True)
 """
 
