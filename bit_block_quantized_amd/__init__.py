@@ -238,6 +238,12 @@ def _per_slot(x, x_per_slot, M, top_k):
     return x_per_slot
 
 
+def _ints(*sizes):
+    """The C ABI takes these as int; ctypes would cut them to 32 bits."""
+    if max(sizes) >= 1 << 31:
+        raise ValueError(f"a size of {max(sizes)} is not below 2^31")
+
+
 def _gpu(dev, fn):
     if dev.type != "cuda":
         raise ValueError(f"{fn} runs on the GPU only; pass device tensors")
@@ -252,6 +258,7 @@ def qmv_dense(wfmt, w_codes, w_scales, x, x_scales=None, y=None, stream=None):
     M, K = x.shape[0], _k_of(w, x)
     N = w_codes.shape[0]
     a, xd = _afmt(w, x)
+    _ints(M, N, K)
     _check_weights(w, w_codes, w_scales, (N,), K)
     _check_x(x, x_scales, M, K, a)
     if y is not None:
@@ -282,6 +289,7 @@ def qmv_gather_moe(wfmt, w_codes, w_scales, expert_ids, x, x_scales=None, x_per_
     K = _k_of(w, x)
     per_slot = _per_slot(x, x_per_slot, M, top_k)
     a, xd = _afmt(w, x)
+    _ints(M, top_k, E, N, K)
     _check_weights(w, w_codes, w_scales, (E, N), K)
     _check_x(x, x_scales, M * top_k if per_slot else M, K, a)
     if y is not None:
@@ -310,6 +318,7 @@ def qmv_gather_moe_swiglu(wfmt, gate_codes, gate_scales, up_codes, up_scales, ex
     E, N = gate_codes.shape[0], gate_codes.shape[1]
     K = _k_of(w, x)
     a, xd = _afmt(w, x)
+    _ints(M, top_k, E, N, K)
     _check_weights(w, gate_codes, gate_scales, (E, N), K, ("gate_codes", "gate_scales"))
     _check_weights(w, up_codes, up_scales, (E, N), K, ("up_codes", "up_scales"))
     _check_x(x, x_scales, M, K, a)
@@ -367,6 +376,7 @@ def _combine(entry, wfmt, w_codes, w_scales, expert_ids, route_weights, x, x_sca
     K = _k_of(w, x)
     per_slot = _per_slot(x, x_per_slot, M, top_k)
     a, xd = _afmt(w, x)
+    _ints(M, top_k, E, N, K)
     _check_weights(w, w_codes, w_scales, (E, N), K)
     _check_x(x, x_scales, M * top_k if per_slot else M, K, a)
     if y is not None:

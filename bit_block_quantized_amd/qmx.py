@@ -134,6 +134,7 @@ def qmx_rmsnorm(x, weight=None, eps=1e-5, residual=None, fmt="bf16", y=None, y_s
     f = _choice(fmt, _FMT, "fmt")
     _tensor(x, "x", _TYPE)
     M, K = _rows(x, "x")
+    _q._ints(M, K)
     dev, shape = x.device, x.shape
     if fmt != "bf16":
         _blocks(K, "x")
@@ -174,6 +175,7 @@ def qmx_router(logits, top_k, scoring="softmax", normalize=True, scale=1.0, ids=
     if logits.dim() != 2 or logits.numel() < 1:
         raise ValueError(f"logits has shape {tuple(logits.shape)}, expected [M][E]")
     M, E = logits.shape
+    _q._ints(M, E)
     top_k = int(top_k)
     if not 1 <= top_k <= min(16, E):
         raise ValueError(f"top_k is {top_k}, expected 1 to {min(16, E)}")
@@ -193,6 +195,7 @@ def qmx_quantize(x, fmt="mxfp4", codes=None, scales=None, stream=None):
         raise ValueError(f"fmt is {fmt!r}, expected one of ('mxfp4', 'q8')")
     _tensor(x, "x", _TYPE)
     rows, K = _rows(x, "x")
+    _q._ints(K)
     _blocks(K, "x")
     _gpu(x, "qmx_quantize")
     cs, ss = _code_spec(fmt, tuple(x.shape[:-1]), K)
@@ -211,6 +214,7 @@ def qmx_dequantize(codes, scales, fmt="mxfp4", dtype=torch.bfloat16, y=None, str
     _tensor(codes, "codes", (torch.uint8 if fmt == "mxfp4" else torch.int8,))
     rows, n = _rows(codes, "codes")
     K = 2 * n if fmt == "mxfp4" else n
+    _q._ints(K)
     _blocks(K, "codes")
     _, ss = _code_spec(fmt, tuple(codes.shape[:-1]), K)
     _tensor(scales, "scales", (ss[0],), codes.device, ss[1])
