@@ -8,6 +8,7 @@
 #include "qmv_device.hpp"
 #include "qmv.h"
 
+#include <atomic>
 #include <mutex>
 #include <stdint.h>
 
@@ -211,10 +212,30 @@ const void *combine_kernel_for(int wi, int kind, int li, int ci, bool q8)
     }
 }
 
-std::once_flag g_attr_once[2][2][2][5][3][4][5];        // [q8][waves][gate_up][kind][variant][lpr][cpl]
-hipError_t g_attr_err[2][2][2][5][3][4][5];
-std::once_flag g_cattr_once[2][2][5][4][4];             // [q8][waves][kind][lpr][cpl]
-hipError_t g_cattr_err[2][2][5][4][4];
+// The most dynamic LDS that any call may ask of a kernel.  A function
+// attribute belongs to a device: it is set at the kernel's first launch on
+// each (at every launch on a device past the 64th).
+struct LdsLimit {
+    std::atomic<uint64_t> devices{0};    // where it is set
+
+    hipError_t set(const void *fn, long long bytes)
+    {
+        int dev = 0;
+        hipError_t e = hipGetDevice(&dev);
+        if (e != hipSuccess)
+            return e;
+        const uint64_t bit = dev >= 0 && dev < 64 ? 1ull << dev : 0;
+        if (devices.load(std::memory_order_acquire) & bit)
+            return hipSuccess;
+        e = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+        if (e == hipSuccess)
+            devices.fetch_or(bit, std::memory_order_release);
+        return e;
+    }
+};
+
+LdsLimit g_lds[2][2][2][5][3][4][5];                    // [q8][waves][gate_up][kind][variant][lpr][cpl]
+LdsLimit g_comb_lds[2][2][5][4][4];                     // [q8][waves][kind][lpr][cpl]
 
 // Arguments common to every kernel of a call (Args in qmv_device.hpp).
 Args base_args(int wfmt, int afmt, int kind, const void *codes, const void *scales, int E,
@@ -258,8 +279,7 @@ size_t batched_lds(int vmax, int pairs)
     return (size_t)2 * vmax * 256 + kPairCountBytes + (((size_t)2 * pairs + 15) & ~(size_t)15);
 }
 
-std::once_flag g_b_once[2][kBatchedMenu];
-hipError_t g_b_err[2][kBatchedMenu];
+LdsLimit g_b_lds[2][kBatchedMenu];
 
 int g_cu_count[64];
 std::once_flag g_cu_once[64];
@@ -351,11 +371,7 @@ qmv_status_t launch_batched(const void *codes, const void *scales, const void *c
     a.bt_vmax = vmost <= 32 ? 32 : vmost <= 64 ? 64 : vmost <= 96 ? 96 : 128;
     const int gu = gate_up ? 1 : 0;
     const void *fn = gate_up ? kTableBatchedGU[pl.shape] : kTableBatched[pl.shape];
-    std::call_once(g_b_once[gu][pl.shape], [&] {
-        g_b_err[gu][pl.shape] = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                                    batched_lds(128, kMaxPairsBatched));
-    });
-    if (g_b_err[gu][pl.shape] != hipSuccess)
+    if (g_b_lds[gu][pl.shape].set(fn, batched_lds(128, kMaxPairsBatched)) != hipSuccess)
         return QMV_EHIP;
     void *kargs[] = {&a};
     const size_t lds = batched_lds(a.bt_vmax, gather ? pairs : 0);
@@ -365,7 +381,8 @@ qmv_status_t launch_batched(const void *codes, const void *scales, const void *c
     return QMV_OK;
 }
 
-std::once_flag g_gr_once[2][2][5][4][5];                // [q8][mode][kind][lpr][cpl]
+LdsLimit g_gr_lds[2][2][5][4][5];                       // [q8][mode][kind][lpr][cpl]
+std::once_flag g_gr_once[2][2][5][4][5];
 hipError_t g_gr_err[2][2][5][4][5];
 int g_gr_occ[2][2][5][4][5];                            // workgroups per CU by registers
 
@@ -396,19 +413,19 @@ qmv_status_t launch_grouped(int wfmt, int afmt, const void *codes, const void *s
     a.codes2 = (const uint8_t *)codes2;
     a.scales2 = (const uint8_t *)scales2;
     const size_t lds = grouped_lds(a.lds_vec_bytes, gather ? pairs : 0);
-    // per kernel, once: the largest LDS any call may ask for, and how many
+    // per kernel: the largest LDS any call may ask for, and (once) how many
     // workgroups a CU holds by the kernel's registers
     auto prepare = [&](int li, int ci) -> hipError_t {
+        const void *f = grouped_kernel_for(kind, mode, li, ci, q8);
+        const int umax = kMaxK / kUnitWeights[kind];
+        const int vmax = (umax * (kUnitXB[kind] + kUnitAB[kind]) + 15) & ~15;
+        const hipError_t e = g_gr_lds[q8][mode][kind][li][ci].set(f, grouped_lds(vmax, kMaxPairsBatched));
+        if (e != hipSuccess)
+            return e;
         std::call_once(g_gr_once[q8][mode][kind][li][ci], [&] {
-            const void *f = grouped_kernel_for(kind, mode, li, ci, q8);
-            const int umax = kMaxK / kUnitWeights[kind];
-            const int vmax = (umax * (kUnitXB[kind] + kUnitAB[kind]) + 15) & ~15;
-            hipError_t err = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                                 grouped_lds(vmax, kMaxPairsBatched));
             int n = 0;
-            if (err == hipSuccess)
-                err = hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, f, 64 * kWaveMenu[0], 0);
-            g_gr_err[q8][mode][kind][li][ci] = err;
+            g_gr_err[q8][mode][kind][li][ci] =
+                hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, f, 64 * kWaveMenu[0], 0);
             g_gr_occ[q8][mode][kind][li][ci] = n > 0 ? n : 1;
         });
         return g_gr_err[q8][mode][kind][li][ci];
@@ -431,6 +448,7 @@ qmv_status_t launch_grouped(int wfmt, int afmt, const void *codes, const void *s
     return QMV_OK;
 }
 
+LdsLimit g_gm_lds[2][2][2][4];
 std::once_flag g_gm_once[2][2][2][4];
 hipError_t g_gm_err[2][2][2][4];
 int g_gm_occ[2][2][2][4];                               // workgroups per CU by registers
@@ -487,12 +505,11 @@ qmv_status_t launch_gmma(int wfmt, int afmt, int kind, const void *codes, const 
     if (lds > (size_t)kLdsPerCU)
         return QMV_EUNSUPPORTED;
     const void *fn = kTableGmma[wv][qi][fi][ni];
+    if (g_gm_lds[wv][qi][fi][ni].set(fn, kLdsPerCU) != hipSuccess)
+        return QMV_EHIP;
     std::call_once(g_gm_once[wv][qi][fi][ni], [&] {
-        hipError_t err = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, kLdsPerCU);
         int n = 0;
-        if (err == hipSuccess)
-            err = hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, 64 * waves, 0);
-        g_gm_err[wv][qi][fi][ni] = err;
+        g_gm_err[wv][qi][fi][ni] = hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, fn, 64 * waves, 0);
         g_gm_occ[wv][qi][fi][ni] = n > 0 ? n : 1;
     });
     if (g_gm_err[wv][qi][fi][ni] != hipSuccess)
@@ -514,8 +531,7 @@ qmv_status_t launch_gmma(int wfmt, int afmt, int kind, const void *codes, const 
     return QMV_OK;
 }
 
-std::once_flag g_ks_once[3];
-hipError_t g_ks_err[3];
+LdsLimit g_ks_lds[3];
 constexpr int kKsMaxM = 64;
 
 // Dense MXFP4 x bf16, 9 to 64 vectors: one launch of K-split tiles, 32 rows
@@ -546,10 +562,7 @@ qmv_status_t launch_batched_ks(const void *codes, const void *scales, const void
     a.bt_vmax = vecs;
     const size_t lds = (size_t)waves * ring * vecs * 256;
     const void *fn = kTableBatchedKS[wi];
-    std::call_once(g_ks_once[wi], [&] {
-        g_ks_err[wi] = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    });
-    if (g_ks_err[wi] != hipSuccess)
+    if (g_ks_lds[wi].set(fn, lds) != hipSuccess)
         return QMV_EHIP;
     void *kargs[] = {&a};
     if (hipLaunchKernel(fn, dim3(8 * a.bt_per_xcd), dim3(64 * waves), kargs, lds, stream) != hipSuccess)
@@ -557,8 +570,7 @@ qmv_status_t launch_batched_ks(const void *codes, const void *scales, const void
     return QMV_OK;
 }
 
-std::once_flag g_d4_once[2];
-hipError_t g_d4_err[2];
+LdsLimit g_d4_lds[2];
 
 qmv_status_t launch_dense4(const void *codes, const void *scales, const void *x, float *y, int M,
                            int N, int K, hipStream_t stream)
@@ -568,11 +580,7 @@ qmv_status_t launch_dense4(const void *codes, const void *scales, const void *x,
     const int waves = dense4_waves(N);
     const int wi = waves == 8 ? 1 : 0;
     const void *fn = kTableDense4[wi];
-    std::call_once(g_d4_once[wi], [&] {
-        g_d4_err[wi] = hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                           dense4_lds(kMaxK, waves));
-    });
-    if (g_d4_err[wi] != hipSuccess)
+    if (g_d4_lds[wi].set(fn, dense4_lds(kMaxK, waves)) != hipSuccess)
         return QMV_EHIP;
     const unsigned quads = (unsigned)((N + 3) / 4);
     const dim3 grid((quads + waves - 1) / waves);
@@ -582,12 +590,7 @@ qmv_status_t launch_dense4(const void *codes, const void *scales, const void *x,
     return QMV_OK;
 }
 
-std::once_flag g_mx4_once[4];
-hipError_t g_mx4_err[4];
-std::once_flag g_mx4_wide_once;
-hipError_t g_mx4_wide_err;
-std::once_flag g_mx4_few_once[3];
-hipError_t g_mx4_few_err[3];
+LdsLimit g_mx4_lds[4], g_mx4_wide_lds, g_mx4_few_lds[3];
 
 // LDS of a tile workgroup: the chunk's list, two buffers of vector codes (chunk
 // x 128 bytes), the waves' weight pieces (rows x 128 bytes), and the
@@ -635,10 +638,7 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
         // tiles (896 tiles 241 us, 270 without; 112 tiles 44 and 63)
         const int cus = cu_count() / 8, rest = cus > 0 ? a.bt_per_xcd % cus : 0, halves = 2 * rest <= cus ? rest : 0;
         a.bt_chunk = a.bt_per_xcd - halves;
-        std::call_once(g_mx4_wide_once, [&] {
-            g_mx4_wide_err = hipFuncSetAttribute(kTableMx4Wide[0], hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-        });
-        if (g_mx4_wide_err != hipSuccess)
+        if (g_mx4_wide_lds.set(kTableMx4Wide[0], lds) != hipSuccess)
             return QMV_EHIP;
         void *kargs[] = {&a};
         return hipLaunchKernel(kTableMx4Wide[0], dim3((unsigned)(8 * (a.bt_per_xcd + halves))), dim3(512), kargs, lds,
@@ -681,11 +681,7 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
         a.bt_chunk = run < 1 ? 1 : run > a.bt_row_tiles ? a.bt_row_tiles : (int)run;
         const long long groups = items * ((a.bt_row_tiles + a.bt_chunk - 1) / a.bt_chunk);
         const int fn = 2 * big + mode;
-        std::call_once(g_mx4_once[fn], [&] {
-            g_mx4_err[fn] = hipFuncSetAttribute(kTableMx4Tile[fn], hipFuncAttributeMaxDynamicSharedMemorySize,
-                                                big ? kLdsPerCU / 2 : mx4_tile_lds(kMaxK, 64));
-        });
-        if (g_mx4_err[fn] != hipSuccess)
+        if (g_mx4_lds[fn].set(kTableMx4Tile[fn], big ? kLdsPerCU / 2 : mx4_tile_lds(kMaxK, 64)) != hipSuccess)
             return QMV_EHIP;
         void *kargs[] = {&a};
         return hipLaunchKernel(kTableMx4Tile[fn], dim3((unsigned)(8 * ((groups + 7) / 8))), dim3(256), kargs,
@@ -715,11 +711,7 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
             grid.y = (unsigned)((M + 15) / 16);
         }
     }
-    std::call_once(g_mx4_few_once[mode], [&] {
-        g_mx4_few_err[mode] = hipFuncSetAttribute(kTableMx4Few[mode], hipFuncAttributeMaxDynamicSharedMemorySize,
-                                                  kLdsPerCU);
-    });
-    if (g_mx4_few_err[mode] != hipSuccess)
+    if (g_mx4_few_lds[mode].set(kTableMx4Few[mode], kLdsPerCU) != hipSuccess)
         return QMV_EHIP;
     void *kargs[] = {&a};
     return hipLaunchKernel(kTableMx4Few[mode], grid, dim3(256), kargs, lds, stream) == hipSuccess ? QMV_OK
@@ -828,13 +820,9 @@ qmv_status_t launch(int wfmt, int afmt, const void *codes, const void *scales, c
 
     const void *fn = kernel_for(wi, kind, variant, sh.li, sh.ci, gate_up, q8);
     // Largest dynamic LDS this kernel can ask for (K = kMaxK, all vectors).
-    std::call_once(g_attr_once[q8][wi][gate_up][kind][variant][sh.li][sh.ci], [&] {
-        const int umax = kMaxK / kUnitWeights[kind];
-        const int vmax = (umax * (kUnitXB[kind] + kUnitAB[kind]) + 15) & ~15;
-        g_attr_err[q8][wi][gate_up][kind][variant][sh.li][sh.ci] = hipFuncSetAttribute(
-            fn, hipFuncAttributeMaxDynamicSharedMemorySize, nvmax * vmax);
-    });
-    if (g_attr_err[q8][wi][gate_up][kind][variant][sh.li][sh.ci] != hipSuccess)
+    const int umax = kMaxK / kUnitWeights[kind];
+    const int vmax = (umax * (kUnitXB[kind] + kUnitAB[kind]) + 15) & ~15;
+    if (g_lds[q8][wi][gate_up][kind][variant][sh.li][sh.ci].set(fn, nvmax * vmax) != hipSuccess)
         return QMV_EHIP;
 
     const dim3 grid((unsigned)((N + a.rows_per_tile - 1) / a.rows_per_tile),
@@ -1030,13 +1018,9 @@ qmv_status_t launch_combine(int wfmt, int afmt, const void *codes, const void *s
     const size_t lds = (size_t)nv * a.lds_vec_bytes;
 
     const void *fn = combine_kernel_for(wi, kind, sh.li, sh.ci, q8);
-    std::call_once(g_cattr_once[q8][wi][kind][sh.li][sh.ci], [&] {
-        const int umax = kMaxK / kUnitWeights[kind];
-        const int vmax = (umax * (kUnitXB[kind] + kUnitAB[kind]) + 15) & ~15;
-        g_cattr_err[q8][wi][kind][sh.li][sh.ci] = hipFuncSetAttribute(
-            fn, hipFuncAttributeMaxDynamicSharedMemorySize, 4 * vmax);
-    });
-    if (g_cattr_err[q8][wi][kind][sh.li][sh.ci] != hipSuccess)
+    const int umax = kMaxK / kUnitWeights[kind];
+    const int vmax = (umax * (kUnitXB[kind] + kUnitAB[kind]) + 15) & ~15;
+    if (g_comb_lds[q8][wi][kind][sh.li][sh.ci].set(fn, 4 * vmax) != hipSuccess)
         return QMV_EHIP;
     const dim3 grid((unsigned)((N + a.rows_per_tile - 1) / a.rows_per_tile), (unsigned)M);
     void *kargs[] = {&a};
