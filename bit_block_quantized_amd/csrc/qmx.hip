@@ -583,7 +583,9 @@ __global__ __launch_bounds__(256) void qmx_router_kernel(const RouterArgs a)
         const float sum = wave_sum(s);
         w = have ? s / sum : 0.0f;
     } else {
-        w = have ? 1.0f / (1.0f + expf(-mine)) : 0.0f;
+        // (e^-l passes fp32's largest where the quotient is still a subnormal number)
+        const float e = expf(-fabsf(mine));
+        w = have ? (mine < 0.0f ? e : 1.0f) / (1.0f + e) : 0.0f;
     }
     if (lane < a.top_k) {
         a.ids[(size_t)t * a.top_k + lane] = my_id;
