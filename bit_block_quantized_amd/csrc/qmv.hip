@@ -602,7 +602,9 @@ int mx4_tile_lds(int K, int chunk)
     return 2 * chunk + 2 * chunk * 128 + 128 * 128 + (128 + chunk) * 16 * (J | 1);
 }
 
-// MXFP4 x MXFP4.  route_w non-null: the combine of up to 4 tokens.
+// MXFP4 x MXFP4.  route_w non-null: the combine of up to 4 tokens.  The times
+// below are a kernel's own: its median in a trace of ten calls with three sets
+// of weights and vectors in turn, in us.
 qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes2, const void *scales2, int E,
                         const int32_t *ids, const float *route_w, int M, int top_k, const void *x,
                         const void *xs, int x_per_slot, float *y, int N, int K, hipStream_t stream)
@@ -622,11 +624,12 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
     auto few_lds = [&](int vectors) { return 64 + 4 * h * 2048 + (size_t)vectors * (xp + sp) + (size_t)h * 16 * sp; };
     int most = pairs < 16 ? pairs : 16;
     // 256 x 256 tiles (or halves of them) once there are more than one for four
-    // CUs and more than half of their vectors exist (us, against the tile
-    // kernel's 128 x 64: 56 tiles 42 and 38; 64 41 and 42, 41 and 40, 41 and 31;
-    // 80 43 and 55; 96 24 and 32, 44 and 45; 112 44 and 71; 224 66 and 131; 896
-    // 241 and 493.  2880 -> 201088: 64 vectors 131 and 93, 128 148 and 146, 256
-    // 171 and 268; 7168 -> 40960: 128 66 and 57, 192 59 and 73)
+    // CUs and more than half of their vectors exist (wide and, after it, the tile
+    // kernel's 128 x 64: 7168 -> 7168: 512 vectors (56 tiles) 43 and 38, 1024 47
+    // and 72, 2048 81 and 134, 8192 296 and 531; 7168 -> 2048: 2048 vectors (64
+    // tiles) 43 and 33; 2880 -> 7168: 768 (84 tiles) 24 and 30; 2880 -> 201088: 64
+    // vectors 125 and 94, 128 146 and 147, 256 179 and 280; 7168 -> 40960: 128 68
+    // and 58, 192 75 and 81)
     const long long wide_tiles = (long long)((N + 255) / 256) * ((M + 255) / 256);
     if (!gather && mode == 0 && M > 128 && 4 * wide_tiles > cu_count()) {
         const int lds = 4 * 256 * 128 + 4 * 256 * 16;
@@ -635,7 +638,8 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
         a.bt_tiles = (int)wide_tiles;
         a.bt_per_xcd = (a.bt_tiles + 7) / 8;
         // a last round that fills at most half of an XCD's CUs is dealt as half
-        // tiles (896 tiles 241 us, 270 without; 112 tiles 44 and 63)
+        // tiles (in halves and whole: 84 tiles 24 and 34, 112 tiles 47 and 69; of
+        // 896 tiles, 3.5 rounds, it is not seen: 279 to 296 and 286 to 287)
         const int cus = cu_count() / 8, rest = cus > 0 ? a.bt_per_xcd % cus : 0, halves = 2 * rest <= cus ? rest : 0;
         a.bt_chunk = a.bt_per_xcd - halves;
         if (g_mx4_wide_lds.set(kTableMx4Wide[0], lds) != hipSuccess)
@@ -644,17 +648,20 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
         return hipLaunchKernel(kTableMx4Wide[0], dim3((unsigned)(8 * (a.bt_per_xcd + halves))), dim3(512), kargs, lds,
                                stream) == hipSuccess ? QMV_OK : QMV_EHIP;
     }
-    // Few vectors: workgroups of 16 rows while the chip is not full of them.
-    // Dense, one per 16 vectors, until there are three per CU (us, against the
-    // tile kernel: 7168 -> 2048: 32 vectors 10 and 15, 64 9.4 and 18.5; 2880 ->
-    // 2880: 64 8.9 and 11.5, 128 14 and 11.5; 7168 -> 7168: 16 11.5 and 17, 32 19
-    // and 18, 64 35 and 20; 2880 -> 201088: 4 79 and 69, 8 86 and 73, 16 99 and
-    // 76; 7168 -> 40960: 4 29 and 34, 8 38 and 34, 16 49 and 35).
+    // Few vectors: workgroups of 16 rows while the chip is not full of them
+    // (few and, after it, the tile kernel).
+    // Dense, one per 16 vectors, until there are three per CU (7168 -> 2048: 32
+    // vectors 8.3 and 15, 64 9.9 and 18; 2880 -> 2880: 64 8.4 and 11, 128 13 and
+    // 11; 7168 -> 7168: 16 10.8 and 12.6, 32 19 and 15, 64 36 and 19; 2880 ->
+    // 201088: 8 77 and 71, 16 99 and 75; 7168 -> 40960: 8 37 and 35, 16 52 and
+    // 36), and with up to 4 vectors whatever the rows (2880 -> 201088: 1 62 and
+    // 66, 4 70.5 and 69; 7168 -> 40960: 1 26 and 34, 4 29 and 34).
     // Routed, one per pair (of gate and of up), until there are seven per CU
-    // (2880 -> 2880 of 32 experts: 4 pairs 10.5 and 13.6, 8 10.9 and 13, 12 16
-    // and 14, 16 20.9 and 19.5, 32 30 and 22, 128 67 and 41; gate/up 4 pairs 12
-    // and 13, 8 21 and 18.6; 7168 -> 2048 of 256: 8 pairs 15.8 and 16.7, 16 28
-    // and 25, 64 104 and 84; 4096 -> 14336 of 8: 2 pairs 14.8 and 15.9).
+    // (2880 -> 2880 of 32 experts: 4 pairs 7.1 and 11.8, 8 11.1 and 12.7, 12 15.2
+    // and 14.2, 16 19.3 and 19.9, 32 28 and 23, 128 65 and 41; gate/up 4 pairs 12
+    // and 12.7, 8 19.2 and 19.4; 7168 -> 2048 of 256: 8 pairs 15.8 and 18.7, 16
+    // 28.7 and 28.1, 64 109 and 84; gate/up 8 25 and 27; 4096 -> 14336 of 8: 2
+    // pairs 14.4 and 15.8).
     const long long row_tiles = (N + 15) / 16;
     const bool many = gather ? pairs * row_tiles * h > 7 * cu_count() : M > kMaxM && (M + 15) / 16 * row_tiles > 3 * cu_count();
     // (the tile kernel counts the pairs of up to 1023 experts)
@@ -662,19 +669,18 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
         const int rows = mode == 1 ? 64 : 128;
         a.bt_row_tiles = (N + rows - 1) / rows;
         // chunks of 128 vectors where many experts have more than 64, as long as
-        // the chip holds two workgroups a CU (2880 -> 2880 of 32 experts, us with
-        // 128 and with 64: gate/up 32 pairs an expert 82 and 81, 48 86 and 86, 64
-        // 93 and 117, 96 105 and 148, 256 243 and 323; gather 64 57 and 63; a dense
-        // matrix differs by less than 3%)
+        // the chip holds two workgroups a CU (2880 -> 2880 of 32 experts, with 128
+        // and with 64: gate/up 32 pairs an expert 76 and 81, 48 85 and 93, 64 93
+        // and 105, 96 114 and 137, 256 218 and 299; gather 64 58 and 60)
         const bool big = gather && pairs >= 48LL * E && 2 * mx4_tile_lds(K, 128) <= kLdsPerCU;
         const int chunk = big ? 128 : 64;
         // items at most: a whole chunk each and a rest per expert
         const long long items = gather ? (pairs < E ? pairs : E) + pairs / chunk : (M + chunk - 1) / chunk;
         // runs of row tiles: about 8 workgroups for each that the chip holds at
-        // a time (fewer, longer runs scan the ids less often but end unevenly:
-        // 1024 tokens x top-8 of 256, 7168 -> 2048: 570 us at 1, 417 at 4, 376
-        // at 8; 512 x top-4 of 32, gate/up 2880 -> 2880, chunks of 64: 110, 112,
-        // 112 us)
+        // a time (1024 tokens x top-8 of 256, 7168 -> 2048: runs for 1 a place 589,
+        // 4 440, 8 404, 16 401; 512 x top-4 of 32, gate/up 2880 -> 2880, chunks of
+        // 64: 1 103, 2 102, 8 102: longer runs scan the ids less often but end
+        // unevenly)
         const int lds = mx4_tile_lds(K, chunk);
         const long long slots = (long long)cu_count() * (lds * 2 <= kLdsPerCU ? 2 : 1);
         const long long run = items * a.bt_row_tiles / (8 * slots);

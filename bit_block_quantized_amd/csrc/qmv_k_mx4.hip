@@ -9,6 +9,9 @@
 // the 32 e2m1 values of row (column) c's block q: 16 bytes exactly as they
 // lie in memory.  So codes go from memory into the operands unchanged, and
 // the sums are formed in fp32.
+//
+// Times here are a kernel's own: its median in a trace of ten calls with three
+// sets of weights and vectors in turn.
 #include "qmv_device.hpp"
 
 #include <type_traits>
@@ -51,11 +54,11 @@ __device__ __forceinline__ f32x4 mfma_mx4_op(u32x4 a, u32x4 b, f32x4 c, uint32_t
 //                       bytes as one dword, which the instruction indexes
 // One barrier per unit; two workgroups of 4 waves share a CU.
 //
-// Bound by the weight stream: 1024 tokens x top-8 of 256, 7168 -> 2048, reads
-// 2.0 GB in 375 us (5.5 TB/s of the 6.3 that default-policy loads reach).  Short
+// Bound by the weight stream: 1024 tokens x top-8 of 256, 7168 -> 2048, moves
+// 2.07 GB in 404 to 414 us (5.1 TB/s of the 6.3 that default-policy loads reach).  Short
 // rows leave more of a tile's time to its start (the ids' counts, the vector
 // list, the scales): 512 tokens x top-4 of 32, gate/up 2880 -> 2880, 282 MB in
-// 92 us, 3.1 TB/s (nontemporal loads of the codes: 104 us).
+// 93 us, 3.0 TB/s (nontemporal loads of the codes took an eighth more).
 __device__ __forceinline__ int swz_chunk(int row, int chunk) { return row * 128 + 16 * (chunk ^ ((row >> 1) & 7)); }
 
 // A row's 16 scale bytes of a slab as loaded: five whole dwords around them.
@@ -566,9 +569,10 @@ __global__ __launch_bounds__(64 * kMx4Waves, 2) void qmv_mx4_tile_kernel(const A
 // start; the vectors and the scale bytes are staged in LDS once.  The waves'
 // partial tiles are summed in wave order.  Columns past the last vector
 // repeat one (nothing of them is stored).  One token's top-4 of 32, 2880 ->
-// 2880: 6.8 us for 18 MB (2.6 TB/s: 720 workgroups of a few loads each, most
-// of it the way from the ids to the first codes); the combine of 4 tokens x 8,
-// 2048 -> 7168: 49 us for 250 MB, 5.1 TB/s.
+// 2880: 7.2 us for 18 MB (2.5 TB/s: 720 workgroups of a few loads each, most
+// of it the way from the ids to the first codes), gate/up 12.1 us for 35 MB;
+// 7168 -> 7168 with 4 vectors 9 us for 27 MB; the combine of 4 tokens x 8,
+// 2048 -> 7168: 51 us for 250 MB, 4.9 TB/s.
 constexpr int kFewAhead = 4;
 
 // Bytes from vector to vector of the staged codes: whole units, and 16 more
@@ -809,13 +813,13 @@ __global__ __launch_bounds__(64 * kMx4Waves) void qmv_mx4_few_kernel(const Args 
 // fragment as soon as its last product of the step is given out, so a step
 // enters with its operands read.  One barrier a unit, in the middle of its
 // second step, where every fragment of the unit is read.
-// 8192 vectors, 7168 -> 7168: 241 us, 3.5 PFLOP/s (270 with the last half round
-// of its 3.5 done in whole tiles, 398 in 128 x 128 tiles of 4 waves, 493 in the
-// tile kernel's 128 x 64).  Measured with whole tiles: all-zero operands take
-// 227 us, which the chip's power limit explains (2.1 GHz against 2.4); of them
-// the products alone take 145, LDS reads add 20, the staging stores 30, the
-// loads 30; loads two steps ahead, or written between other products, change
-// nothing.
+// 8192 vectors, 7168 -> 7168: 266 to 296 us from card to card, 2.8 to 3.2
+// PFLOP/s (531 in the tile kernel's 128 x 64).  With one set of inputs again and
+// again, before the last round's halves: 270, in 128 x 128 tiles of 4 waves 398;
+// all-zero operands 227, which the chip's power limit explains (2.1 GHz against
+// 2.4); of those the products alone take 145, LDS reads add 20, the staging stores
+// 30, the loads 30; loads two steps ahead, or written between other products,
+// change nothing.
 //
 // RF: 16-row fragments per wave; the tile starts at row0 and vec0.
 template <int RF>

@@ -3,7 +3,8 @@
 //
 // Everything here is bound by the bytes it moves (or, for a few tokens, by a
 // launch): one pass over the data, 16-byte accesses, rows held in registers
-// between the reduction and the output.
+// between the reduction and the output.  Times are a kernel's own: its median in
+// a trace of ten calls with three sets of inputs in turn.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -230,8 +231,8 @@ __device__ __forceinline__ void put8(void *y, void *ys, size_t i, const float (&
 // sum(h^2) and the products are formed in fp64: the quantizers round to a
 // border-exact code, and an fp32 norm is off by 1e-7, which moves one code
 // in 1e5 across a border.  The kernel waits for memory, not for the fp64
-// rate: 2048 rows of 7168, bf16 with an fp32 residual, to int8: 32 us for 162 MB,
-// 5.1 TB/s, which is what a copy reaches.
+// rate: 2048 rows of 7168, to int8: bf16 with an fp32 residual 35 us for 162 MB,
+// 4.6 TB/s, fp32 with a bf16 one 29 us for 133 MB (a copy reaches 5.1 TB/s).
 struct NormArgs {
     const void *x, *res, *w;
     void *res_out, *y, *ys;
@@ -358,10 +359,11 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void qmx_rmsnorm_odd_kernel(cons
 }
 
 // Threads a row: a step of 8 values each keeps the most bytes in flight
-// (2048 rows of 7168, us: 256 threads 34.8, 512 32.7, 1024 32.1; one row of
-// 7168 5.4, 4.5, 4.2), except where a row of up to 4096 leaves many of 512
+// (2048 rows of 7168, us: 256 threads 38.7, 512 35.4, 1024 34.9; one row of
+// 7168 5.6, 4.3, 4.0), except where a row of up to 4096 leaves many of 512
 // threads idle and there are rows enough to fill the chip (rows of 2880: 2048
-// of them 13.6 us with 256 threads, 14.9 with 512; one 3.9 and 3.2).
+// of them 14.1 us with 256 threads, 15.7 with 512; 1024 10.5 and 10.2; 512 7.0
+// and 6.8; one 3.6 and 3.1).
 template <int FMT>
 const void *norm_kernel(int M, int K, int &threads, int &rows)
 {
@@ -388,8 +390,8 @@ const void *norm_odd_kernel(int K, int &threads, int &rows)
 // ---------------------------------------------------- quantize / dequantize
 // A flat array of 8-value pieces: thread t of a workgroup takes pieces
 // t, t + 256, ... (UN of them in flight) of the workgroup's run.  Bound by the
-// bytes: 92160 rows of 2880 bf16 to MXFP4 and back, 1.34 GB in 260 us, 5.2
-// TB/s, the rate of a copy.
+// bytes: 92160 rows of 2880 bf16 to MXFP4 124 us, back 129, to int8 145: 5.2 to
+// 5.6 TB/s, the rate of a copy.
 constexpr int kPieceUnroll = 4;
 
 template <int FMT>
