@@ -43,7 +43,7 @@ def nan_like(*shape):
 DENSE = [(FEW, 3, 100, 16384), (FEW, 16, 200, 7168), (FEW, 20, 90, 16352),
          (TILE64, 17, 6200, 16384), (TILE64, 70, 2900, 7168), (TILE64, 64, 3100, 16352), (TILE64, 33, 4100, 544),
          (WIDE, 257, 8300, 7168), (WIDE, 1030, 3400, 16352), (WIDE, 300, 8300, 16384), (WIDE, 2050, 2100, 2880),
-         (WIDE, 4100, 1030, 32), (WIDE, 2300, 7500, 288)]
+         (WIDE, 4100, 1030, 32), (WIDE, 2300, 7500, 288), (TILE64, 8192, 200, 96), (FEW, 8192, 16, 64)]
 
 
 @pytest.mark.parametrize("kernel,M,N,K", DENSE)
@@ -61,6 +61,9 @@ GATHER = [(FEW, 4, 8, 4, 100, 7168), (FEW, 40, 8, 2, 130, 7168), (FEW, 33, 1000,
           (TILE64, 60, 40, 2, 300, 7168), (TILE64, 60, 5, 2, 300, 16384), (TILE64, 100, 40, 2, 301, 16352),
           (TILE64, 4, 40, 8, 1000, 544), (TILE64, 300, 3, 2, 400, 3616),
           (TILE128, 150, 4, 4, 96, 3584), (TILE128, 300, 8, 4, 70, 3552), (TILE128, 700, 3, 2, 200, 1024)]
+# as many pairs as a call may have, and as many as the few-vector kernel takes
+GATHER += [(TILE64, 512, 1023, 16, 33, 96), (TILE128, 512, 100, 16, 33, 96), (TILE128, 8192, 5, 1, 20, 64),
+           (FEW, 112, 1023, 16, 16, 96), (FEW, 1792, 40, 1, 9, 64)]
 
 
 @pytest.mark.parametrize("per_slot", [False, True])
@@ -257,6 +260,39 @@ def test_scales_start_at_any_byte(kernel, M, E, top_k, N, off_w, off_x):
     want, A = reference(E, wc, ws, ids, xc, xs)
     X.held(A)
     equal(product(E, wc, shifted(ws, off_w), ids, xc, shifted(xs, off_x)), want, (kernel, off_w, off_x))
+
+
+# (kernel, entry, M, E, top_k, N)
+SHIFTED = [(FEW_GU, "swiglu", 4, 8, 4, 100), (FEW_GU, "swiglu", 40, 8, 2, 70), (GU64, "swiglu", 60, 40, 2, 301),
+           (GU128, "swiglu", 150, 4, 4, 97), (FEW_COMB, "combine", 4, 8, 4, 101)]
+
+
+@pytest.mark.parametrize("kernel,entry,M,E,top_k,N", SHIFTED)
+def test_gate_up_and_combine_scales_start_at_any_byte(kernel, entry, M, E, top_k, N):
+    K = 1120
+    w_lo, x_lo = swiglu_bytes(K)
+    g = gen(M + N)
+
+    def shifted(a, off):
+        buf = torch.full((a.numel() + 16,), 255, dtype=torch.uint8, device="cuda")
+        buf[off:off + a.numel()] = a.reshape(-1)
+        return buf[off:off + a.numel()].view(a.shape)
+
+    (wc, ws), (uc, us) = (X.codes(g, (E, N), K, w_lo) for _ in range(2))
+    for offs in ((1, 2, 3), (3, 0, 1), (2, 3, 0)):
+        xc, xs = X.codes(g, (M, top_k) if entry == "combine" else (M,), K, x_lo)
+        ids = X.make_ids(g, M, top_k, E)
+        rows, A = X.gather(ids, wc, ws, X.values(xc, xs))
+        X.held(A, w_lo, x_lo)
+        ws_, us_, xs_ = (shifted(t, o) for t, o in zip((ws, us, xs), offs))
+        if entry == "combine":
+            ones = torch.ones(M, top_k, device="cuda")
+            X.held(A.sum(1), w_lo, x_lo)
+            equal(q.qmv_gather_moe_combine("mxfp4", wc, ws_, ids, ones, xc, xs_), rows.sum(1), (kernel, offs))
+        else:
+            up, A = X.gather(ids, uc, us, X.values(xc, xs))
+            X.held(A, w_lo, x_lo)
+            check_swiglu(q.qmv_gather_moe_swiglu("mxfp4", wc, ws_, uc, us_, ids, xc, xs_), rows, up, (kernel, offs))
 
 
 @pytest.mark.parametrize("at", [0, 1])

@@ -69,6 +69,8 @@ def test_edges(L):
     for kernel, entry, M, E, top_k, N in G.EMPTY:
         assert M * top_k > 64
         first(entries[entry](L, M, E, top_k, N, 544), kernel)
+    for kernel, entry, M, E, top_k, N in G.SHIFTED:
+        first((mx4_swiglu if entry == "swiglu" else mx4_combine)(L, M, E, top_k, N, 1120), kernel)
     for kernel, entry, M, E, top_k, N, K in G.FAR:
         first(entries[entry](L, M, E, top_k, N, K), kernel)
         assert (E - 1) * N * (K // 2) > (2 ** 31 if kernel == G.FEW else 2 ** 32)
