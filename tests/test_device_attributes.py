@@ -5,7 +5,7 @@ the process used first.
 import pytest
 
 import launches
-from launches import P, mx4_combine, mx4_dense, mx4_gather, mx4_swiglu
+from launches import P
 
 DEFAULT = 64 * 1024                                            # dynamic LDS that needs no attribute
 
