@@ -20,7 +20,11 @@ bf16 activations with 2-bit or 3-bit weights (x_scales None) are quantized
 to int8 per 32 inside the kernel (QMV_A_BF16_Q8); MXFP4 weights take bf16
 activations, int8 activations with their scales (QMV_A_Q8B32), or MXFP4
 activations (QMV_A_MXFP4: x uint8 [M][K/2] of e2m1 codes, x_scales uint8
-[M][K/32]), which qmx_quantize and qmx_rmsnorm write (qmx.py).
+[M][K/32]), which qmx_quantize and qmx_rmsnorm write (qmx.py).  "f8" weights
+(float8_e4m3fn or uint8 codes [E][N][K], float32 scales
+[E][ceil(N/128)][ceil(K/128)], which qmt_quantize_weights writes) take e4m3
+activations (x [M][K], x_scales float32 [M][ceil(K/128)]; fmt "f8" of
+qmx_quantize and qmx_rmsnorm).
 """
 from __future__ import annotations
 
@@ -33,15 +37,17 @@ __all__ = ["qmv_dense", "qmv_gather_moe", "qmv_gather_moe_swiglu", "qmv_gather_m
            "qmv_gather_moe_combine_noalloc",
            "qmv_strerror",
            "qmv_probe_stream_read", "qmv_probe_clock", "lib", "LIB_PATH",
-           "W_MXFP4", "W_CB2", "W_CB3", "A_BF16", "A_Q8B32", "A_BF16_Q8", "A_MXFP4", "QmvError",
+           "W_MXFP4", "W_CB2", "W_CB3", "W_F8B128", "A_BF16", "A_Q8B32", "A_BF16_Q8", "A_MXFP4", "A_F8B128", "QmvError",
            "qmx_rmsnorm", "qmx_router", "qmx_quantize", "qmx_dequantize", "qmx_strerror", "qmx_lib",
-           "QMX_LIB_PATH"]
+           "QMX_LIB_PATH",
+           "qmt_quantize_weights", "qmt_dequantize_weights", "qmt_qk_norm_rope", "qmt_logprobs", "qmt_strerror",
+           "qmt_lib", "QMT_LIB_PATH"]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqmv.so")
 
-W_MXFP4, W_CB2, W_CB3 = 0, 1, 2
-A_BF16, A_Q8B32, A_BF16_Q8, A_MXFP4 = 0, 1, 2, 4
-_WFMT = {"mxfp4": W_MXFP4, "cb2": W_CB2, "cb3": W_CB3}
+W_MXFP4, W_CB2, W_CB3, W_F8B128 = 0, 1, 2, 3
+A_BF16, A_Q8B32, A_BF16_Q8, A_MXFP4, A_F8B128 = 0, 1, 2, 4, 5
+_WFMT = {"mxfp4": W_MXFP4, "cb2": W_CB2, "cb3": W_CB3, "f8": W_F8B128}
 _AFMT_OF = {W_MXFP4: A_BF16, W_CB2: A_Q8B32, W_CB3: A_Q8B32}
 STATUS = {0: "QMV_OK", 1: "QMV_EINVAL", 2: "QMV_EUNSUPPORTED", 3: "QMV_EHIP", 4: "QMV_ESCRATCH"}
 # bytes of the allocation-free combine's fixed temporary per GPU (include/qmv.h)
@@ -136,13 +142,28 @@ def _check(status):
         raise QmvError(status, qmv_strerror(status))
 
 
+F8_DT = (torch.float8_e4m3fn, torch.uint8)
 _SCALE_DT = (torch.uint8, torch.float16)
+
+
+def _code_dt(w):
+    return F8_DT if w == W_F8B128 else (torch.uint8,)
+
+
+def _scale_dt(w):
+    return (torch.float32,) if w == W_F8B128 else _SCALE_DT
+
+
+def _blocks128(n):
+    return (n + 127) // 128
 
 
 def _afmt(w, x):
     """Activation format from the weight format and x's dtype: MXFP4 takes
     bf16, int8 (+ scales) or uint8 e2m1 codes (+ scales); 2-/3-bit weights
-    take int8 (+ scales) or bf16 (quantized in-kernel)."""
+    take int8 (+ scales) or bf16 (quantized in-kernel), "f8" e4m3 (+ scales)."""
+    if w == W_F8B128:
+        return A_F8B128, F8_DT
     is_bf16 = isinstance(x, torch.Tensor) and x.dtype == torch.bfloat16
     if w == W_MXFP4:
         if isinstance(x, torch.Tensor) and x.dtype == torch.uint8:
@@ -168,7 +189,16 @@ def _nbytes(t):
 
 def _check_weights(w, codes, scales, lead, K, what=("w_codes", "w_scales")):
     """codes/scales hold exactly the rows the kernel will address: leading
-    dimensions ``lead`` ((E, N) or (N,)) and the row bytes of K weights."""
+    dimensions ``lead`` ((E, N) or (N,)) and the row bytes of K weights; "f8"
+    scales one for each 128 x 128 block."""
+    if w == W_F8B128:
+        for t, name, shape in ((codes, what[0], lead + (K,)),
+                               (scales, what[1], lead[:-1] + (_blocks128(lead[-1]), _blocks128(K)))):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            if t.shape != shape:
+                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        return
     rcb, rsb = _row_bytes(w, K)
     rows = 1
     for d in lead:
@@ -185,13 +215,20 @@ def _check_weights(w, codes, scales, lead, K, what=("w_codes", "w_scales")):
 
 def _check_x(x, x_scales, vectors, K, a):
     """x holds ``vectors`` activation vectors of K values, and x_scales (int8
-    or MXFP4 activations) one fp16 or E8M0 scale per 32 of them."""
+    or MXFP4 activations) one fp16 or E8M0 scale per 32 of them (e4m3: one
+    float32 per 128)."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
     held = K // 2 if a == A_MXFP4 else K
     if not (x.dim() >= 1 and x.shape[-1] == held and x.numel() == vectors * held):
         raise ValueError(f"x has shape {tuple(x.shape)}, expected {vectors} vectors of K={K}")
-    if a == A_Q8B32 or a == A_MXFP4:
+    if a == A_F8B128:
+        if not isinstance(x_scales, torch.Tensor):
+            raise ValueError("e4m3 activations need x_scales (float32, one per 128)")
+        if x_scales.shape != x.shape[:-1] + (_blocks128(K),):
+            raise ValueError(f"x_scales has shape {tuple(x_scales.shape)}, expected "
+                             f"{tuple(x.shape[:-1] + (_blocks128(K),))}")
+    elif a == A_Q8B32 or a == A_MXFP4:
         kind, scale = ("int8", "fp16") if a == A_Q8B32 else ("MXFP4", "E8M0")
         if not isinstance(x_scales, torch.Tensor):
             raise ValueError(f"{kind} activations need x_scales "
@@ -200,7 +237,7 @@ def _check_x(x, x_scales, vectors, K, a):
             raise ValueError(f"x_scales has shape {tuple(x_scales.shape)}, expected {vectors} x {K // 32} "
                              f"{scale} scales")
     elif x_scales is not None:
-        raise ValueError("x_scales is only used with int8 or MXFP4 activations")
+        raise ValueError("x_scales is only used with int8, MXFP4 or e4m3 activations")
 
 
 def _k_of(w, x):
@@ -209,7 +246,7 @@ def _k_of(w, x):
 
 
 def _xs_dtypes(a):
-    return (torch.uint8,) if a == A_MXFP4 else (torch.float16,)
+    return (torch.uint8,) if a == A_MXFP4 else (torch.float32,) if a == A_F8B128 else (torch.float16,)
 
 
 def _check_y(y, shape):
@@ -267,8 +304,8 @@ def qmv_dense(wfmt, w_codes, w_scales, x, x_scales=None, y=None, stream=None):
     _gpu(dev, "qmv_dense")
     if y is None:
         y = torch.empty((M, N), dtype=torch.float32, device=dev)
-    s = _on_device(lib().qmv_dense, dev, stream, w, _dev_ptr(w_codes, "w_codes", (torch.uint8,), dev),
-                        _dev_ptr(w_scales, "w_scales", _SCALE_DT, dev), a,
+    s = _on_device(lib().qmv_dense, dev, stream, w, _dev_ptr(w_codes, "w_codes", _code_dt(w), dev),
+                        _dev_ptr(w_scales, "w_scales", _scale_dt(w), dev), a,
                         _dev_ptr(x, "x", xd, dev),
                         _dev_ptr(x_scales, "x_scales", _xs_dtypes(a), dev),
                         _dev_ptr(y, "y", (torch.float32,), dev), M, N, K)
@@ -298,8 +335,8 @@ def qmv_gather_moe(wfmt, w_codes, w_scales, expert_ids, x, x_scales=None, x_per_
     _gpu(dev, "qmv_gather_moe")
     if y is None:
         y = torch.empty((M, top_k, N), dtype=torch.float32, device=dev)
-    s = _on_device(lib().qmv_gather_moe, dev, stream, w, _dev_ptr(w_codes, "w_codes", (torch.uint8,), dev),
-                             _dev_ptr(w_scales, "w_scales", _SCALE_DT, dev), E,
+    s = _on_device(lib().qmv_gather_moe, dev, stream, w, _dev_ptr(w_codes, "w_codes", _code_dt(w), dev),
+                             _dev_ptr(w_scales, "w_scales", _scale_dt(w), dev), E,
                              _dev_ptr(expert_ids, "expert_ids", (torch.int32,), dev), M, top_k, a,
                              _dev_ptr(x, "x", xd, dev),
                              _dev_ptr(x_scales, "x_scales", _xs_dtypes(a), dev),
@@ -329,10 +366,10 @@ def qmv_gather_moe_swiglu(wfmt, gate_codes, gate_scales, up_codes, up_scales, ex
     if y is None:
         y = torch.empty((M, top_k, N), dtype=torch.float32, device=dev)
     s = _on_device(
-        lib().qmv_gather_moe_swiglu, dev, stream, w, _dev_ptr(gate_codes, "gate_codes", (torch.uint8,), dev),
-        _dev_ptr(gate_scales, "gate_scales", _SCALE_DT, dev),
-        _dev_ptr(up_codes, "up_codes", (torch.uint8,), dev),
-        _dev_ptr(up_scales, "up_scales", _SCALE_DT, dev), E,
+        lib().qmv_gather_moe_swiglu, dev, stream, w, _dev_ptr(gate_codes, "gate_codes", _code_dt(w), dev),
+        _dev_ptr(gate_scales, "gate_scales", _scale_dt(w), dev),
+        _dev_ptr(up_codes, "up_codes", _code_dt(w), dev),
+        _dev_ptr(up_scales, "up_scales", _scale_dt(w), dev), E,
         _dev_ptr(expert_ids, "expert_ids", (torch.int32,), dev), M, top_k, a,
         _dev_ptr(x, "x", xd, dev), _dev_ptr(x_scales, "x_scales", _xs_dtypes(a), dev),
         _dev_ptr(y, "y", (torch.float32,), dev), N, K)
@@ -386,8 +423,8 @@ def _combine(entry, wfmt, w_codes, w_scales, expert_ids, route_weights, x, x_sca
     if y is None:
         y = torch.empty((M, N), dtype=torch.float32, device=dev)
     s = _on_device(
-        getattr(lib(), entry), dev, stream, w, _dev_ptr(w_codes, "w_codes", (torch.uint8,), dev),
-        _dev_ptr(w_scales, "w_scales", _SCALE_DT, dev), E,
+        getattr(lib(), entry), dev, stream, w, _dev_ptr(w_codes, "w_codes", _code_dt(w), dev),
+        _dev_ptr(w_scales, "w_scales", _scale_dt(w), dev), E,
         _dev_ptr(expert_ids, "expert_ids", (torch.int32,), dev),
         _dev_ptr(route_weights, "route_weights", (torch.float32,), dev), M, top_k, a,
         _dev_ptr(x, "x", xd, dev), _dev_ptr(x_scales, "x_scales", _xs_dtypes(a), dev),
@@ -421,3 +458,5 @@ def qmv_probe_clock(out, stream=None):
 
 from .qmx import (QMX_LIB_PATH, qmx_dequantize, qmx_lib, qmx_quantize, qmx_rmsnorm,  # noqa: E402
                   qmx_router, qmx_strerror)
+from .qmt import (QMT_LIB_PATH, qmt_dequantize_weights, qmt_lib, qmt_logprobs, qmt_qk_norm_rope,  # noqa: E402
+                  qmt_quantize_weights, qmt_strerror)

@@ -1,11 +1,12 @@
-"""Build libqmv.so and libqmx.so (HIP, gfx950) in-tree with hipcc.
+"""Build libqmv.so, libqmx.so and libqmt.so (HIP, gfx950) in-tree with hipcc.
 
     python -m bit_block_quantized_amd.build
 
 libqmv.so holds the expert products (include/qmv.h), libqmx.so the steps
-around them (include/qmx.h).  Each translation unit (for libqmv.so the
+around them (include/qmx.h), libqmt.so those around the 8-bit floating-point
+ones (include/qmt.h).  Each translation unit (for libqmv.so the
 launcher/ABI and one kernel table per weight format) is compiled in parallel,
-then linked into its shared library.  Both are compiled for gfx950 only.  Packed-FP32 VALU forms are switched off
+then linked into its shared library.  All are compiled for gfx950 only.  Packed-FP32 VALU forms are switched off
 (``-packed-fp32-ops``) so the compiler never emits v_pk_{add,mul,fma}_f32.
 """
 from __future__ import annotations
@@ -23,21 +24,24 @@ CSRC = os.path.join(HERE, "csrc")
 KERNEL_SOURCES = ["qmv_k_mxfp4.hip", "qmv_k_mxfp4i.hip", "qmv_k_cb2.hip", "qmv_k_cb2s.hip", "qmv_k_cb3.hip",
                   "qmv_k_cb2q.hip", "qmv_k_cb2sq.hip", "qmv_k_cb3q.hip"]
 # (source, extra flags, object): the launcher, the probe, the matrix-core
-# kernels (MXFP4 x bf16 for 2-4 vectors and for more, MXFP4 x MXFP4, codebook
-# x int8 for more than 4; their workgroup size is a template argument or fixed), and
+# kernels (MXFP4 x bf16 for 2-4 vectors and for more, MXFP4 x MXFP4, e4m3 x
+# e4m3, codebook x int8 for more than 4; their workgroup size is a template argument or fixed), and
 # every other kernel table twice -- 4 and 8 wave64s per workgroup, in
 # namespaces qmv / qmv_w8.
 UNITS = ([("qmv.hip", [], "qmv.o"), ("qmv_probe.hip", [], "qmv_probe.o"),
           ("qmv_k_mxfp4m.hip", [], "qmv_k_mxfp4m.o"),
           ("qmv_k_mxfp4b.hip", [], "qmv_k_mxfp4b.o"),
           ("qmv_k_mx4.hip", [], "qmv_k_mx4.o"),
+          ("qmv_k_f8.hip", [], "qmv_k_f8.o"),
           ("qmv_k_cbm.hip", [], "qmv_k_cbm.o")] +
          [(k, [], k.replace(".hip", ".o")) for k in KERNEL_SOURCES] +
          [(k, ["-DQMV_WAVES=8", "-DQMV_NS=qmv_w8"], k.replace(".hip", "_w8.o")) for k in KERNEL_SOURCES])
 QMX_UNITS = [("qmx.hip", [], "qmx.o")]
-SOURCES = [u[0] for u in UNITS + QMX_UNITS]
+QMT_UNITS = [("qmt.hip", [], "qmt.o")]
+SOURCES = [u[0] for u in UNITS + QMX_UNITS + QMT_UNITS]
 LIB = os.path.join(HERE, "libqmv.so")
 LIB_QMX = os.path.join(HERE, "libqmx.so")
+LIB_QMT = os.path.join(HERE, "libqmt.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 FLAGS = [
@@ -88,9 +92,9 @@ class ScratchError(RuntimeError):
 
 
 def build(out: str = LIB, extra: list | None = None, verbose: bool = False,
-          out_qmx: str = LIB_QMX) -> str:
+          out_qmx: str = LIB_QMX, out_qmt: str = LIB_QMT) -> str:
     inc = ["-I", os.path.join(ROOT, "include"), "-I", CSRC]
-    units = UNITS + QMX_UNITS
+    units = UNITS + QMX_UNITS + QMT_UNITS
     with tempfile.TemporaryDirectory(prefix="qmv_build_") as tmp:
         def compile_one(unit):
             src, defs, objname = unit
@@ -116,7 +120,9 @@ def build(out: str = LIB, extra: list | None = None, verbose: bool = False,
                                "; ".join(f"{n} {r}" for n, r in bad))
         if verbose:
             print(f"{len(kernels)} kernels, none uses scratch memory", flush=True)
-        for lib, of in ((out, res[:len(UNITS)]), (out_qmx, res[len(UNITS):])):
+        at = 0
+        for lib, n in ((out, len(UNITS)), (out_qmx, len(QMX_UNITS)), (out_qmt, len(QMT_UNITS))):
+            of, at = res[at:at + n], at + n
             cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", *[o for o, _ in of], "-o", lib + ".tmp"]
             if verbose:
                 print(" ".join(cmd), flush=True)

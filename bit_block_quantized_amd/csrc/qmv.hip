@@ -74,6 +74,13 @@ extern const void *const kTableMx4Tile[4];
 extern const void *const kTableMx4Wide[1];
 }
 
+// e4m3 x e4m3 with a scale per block of 128 (qmv_k_f8.hip): [plain, gate/up,
+// combine], [plain, gate/up].
+namespace qmv {
+extern const void *const kTableF8Few[3];
+extern const void *const kTableF8Tile[2];
+}
+
 namespace qmv {
 constexpr int kBatchedMenu = 6;
 extern const int kBatchedShapes[kBatchedMenu][3];
@@ -724,6 +731,92 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
                                                                                                   : QMV_EHIP;
 }
 
+LdsLimit g_f8_lds[2], g_f8_few_lds[3];
+
+// LDS of a tile workgroup: the chunk's list, two buffers of vector codes (chunk
+// x 128 bytes), the waves' weight pieces (128 rows x 128 bytes), and the scales
+// of the rows' one or two block rows and of the vectors.
+int f8_tile_lds(int K, int chunk)
+{
+    const int KB = (K + 127) / 128;
+    return 2 * chunk + 2 * chunk * 128 + 128 * 128 + 4 * ((2 * KB + 3) & ~3) + 4 * chunk * KB;
+}
+
+// e4m3 x e4m3.  route_w non-null: the combine of up to 4 tokens.
+qmv_status_t launch_f8(const void *codes, const void *scales, const void *codes2, const void *scales2, int E,
+                       const int32_t *ids, const float *route_w, int M, int top_k, const void *x, const void *xs,
+                       int x_per_slot, float *y, int N, int K, hipStream_t stream)
+{
+    const bool gather = ids != nullptr;
+    Args a = base_args(QMV_W_F8B128, QMV_A_F8B128, kMXFP4, codes, scales, gather ? E : 1, ids, M,
+                       gather ? top_k : 1, x, xs, gather ? x_per_slot : 0, y, N, K);
+    const int KB = (K + 127) / 128;
+    a.codes2 = (const uint8_t *)codes2;
+    a.scales2 = (const uint8_t *)scales2;
+    a.route_w = route_w;
+    a.x_vec_bytes = K;
+    a.units = KB;
+    a.rsb = 4 * KB;                              // of a block row of 128 rows
+    a.expert_sb = (long long)((N + 127) / 128) * a.rsb;
+    const int mode = route_w ? 2 : codes2 ? 1 : 0;
+    const int pairs = gather ? M * top_k : M;
+    // the few kernel's LDS: weight pieces, the vectors' codes and scales, the rows' scales
+    const int h = mode == 1 ? 2 : 1, xp = KB * 128 + 16, sp = 4 * (KB | 1);
+    auto few_lds = [&](int vectors) { return 64 + 4 * h * 2048 + vectors * (xp + sp) + h * sp; };
+    int most = pairs < 16 ? pairs : 16;
+    const long long row_tiles = (N + 15) / 16;
+    const bool many = gather ? pairs * row_tiles * h > 7 * cu_count() : M > kMaxM && (M + 15) / 16 * row_tiles > 3 * cu_count();
+    // (the tile kernel counts the pairs of up to 1023 experts)
+    if (mode != 2 && (!gather || E <= kMaxEBatched) && (many || few_lds(most) > kLdsPerCU)) {
+        const int rows = mode == 1 ? 64 : 128;
+        a.bt_row_tiles = (N + rows - 1) / rows;
+        const int chunk = 64;
+        // items at most: a whole chunk each and a rest per expert
+        const long long items = gather ? (pairs < E ? pairs : E) + pairs / chunk : (M + chunk - 1) / chunk;
+        // runs of row tiles: about 8 workgroups for each that the chip holds at a time
+        const int lds = f8_tile_lds(K, chunk);
+        const long long slots = (long long)cu_count() * (lds * 2 <= kLdsPerCU ? 2 : 1);
+        const long long run = items * a.bt_row_tiles / (8 * slots);
+        a.bt_chunk = run < 1 ? 1 : run > a.bt_row_tiles ? a.bt_row_tiles : (int)run;
+        const long long groups = items * ((a.bt_row_tiles + a.bt_chunk - 1) / a.bt_chunk);
+        if (g_f8_lds[mode].set(kTableF8Tile[mode], f8_tile_lds(kMaxK, chunk)) != hipSuccess)
+            return QMV_EHIP;
+        void *kargs[] = {&a};
+        return hipLaunchKernel(kTableF8Tile[mode], dim3((unsigned)(8 * ((groups + 7) / 8))), dim3(256), kargs, lds,
+                               stream) == hipSuccess ? QMV_OK : QMV_EHIP;
+    }
+    // few vectors: 16-row tiles, K split over the waves
+    a.bt_row_tiles = (int)row_tiles;
+    // (up to 4 tokens' pairs with the longest rows of more than 1023 experts)
+    while (mode != 2 && few_lds(most) > kLdsPerCU)
+        most = (most + 1) / 2;
+    int lds = few_lds(most);
+    dim3 grid((unsigned)a.bt_row_tiles, 1);
+    if (mode == 2) {
+        // as many slots staged at a time as 64 KB hold
+        const int per_slot = xp + 2 * sp, fit = 64 * 1024 / per_slot;
+        a.bt_vmax = fit < 1 ? 1 : fit < top_k ? fit : top_k;
+        lds = 64 + 4 * 2048 + a.bt_vmax * per_slot;
+        grid.y = (unsigned)M;
+    } else {
+        a.bt_vmax = most;
+        if (gather && pairs > 64) {
+            if (lds < 64 + 4 * 1032) lds = 64 + 4 * 1032;      // the counts per expert
+            const long long items = (pairs < E ? pairs : E) + pairs / 16;
+            grid.x = (unsigned)(8 * ((items * row_tiles + 7) / 8));
+        } else if (gather) {
+            grid.y = (unsigned)(pairs * ((pairs + most - 1) / most));
+        } else {
+            grid.y = (unsigned)((M + 15) / 16);
+        }
+    }
+    if (g_f8_few_lds[mode].set(kTableF8Few[mode], kLdsPerCU) != hipSuccess)
+        return QMV_EHIP;
+    void *kargs[] = {&a};
+    return hipLaunchKernel(kTableF8Few[mode], grid, dim3(256), kargs, (size_t)lds, stream) == hipSuccess ? QMV_OK
+                                                                                                         : QMV_EHIP;
+}
+
 // codes2/scales2 non-null selects the gate/up mode: codes/scales are the gate
 // projection, codes2/scales2 the up projection, y = swiglu(gate x, up x).
 qmv_status_t launch(int wfmt, int afmt, const void *codes, const void *scales, const void *codes2,
@@ -736,6 +829,9 @@ qmv_status_t launch(int wfmt, int afmt, const void *codes, const void *scales, c
     if (afmt == QMV_A_MXFP4)
         return launch_mx4(codes, scales, codes2, scales2, E, ids, nullptr, M, top_k, x, xs, x_per_slot, y, N, K,
                           stream);
+    if (afmt == QMV_A_F8B128)
+        return launch_f8(codes, scales, codes2, scales2, E, ids, nullptr, M, top_k, x, xs, x_per_slot, y, N, K,
+                         stream);
     const int kind = kind_of(wfmt, afmt, K);
     // Dense MXFP4 x bf16 with 9 to 64 vectors: K-split tiles, one launch.
     // Measured on 7168 x 7168: 16 vectors 34.3 us as four 4-vector launches,
@@ -1008,6 +1104,9 @@ qmv_status_t launch_combine(int wfmt, int afmt, const void *codes, const void *s
     if (afmt == QMV_A_MXFP4)
         return launch_mx4(codes, scales, nullptr, nullptr, E, ids, route_w, M, top_k, x, xs, x_per_slot, y, N, K,
                           stream);
+    if (afmt == QMV_A_F8B128)
+        return launch_f8(codes, scales, nullptr, nullptr, E, ids, route_w, M, top_k, x, xs, x_per_slot, y, N, K,
+                         stream);
     const int kind = kind_of(wfmt, afmt, K);
     Args a = base_args(wfmt, afmt, kind, codes, scales, E, ids, M, top_k, x, xs, x_per_slot, y, N, K);
     a.route_w = route_w;

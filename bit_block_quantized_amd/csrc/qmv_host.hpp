@@ -78,7 +78,7 @@ inline bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)
 
 inline long long row_code_bytes(int wfmt, long long K)
 {
-    return wfmt == QMV_W_MXFP4 ? K / 2 : wfmt == QMV_W_CB2 ? K / 4 : 3 * K / 8;
+    return wfmt == QMV_W_F8B128 ? K : wfmt == QMV_W_MXFP4 ? K / 2 : wfmt == QMV_W_CB2 ? K / 4 : 3 * K / 8;
 }
 inline long long row_scale_bytes(int wfmt, long long K)
 {
@@ -101,15 +101,19 @@ inline qmv_status_t validate(int wfmt, const void *codes, const void *scales, lo
 {
     if (!codes || !scales || !x || !y || (gather && !ids))
         return QMV_EINVAL;
-    if ((afmt == QMV_A_Q8B32 || afmt == QMV_A_MXFP4) && !xs)
+    if ((afmt == QMV_A_Q8B32 || afmt == QMV_A_MXFP4 || afmt == QMV_A_F8B128) && !xs)
         return QMV_EINVAL;
     if (M <= 0 || N <= 0 || K <= 0 || E <= 0 || top_k <= 0)
         return QMV_EINVAL;
-    if (wfmt < QMV_W_MXFP4 || wfmt > QMV_W_CB3 ||
-        (afmt != QMV_A_BF16 && afmt != QMV_A_Q8B32 && afmt != QMV_A_BF16_Q8 && afmt != QMV_A_MXFP4))
+    if (wfmt < QMV_W_MXFP4 || wfmt > QMV_W_F8B128 ||
+        (afmt != QMV_A_BF16 && afmt != QMV_A_Q8B32 && afmt != QMV_A_BF16_Q8 && afmt != QMV_A_MXFP4 &&
+         afmt != QMV_A_F8B128))
         return QMV_EUNSUPPORTED;
-    // pairs: (MXFP4, BF16), (MXFP4, Q8B32), (MXFP4, MXFP4), (CB2 or CB3, Q8B32), (CB2 or CB3, BF16_Q8)
-    if ((wfmt == QMV_W_MXFP4) ? afmt == QMV_A_BF16_Q8 : (afmt == QMV_A_BF16 || afmt == QMV_A_MXFP4))
+    // pairs: (MXFP4, BF16), (MXFP4, Q8B32), (MXFP4, MXFP4), (CB2 or CB3, Q8B32), (CB2 or CB3, BF16_Q8),
+    // (F8B128, F8B128)
+    if ((wfmt == QMV_W_F8B128) != (afmt == QMV_A_F8B128))
+        return QMV_EUNSUPPORTED;
+    if (wfmt == QMV_W_MXFP4 ? afmt == QMV_A_BF16_Q8 : (afmt == QMV_A_BF16 || afmt == QMV_A_MXFP4))
         return QMV_EUNSUPPORTED;
     if (top_k > kMaxTopK || K % 32 != 0 || K > kMaxK)
         return QMV_EUNSUPPORTED;
@@ -121,7 +125,7 @@ inline qmv_status_t validate(int wfmt, const void *codes, const void *scales, lo
     }
     const uintptr_t calign = (wfmt == QMV_W_CB2 && K % 64 != 0) ? 8 : (wfmt == QMV_W_CB3 ? 4 : 16);
     if (!aligned(codes, calign) || !aligned(x, 16) || !aligned(y, 4) ||
-        (wfmt != QMV_W_MXFP4 && !aligned(scales, 4)) || (xs && afmt == QMV_A_Q8B32 && !aligned(xs, 4)) ||
+        (wfmt != QMV_W_MXFP4 && !aligned(scales, 4)) || (xs && (afmt == QMV_A_Q8B32 || afmt == QMV_A_F8B128) && !aligned(xs, 4)) ||
         (ids && !aligned(ids, 4)))
         return QMV_EINVAL;
     // in-expert row offsets and output indices are 32-bit on the device
@@ -134,10 +138,10 @@ inline qmv_status_t validate(int wfmt, const void *codes, const void *scales, lo
 }
 
 // The checks of each entry point, in the order the entry point makes them.
-// x_scales is used only with QMV_A_Q8B32 and QMV_A_MXFP4.
+// x_scales is used only with QMV_A_Q8B32, QMV_A_MXFP4 and QMV_A_F8B128.
 inline const void *used_xs(int afmt, const void *x_scales)
 {
-    return afmt == QMV_A_Q8B32 || afmt == QMV_A_MXFP4 ? x_scales : nullptr;
+    return afmt == QMV_A_Q8B32 || afmt == QMV_A_MXFP4 || afmt == QMV_A_F8B128 ? x_scales : nullptr;
 }
 
 inline qmv_status_t check_dense(int wfmt, const void *codes, const void *scales, int afmt, const void *x,
@@ -386,7 +390,7 @@ inline const char *status_text(int status)
                                   "(token, slot) pairs and E <= 1023; top_k in [1,16], "
                                   "K % 32 == 0 and K <= 16384; "
                                   "pairs MXFP4+BF16, MXFP4+Q8B32, MXFP4+MXFP4, CB2/CB3+Q8B32, "
-                                  "CB2/CB3+BF16_Q8)";
+                                  "CB2/CB3+BF16_Q8, F8B128+F8B128)";
     case QMV_EHIP: return "the HIP runtime rejected the kernel launch";
     case QMV_ESCRATCH: return "the call needs more temporary memory than the allocation-free entry point's "
                               "fixed 64 MiB per GPU (M * top_k * N * 4 bytes with more than 4 tokens)";

@@ -1,0 +1,612 @@
+// qmv_k_f8.hip -- e4m3 weights with an fp32 scale per 128 x 128 block x e4m3
+// activations with an fp32 scale per 128, on the f16 matrix cores
+// (v_mfma_f32_16x16x32_f16): dense, gather, gate/up with SwiGLU, and the
+// combine of up to 4 tokens.
+//
+//     y = sum over blocks b of (sw_b * sx_b) * sum_128 e4m3 * e4m3
+//
+// Codes stay e4m3 in memory and LDS and are widened to f16 (which holds every
+// e4m3 value) in registers.  The f8f6f4 instructions would take them as they
+// are at twice the rate, but they add products eight at a time to 14 bits of
+// the largest: a block of normal values' codes came out 2e-6 of the sum of its
+// magnitudes off (1e-5 of the result), with f16 operands 2e-9.
+//
+// Four instructions (16 rows x 32 k of A, 32 k x 16 columns of B) form a
+// block's whole sum in fp32 from zero, which one multiply-add per output adds
+// to the result with the product of the block's two scales.  A lane holds 32
+// bytes of its row (column): lane (c, q) = lane 16 q + c takes chunks q and q +
+// 4 (16 bytes each) of row c's 128.  (A sum does not care which k a lane
+// holds, as long as both operands agree.)
+//
+// Times here are a kernel's own: its median in a trace of ten calls with three
+// sets of weights and vectors in turn.
+#include "qmv_routed.hpp"
+
+#include <type_traits>
+#include <utility>
+
+namespace qmv {
+
+constexpr int kF8Few = 16;           // vectors of a few-vector workgroup
+constexpr int kF8Waves = kRoutedWaves;
+constexpr int kF8Chunk = 64;         // vectors of a tile at most
+constexpr int kF8RF = 2;             // 16-row fragments per wave of a tile
+constexpr int kF8Block = 128;        // weights of a block, and code bytes
+
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+
+// A lane's 32 codes as operands: two chunks, four instructions' values.
+struct Wide {
+    f16x8 v[4];
+};
+
+__device__ __forceinline__ Wide widen(const u32x4 (&c)[2])
+{
+    Wide r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        u32x4 h;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t w = c[i >> 1][2 * (i & 1) + j];
+            h[2 * j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false));
+            h[2 * j + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true));
+        }
+        r.v[i] = __builtin_bit_cast(f16x8, h);
+    }
+    return r;
+}
+
+// The block sums of 16 rows x 16 columns.
+__device__ __forceinline__ f32x4 block_sum(const Wide &a, const Wide &b)
+{
+    f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.v[i], b.v[i], s, 0, 0, 0);
+    return s;
+}
+
+__device__ __forceinline__ void add_scaled(f32x4 &acc, f32x4 part, float s)
+{
+#pragma unroll
+    for (int k = 0; k < 4; ++k) acc[k] = __builtin_fmaf(part[k], s, acc[k]);
+}
+
+// ------------------------------------------------------------- many vectors
+// A tile is (expert, 128 weight rows; gate/up: 64 of each) against a chunk of
+// its vectors (up to 64), 4 waves of 2 x CF fragments each.  K goes in
+// units of one block.
+//
+// Codes are loaded as they lie -- 8 lanes take a row's 128 bytes, 8 rows a
+// load -- and turned into operand order by a pass through LDS (swz_chunk):
+//   codes of the rows   through a piece of LDS of the wave's own (LDS keeps a
+//                       wave's accesses in order: no barrier), two units ahead
+//                       in registers
+//   codes of the vectors  staged by all waves, double-buffered, one unit ahead
+//   scales              of the tile's block row(s) and of all the vectors,
+//                       staged once for all of K
+// One barrier per unit; two workgroups of 4 waves share a CU.
+//
+template <int... I, class Part>
+__device__ __forceinline__ void parts(std::integer_sequence<int, I...>, Part part)
+{
+    (part(std::integral_constant<int, I>{}), ...);
+}
+
+// Row tiles rt0 .. rt1 - 1 of expert e against nv vectors: pairs vecs[0..nv)
+// of a routed call, vectors vstart .. of a dense one (vecs null).
+template <int MODE, int CF>
+__device__ __forceinline__ void f8_tile_run(const Args &a, uint8_t *lds, int e, int rt0, int rt1,
+                                            const uint16_t *vecs, int vstart, int nv)
+{
+    constexpr int NW = kF8Waves, RF = kF8RF;
+    constexpr int RH = MODE == 1 ? RF / 2 : RF;      // output row fragments per wave
+    constexpr int TR = 16 * RH * NW;                 // output rows of a tile
+    constexpr int XU = (2 * CF + NW - 1) / NW;       // staged pieces (8 vectors x 128 bytes) per wave and unit
+    constexpr int XB = CF * 2048;                    // bytes of one vector buffer
+    constexpr int GB = CF < 2 ? 1 : 2, HG = CF / GB; // vector fragments read at a time; groups of them
+    int tid = threadIdx.x;
+    asm volatile("" : "+v"(tid));                    // (keeps the offsets below out of the caller's loop head)
+    const int lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    uint8_t *const lx = lds;                                      // [2][CF][16 vectors x 128 bytes]
+    uint8_t *const la = lds + 2 * kF8Chunk * 128 + w * (RF * 2048);     // [RF][16 rows x 128 bytes], this wave's
+    float *const lw = (float *)(lds + 2 * kF8Chunk * 128 + NW * RF * 2048);   // [MODE == 1 ? 2 : 1][KB]
+    const int c = lane & 15, q = lane >> 4;
+    const int lr = lane >> 3, lc = lane & 7;         // row and chunk of a load
+    const bool gather = vecs != nullptr;
+    const int N = a.N;
+    const int KB = a.units, U = a.K >> 4;            // blocks, 16-byte chunks of a row
+    float *const ls = lw + ((2 * KB + 3) & ~3);      // [KB][16][CF]
+
+    const __amdgpu_buffer_rsrc_t rc0 = buffer_rsrc(a.codes + e * a.expert_cb, a.expert_cb);
+    const __amdgpu_buffer_rsrc_t rc1 = buffer_rsrc((MODE == 1 ? a.codes2 : a.codes) + e * a.expert_cb, a.expert_cb);
+    // rows past N repeat the last one and are not stored
+    uint32_t oc[RF][2];
+    auto set_rows = [&](int row_base) {
+#pragma unroll
+        for (int f = 0; f < RF; ++f)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int n = min(row_base + 16 * RH * w + 16 * (MODE == 1 ? f % RH : f) + 8 * i + lr, N - 1);
+                oc[f][i] = (uint32_t)n * (uint32_t)a.rcb + 16u * lc;
+            }
+    };
+    // (chunks past the row's end read zeros: the bytes there are another row's)
+    auto load_a = [&](int u, u32x4 (&A)[RF][2]) {
+        const uint32_t so = 8 * u + lc < U ? 128u * u : kXPast;      // (oc < 2^31: the sum does not wrap)
+#pragma unroll
+        for (int f = 0; f < RF; ++f)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                A[f][i] = __builtin_amdgcn_raw_buffer_load_b128(MODE == 1 && f >= RH ? rc1 : rc0, oc[f][i] + so, 0, 0);
+    };
+    const int wst = swz_chunk(lr, lc);               // rows 8 further: + 1024, ^ 64
+    auto store_a = [&](const u32x4 (&A)[RF][2]) {
+#pragma unroll
+        for (int f = 0; f < RF; ++f) {
+            *(u32x4 *)(la + f * 2048 + wst) = A[f][0];
+            *(u32x4 *)(la + f * 2048 + 1024 + (wst ^ 64)) = A[f][1];
+        }
+    };
+
+    // staged vectors: piece p = vectors 8 p .. 8 p + 7; wave w takes pieces w, w + NW, ...
+    const int top_k = a.top_k;
+    const bool by_token = gather && !a.x_per_slot;
+    auto vec_row = [&](int v) -> uint32_t {
+        const int i = gather ? (int)vecs[v] : vstart + v;
+        return (uint32_t)(by_token ? i / top_k : i);
+    };
+    const int x_rows = gather && a.x_per_slot ? a.M * a.top_k : a.M;
+    const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(a.x, (long long)x_rows * a.x_vec_bytes);
+    uint32_t ox[XU];
+#pragma unroll
+    for (int k = 0; k < XU; ++k) {
+        const int v = 8 * (w + NW * k) + lr;
+        ox[k] = v < nv ? vec_row(v) * (uint32_t)a.x_vec_bytes + 16u * lc : kXPast;
+    }
+    auto load_x = [&](int u, u32x4 (&X)[XU]) {
+#pragma unroll
+        for (int k = 0; k < XU; ++k) {
+            const bool ok = 8 * u + lc < U && ox[k] != kXPast;
+            X[k] = __builtin_amdgcn_raw_buffer_load_b128(rx, ok ? ox[k] + 128u * u : kXPast, 0, 0);
+        }
+    };
+    auto store_x = [&](int buf, const u32x4 (&X)[XU]) {
+#pragma unroll
+        for (int k = 0; k < XU; ++k) {
+            const int p = w + NW * k;
+            if (2 * CF >= NW || w < 2 * CF)
+                *(u32x4 *)(lx + buf * XB + p * 1024 + (wst ^ ((p & 1) << 6))) = X[k];
+        }
+    };
+    // scales: the tile's rows lie in one block row
+    auto stage_rows = [&](int row_base) {
+        const float *const s0 = (const float *)(a.scales + e * a.expert_sb) + (size_t)(row_base / kF8Block) * KB;
+        const float *const s1 = (const float *)((MODE == 1 ? a.scales2 : a.scales) + e * a.expert_sb) +
+                                (size_t)(row_base / kF8Block) * KB;
+        if (tid < KB) {
+            lw[tid] = s0[tid];
+            if constexpr (MODE == 1) lw[KB + tid] = s1[tid];
+        }
+    };
+    auto stage_vecs = [&] {
+        const float *const xs = (const float *)a.xs;
+#pragma unroll 4
+        for (int t = tid; t < 16 * CF * KB; t += 64 * NW) {
+            const int v = t / KB, u = t - v * KB;
+            ls[(u * 16 + (v & 15)) * CF + (v >> 4)] = v < nv ? xs[(size_t)vec_row(v) * KB + u] : 0.0f;
+        }
+    };
+    const int rd = c * 128 + 16 * (q ^ ((c >> 1) & 7));         // chunk q of row c; chunk q + 4: ^ 64
+    const bool vec4 = (N & 3) == 0 && ((uintptr_t)a.y & 15) == 0;
+
+    // While unit u multiplies, its codes stand in LDS and those of units u + 1
+    // and u + 2 are on their way to A[(u + 1) % 2], A[u % 2] and X likewise:
+    // every load has a whole unit's time before its registers are needed.
+    u32x4 A0[RF][2], A[2][RF][2], X[2][XU];
+    auto first_loads = [&](int row_base) {
+        set_rows(row_base);
+        load_a(0, A0);
+        load_x(0, X[0]);
+        load_x(1, X[1]);
+        load_a(1, A[1]);
+        load_a(2, A[0]);
+    };
+    first_loads(rt0 * TR);
+    for (int rt = rt0; rt < rt1; ++rt) {
+        const int row_base = rt * TR;
+        if (rt == rt0) stage_vecs();
+        stage_rows(row_base);
+        store_a(A0);
+        store_x(0, X[0]);
+        f32x4 acc[RF][CF];
+#pragma unroll
+        for (int f = 0; f < RF; ++f)
+#pragma unroll
+            for (int g = 0; g < CF; ++g) acc[f][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        __syncthreads();
+        auto unit = [&](auto HALF, int u) {
+            constexpr int h = decltype(HALF)::value;            // the unit's vector buffer too
+            u32x4 F[RF][2], B[2][GB][2];
+            auto read_b = [&](int i, u32x4 (&b)[GB][2]) {
+#pragma unroll
+                for (int g = 0; g < GB; ++g)
+#pragma unroll
+                    for (int s = 0; s < 2; ++s)
+                        b[g][s] = *(const u32x4 *)(lx + h * XB + (i * GB + g) * 2048 + (rd ^ (64 * s)));
+            };
+#pragma unroll
+            for (int f = 0; f < RF; ++f)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) F[f][s] = *(const u32x4 *)(la + f * 2048 + (rd ^ (64 * s)));
+            read_b(0, B[0]);
+            const float sw0 = lw[u], sw1 = MODE == 1 ? lw[KB + u] : 0.0f;
+            load_x(u + 2, X[h]);
+            asm volatile("" ::: "memory");                      // (the next unit's codes go where these were)
+            store_a(A[h ^ 1]);
+            load_a(u + 3, A[h ^ 1]);
+            Wide W[RF];
+#pragma unroll
+            for (int f = 0; f < RF; ++f) W[f] = widen(F[f]);
+            auto part = [&](auto IDX) {
+                constexpr int i = decltype(IDX)::value;
+                __builtin_amdgcn_sched_barrier(0);
+                if constexpr (i + 1 < HG) read_b(i + 1, B[(i + 1) & 1]);
+                f32x4 sum[RF][GB];
+                Wide b[GB];
+                float sx[GB];
+#pragma unroll
+                for (int g = 0; g < GB; ++g) b[g] = widen(B[i & 1][g]);
+#pragma unroll
+                for (int g = 0; g < GB; ++g) sx[g] = ls[(u * 16 + c) * CF + i * GB + g];
+#pragma unroll
+                for (int g = 0; g < GB; ++g)
+#pragma unroll
+                    for (int f = 0; f < RF; ++f) sum[f][g] = block_sum(W[f], b[g]);
+#pragma unroll
+                for (int g = 0; g < GB; ++g)
+#pragma unroll
+                    for (int f = 0; f < RF; ++f)
+                        add_scaled(acc[f][i * GB + g], sum[f][g], (MODE == 1 && f >= RH ? sw1 : sw0) * sx[g]);
+                // (keeps the products on this side of the barrier)
+#pragma unroll
+                for (int g = 0; g < GB; ++g)
+#pragma unroll
+                    for (int f = 0; f < RF; ++f) asm volatile("" : "+v"(acc[f][i * GB + g]));
+            };
+            parts(std::make_integer_sequence<int, HG>{}, part);
+            store_x(h ^ 1, X[h ^ 1]);
+            __syncthreads();
+        };
+        int u = 0;
+        for (; u + 1 < KB; u += 2) {
+            unit(std::integral_constant<int, 0>{}, u);
+            unit(std::integral_constant<int, 1>{}, u + 1);
+        }
+        if (u < KB) unit(std::integral_constant<int, 0>{}, u);
+
+        // the next tile's first loads go out before this tile's results
+        if (rt + 1 < rt1) first_loads(row_base + TR);
+        // lane (c, q) holds rows 4 q .. 4 q + 3 of vector c of each fragment
+        int vc = c;
+        asm volatile("" : "+v"(vc));                                // (the rows' addresses are formed here, not kept)
+#pragma unroll
+        for (int g = 0; g < CF; ++g) {
+            const int v = 16 * g + vc;
+            if (v < nv) {
+                float *const yr = a.y + (size_t)(gather ? (int)vecs[v] : vstart + v) * N;
+#pragma unroll
+                for (int f = 0; f < RH; ++f) {
+                    const int n0 = row_base + 16 * RH * w + 16 * f + 4 * q;
+                    float r[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        r[k] = MODE == 1 ? swiglu(acc[f][g][k], acc[f + RF - RH][g][k]) : acc[f][g][k];
+                    if (n0 < N) {
+                        if (vec4) {
+                            *(float4 *)(yr + n0) = make_float4(r[0], r[1], r[2], r[3]);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (n0 + k < N) yr[n0 + k] = r[k];
+                        }
+                    }
+                }
+            }
+        }
+    }
+}
+
+// A workgroup takes a run of up to bt_chunk row tiles of one item.  Workgroup
+// b runs on XCD b % 8; the runs (item-major) are dealt to the XCDs in
+// contiguous parts, so that an XCD's L2 holds the vectors of a few experts,
+// and an expert's second chunk finds its weights there.
+template <int MODE>
+__global__ __launch_bounds__(64 * kF8Waves, 2) void qmv_f8_tile_kernel(const Args a)
+{
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    constexpr int CHUNK = kF8Chunk, TR = 16 * kF8RF * kF8Waves / (MODE == 1 ? 2 : 1);
+    uint16_t *const list = (uint16_t *)lds;           // [CHUNK]
+    uint8_t *const buf = lds + 2 * CHUNK;
+    const int runs = (a.bt_row_tiles + a.bt_chunk - 1) / a.bt_chunk;   // per item
+    int item = -1, rt0 = 0, rt1 = 0;
+    auto pick = [&](int items) {
+        const int all = items * runs, per_xcd = (all + 7) / 8, i = blockIdx.x >> 3;
+        const int r = i < per_xcd ? (int)(blockIdx.x & 7) * per_xcd + i : all;
+        if (r < all) {
+            item = r / runs;
+            rt0 = (r - item * runs) * a.bt_chunk;
+            rt1 = min(rt0 + a.bt_chunk, a.bt_row_tiles);
+        }
+        return item;
+    };
+    int e = 0, nv, vstart = 0;
+    const bool gather = a.ids != nullptr;
+    if (gather) {
+        // (a call without any id in [0, E) still has its zero rows: one item)
+        const int P = a.M * a.top_k;
+        const RoutedItem it = routed_item<CHUNK>(a.ids, P, a.E, (int *)buf, list, [&](int items) { return pick(max(items, 1)); });
+        if (item < 0) return;
+        e = it.e;
+        nv = it.nv;
+        routed_zero_rows(a, item, max(it.items, 1), rt0 * TR, min(rt1 * TR, a.N));
+        if (nv == 0) return;
+    } else {
+        if (pick((a.M + CHUNK - 1) / CHUNK) < 0) return;
+        vstart = item * CHUNK;
+        nv = min(CHUNK, a.M - vstart);
+    }
+    const uint16_t *const vecs = gather ? list : nullptr;
+    if (nv > 32)
+        f8_tile_run<MODE, 4>(a, buf, e, rt0, rt1, vecs, vstart, nv);
+    else if (nv > 16)
+        f8_tile_run<MODE, 2>(a, buf, e, rt0, rt1, vecs, vstart, nv);
+    else
+        f8_tile_run<MODE, 1>(a, buf, e, rt0, rt1, vecs, vstart, nv);
+}
+
+// -------------------------------------------------------------- few vectors
+// Up to 16 vectors of an expert (a dense matrix), or (MODE 2, the combine) a
+// token's slots, each with its expert, against one tile of 16 rows.  The call
+// waits for its weight bytes, so the 4 waves of a workgroup split K -- wave w
+// takes blocks w, w + 4, ... -- and each has up to kF8Ahead blocks of its rows
+// on their way from the start; the vectors and the scales are staged in LDS
+// once.  The waves' partial tiles are summed in wave order.  Columns past the
+// last vector repeat one (nothing of them is stored).
+constexpr int kF8Ahead = 4;
+
+// Bytes from vector to vector of the staged codes (whole blocks, and 16 more
+// so that the 16 vectors of a read lie in different bank groups), and floats
+// from vector to vector of the staged scales.
+__host__ __device__ constexpr int f8_x_pitch(int KB) { return KB * 128 + 16; }
+__host__ __device__ constexpr int f8_s_pitch(int KB) { return KB | 1; }
+
+template <int MODE>
+__global__ __launch_bounds__(64 * kF8Waves) void qmv_f8_few_kernel(const Args a)
+{
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    constexpr int NW = kF8Waves, H = MODE == 1 ? 2 : 1, D = kF8Ahead;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int c = lane & 15, q = lane >> 4, lr = lane >> 3, lc = lane & 7;
+    const int KB = a.units, U = a.K >> 4;
+    const int XP = f8_x_pitch(KB), SP = f8_s_pitch(KB);
+    const int N = a.N;
+    const bool gather = MODE != 2 && a.ids != nullptr;
+    const int P = gather ? a.M * a.top_k : a.M;
+
+    uint16_t *const list = (uint16_t *)lds;                    // [kF8Few]
+    uint8_t *const la = lds + 64 + w * (H * 2048);             // this wave's weight pieces; its partial sums
+    uint8_t *const lx = lds + 64 + NW * H * 2048;              // [vectors] x XP
+    float *const lxs = (float *)(lx + a.bt_vmax * XP);         // [vectors] x SP
+    float *const ls = lxs + a.bt_vmax * SP;                    // [H or slots] x SP
+
+    // ---- which expert, vectors and row tiles
+    int e = 0, nv = 1, v0 = 0, rt = blockIdx.x;
+    int ids_lane = 0;
+    float rw_lane = 0.0f;
+    if constexpr (MODE == 2) {
+        // lane j holds slot j's expert and weight
+        if (lane < a.top_k) {
+            ids_lane = a.ids[blockIdx.y * a.top_k + lane];
+            rw_lane = a.route_w[blockIdx.y * a.top_k + lane];
+        }
+    } else if (!gather) {
+        v0 = blockIdx.y * kF8Few;
+        nv = min(kF8Few, a.M - v0);
+    } else if (P <= 64) {
+        // workgroup row blockIdx.y: pair blockIdx.y's expert, if no earlier
+        // pair has it (up to 64 pairs: one lane each)
+        const int id = lane < P ? a.ids[lane] : -1, y = blockIdx.y % P;
+        const int chunk = blockIdx.y / P;                      // of bt_vmax pairs of the expert
+        e = __builtin_amdgcn_readlane(id, y);
+        if ((unsigned)e >= (unsigned)a.E) {
+            if (chunk == 0)
+                for (int n = rt * 16 + tid; n < min(rt * 16 + 16, N); n += 64 * NW) a.y[(size_t)y * N + n] = 0.0f;
+            return;
+        }
+        const unsigned long long m = __ballot(id == e);
+        if (__ffsll((long long)m) - 1 != y) return;
+        // (bit counts are unsigned: as int before anything is subtracted)
+        const int r = (int)__popcll(m & ((1ull << lane) - 1ull)) - chunk * a.bt_vmax;
+        const int left = (int)__popcll(m) - chunk * a.bt_vmax;
+        if (left <= 0) return;
+        nv = min(left, a.bt_vmax);
+        if ((m >> lane & 1) && r >= 0 && r < a.bt_vmax) list[r] = (uint16_t)lane;    // (every wave the same)
+    } else {
+        int item = -1;
+        const RoutedItem it = routed_item<kF8Few>(a.ids, P, a.E, (int *)(lds + 64), list, [&](int items) {
+            const int all = max(items, 1) * a.bt_row_tiles, per_xcd = (all + 7) / 8, i = blockIdx.x >> 3;
+            const int r = i < per_xcd ? (int)(blockIdx.x & 7) * per_xcd + i : all;
+            if (r < all) {
+                item = r / a.bt_row_tiles;
+                rt = r - item * a.bt_row_tiles;
+            }
+            return item;
+        });
+        if (item < 0) return;
+        e = it.e;
+        nv = it.nv;
+        routed_zero_rows(a, item, max(it.items, 1), rt * 16, min(rt * 16 + 16, N));
+        if (nv == 0) return;
+        __syncthreads();                                       // (the counts lie where the staging goes)
+    }
+    const bool routed = MODE == 2 || gather;
+    const int top_k = a.top_k;
+    const int x_rows = routed && a.x_per_slot ? a.M * top_k : a.M;
+    auto pair_of = [&](int v) { return MODE == 2 ? (int)blockIdx.y * top_k + v : gather ? (int)list[v] : v0 + v; };
+    auto vec_row = [&](int v) -> uint32_t {
+        const int p = pair_of(v);
+        return (uint32_t)(routed && !a.x_per_slot ? p / top_k : p);
+    };
+
+    // ---- groups of slots (MODE 2: bt_vmax at a time; else one pass)
+    const int slots = MODE == 2 ? top_k : 1, per = MODE == 2 ? a.bt_vmax : 1;
+    const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(a.x, (long long)x_rows * a.x_vec_bytes);
+    f32x4 tot = {0.0f, 0.0f, 0.0f, 0.0f};
+    u32x4 A[D][H][2];
+    const int row0 = rt * 16;
+    uint32_t oc[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) oc[i] = (uint32_t)min(row0 + 8 * i + lr, N - 1) * (uint32_t)a.rcb + 16u * lc;
+    for (int s0 = 0; s0 < slots; s0 += per) {
+        const int ns = min(per, slots - s0), total = ns * KB;
+        auto load_a = [&](int i, u32x4 (&R)[H][2]) {
+            const int g = w + NW * i;
+            const int slot = MODE == 2 ? g / KB : 0, u = g - slot * KB;
+            int ee = e;
+            long long size = a.expert_cb;
+            if constexpr (MODE == 2) {
+                ee = __builtin_amdgcn_readlane(ids_lane, g < total ? s0 + slot : 0);
+                if ((unsigned)ee >= (unsigned)a.E) ee = 0, size = 0;           // reads zeros
+            }
+            const uint32_t so = g < total && 8 * u + lc < U ? 128u * u : kXPast;
+#pragma unroll
+            for (int h = 0; h < H; ++h) {                                      // (nt: read once)
+                const __amdgpu_buffer_rsrc_t rc = buffer_rsrc((h ? a.codes2 : a.codes) + ee * a.expert_cb, size);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) R[h][k] = __builtin_amdgcn_raw_buffer_load_b128(rc, oc[k] + so, 0, 2);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < D; ++i) load_a(i, A[i]);
+        // the vectors (MODE 2: those of the group's slots), and all scales
+        const int vecs = MODE == 2 ? (a.x_per_slot ? ns : 1) : nv;
+        for (int t = tid; t < vecs * 8 * KB; t += 64 * NW) {
+            const int v = t / (8 * KB), b = t - v * 8 * KB;
+            const uint32_t o = vec_row(MODE == 2 ? s0 + v : v) * (uint32_t)a.x_vec_bytes + 16u * b;
+            *(u32x4 *)(lx + v * XP + 16 * b) =
+                __builtin_amdgcn_raw_buffer_load_b128(rx, b < U ? o : kXPast, 0, 0);
+        }
+        for (int t = tid; t < vecs * KB; t += 64 * NW) {
+            const int v = t / KB, u = t - v * KB;
+            lxs[v * SP + u] = ((const float *)a.xs)[(size_t)vec_row(MODE == 2 ? s0 + v : v) * KB + u];
+        }
+        const size_t block_row = (size_t)(row0 / kF8Block) * KB;
+        for (int k = 0; k < (MODE == 2 ? ns : H); ++k) {
+            int ee = e;
+            if constexpr (MODE == 2) {
+                ee = __builtin_amdgcn_readlane(ids_lane, s0 + k);
+                if ((unsigned)ee >= (unsigned)a.E) ee = 0;                     // (unused)
+            }
+            const uint8_t *const base = MODE == 1 && k == 1 ? a.scales2 : a.scales;
+            if (tid < KB) ls[k * SP + tid] = ((const float *)(base + ee * a.expert_sb))[block_row + tid];
+        }
+        __syncthreads();
+
+        f32x4 acc[H];
+#pragma unroll
+        for (int h = 0; h < H; ++h) acc[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        const int wst = swz_chunk(lr, lc), rd = c * 128 + 16 * (q ^ ((c >> 1) & 7));
+        const int vc = MODE == 2 ? 0 : (c < nv ? c : nv - 1);                  // columns past nv repeat
+        const int mine = total > w ? (total - w + NW - 1) / NW : 0;            // this wave's blocks
+        for (int i0 = 0; i0 < mine; i0 += D) {
+#pragma unroll
+            for (int d = 0; d < D; ++d) {
+                const int i = i0 + d;
+                if (i < mine) {
+                    const int g = w + NW * i;
+                    const int slot = MODE == 2 ? g / KB : 0, u = g - slot * KB;
+                    const int v = MODE == 2 ? (a.x_per_slot ? slot : 0) : vc;
+                    const float sx = lxs[v * SP + u];
+                    u32x4 B[2];
+                    B[0] = *(const u32x4 *)(lx + v * XP + 128 * u + 16 * q);
+                    B[1] = *(const u32x4 *)(lx + v * XP + 128 * u + 64 + 16 * q);
+                    const Wide b = widen(B);
+#pragma unroll
+                    for (int h = 0; h < H; ++h) {
+                        *(u32x4 *)(la + h * 2048 + wst) = A[d][h][0];
+                        *(u32x4 *)(la + h * 2048 + 1024 + (wst ^ 64)) = A[d][h][1];
+                    }
+                    asm volatile("" ::: "memory");                             // (written before read: one wave's LDS)
+                    load_a(i + D, A[d]);
+#pragma unroll
+                    for (int h = 0; h < H; ++h) {
+                        const float sw = ls[(MODE == 2 ? slot : h) * SP + u];
+                        u32x4 F[2];
+                        F[0] = *(const u32x4 *)(la + h * 2048 + rd);
+                        F[1] = *(const u32x4 *)(la + h * 2048 + (rd ^ 64));
+                        add_scaled(acc[h], block_sum(widen(F), b), sw * sx);
+                    }
+                    asm volatile("" ::: "memory");
+                    if constexpr (MODE == 2) {
+                        if ((g + NW) / KB != slot || i + 1 == mine) {          // this wave's last block of the slot
+                            const float rw = __uint_as_float(
+                                __builtin_amdgcn_readlane(__float_as_uint(rw_lane), s0 + slot));
+                            // (a slot without an expert is 0 whatever its vector holds)
+                            const bool have = (unsigned)__builtin_amdgcn_readlane(ids_lane, s0 + slot) < (unsigned)a.E;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) tot[k] = __builtin_fmaf(rw, have ? acc[0][k] : 0.0f, tot[k]);
+                            acc[0] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+                        }
+                    }
+                }
+            }
+        }
+        if constexpr (MODE == 2) {
+            if (s0 + per < slots) {
+                __syncthreads();                           // (the next group's staging)
+                continue;
+            }
+            acc[0] = tot;
+        }
+#pragma unroll
+        for (int h = 0; h < H; ++h) *(f32x4 *)(la + h * 2048 + 16 * lane) = acc[h];
+        __syncthreads();
+        // lane (c, q): rows 4 q .. 4 q + 3 of vector c, summed over the waves
+        if (w == 0 && c < nv) {
+            f32x4 r[H];
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                r[h] = acc[h];
+#pragma unroll
+                for (int i = 1; i < NW; ++i) r[h] += *(const f32x4 *)(la + (i * H + h) * 2048 + 16 * lane);
+            }
+            float *const yr = a.y + (size_t)(MODE == 2 ? (int)blockIdx.y : pair_of(c)) * N;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int n = row0 + 4 * q + k;
+                if (n < N) yr[n] = MODE == 1 ? swiglu(r[0][k], r[H - 1][k]) : r[0][k];
+            }
+        }
+    }
+}
+
+// [plain, gate/up, combine]
+extern const void *const kTableF8Few[3];
+const void *const kTableF8Few[3] = {
+    (const void *)&qmv_f8_few_kernel<0>,
+    (const void *)&qmv_f8_few_kernel<1>,
+    (const void *)&qmv_f8_few_kernel<2>,
+};
+
+// [plain, gate/up]
+extern const void *const kTableF8Tile[2];
+const void *const kTableF8Tile[2] = {
+    (const void *)&qmv_f8_tile_kernel<0>,
+    (const void *)&qmv_f8_tile_kernel<1>,
+};
+
+}  // namespace qmv

@@ -12,16 +12,11 @@
 //
 // Times here are a kernel's own: its median in a trace of ten calls with three
 // sets of weights and vectors in turn.
-#include "qmv_device.hpp"
+#include "qmv_routed.hpp"
 
 #include <type_traits>
 
 namespace qmv {
-
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-constexpr uint32_t kXPast = 0x80000000u;       // >= every buffer size: reads zeros
 
 // The product with the lane's scale bytes in byte OP of sa and of sb.
 template <int OP>
@@ -59,7 +54,6 @@ __device__ __forceinline__ f32x4 mfma_mx4_op(u32x4 a, u32x4 b, f32x4 c, uint32_t
 // rows leave more of a tile's time to its start (the ids' counts, the vector
 // list, the scales): 512 tokens x top-4 of 32, gate/up 2880 -> 2880, 282 MB in
 // 93 us, 3.0 TB/s (nontemporal loads of the codes took an eighth more).
-__device__ __forceinline__ int swz_chunk(int row, int chunk) { return row * 128 + 16 * (chunk ^ ((row >> 1) & 7)); }
 
 // A row's 16 scale bytes of a slab as loaded: five whole dwords around them.
 struct ScaleSeg {
@@ -106,125 +100,9 @@ __device__ __forceinline__ u32x4 seg_order(const ScaleSeg &s, uint32_t o, int n)
                  perm(h23, h01, 0x07060302u)};
 }
 
-// The routed calls' work: an expert's pairs in chunks of at most CHUNK.
-// Every workgroup counts the pairs per expert itself (LDS atomics on whole
-// numbers: the same counts everywhere), so the grid needs no device-wide
-// knowledge: item i is the i-th (expert, chunk) of the experts in order.
 constexpr int kMx4Few = 16;          // few kernel
 constexpr int kMx4Waves = 4;
 constexpr int kMx4RF = 2;            // 16-row fragments per wave of a tile
-
-struct Mx4Item {
-    int e;               // expert
-    int nv;              // vectors of the chunk (0: no pair has an id in [0, E))
-    int items;           // items of the call
-};
-
-// Inclusive sum over the lanes of a wave.
-__device__ __forceinline__ int wave_scan(int v)
-{
-    v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);   // row_shr 1, 2, 4, 8: within 16 lanes
-    v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
-    v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);   // lane 15 of rows 0, 2 to rows 1, 3
-    v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);   // lane 31 to rows 2, 3
-    return v;
-}
-
-// cnt: 1024 + 8 words of LDS.  `pick` maps the number of items to this
-// workgroup's item (or -1); the chunk's pairs go to list.  ids: thread t
-// looks at ids t, t + 256, ...  Every wave finds the item by itself.
-template <int CHUNK, class Pick>
-__device__ __forceinline__ Mx4Item mx4_item(const int32_t *ids, int P, int E, int *cnt, uint16_t *list, Pick pick)
-{
-    int tid = threadIdx.x;
-    asm volatile("" : "+v"(tid));
-    const int lane = tid & 63, w = tid >> 6;
-    int *const info = cnt + 1024;
-    int idv[32];
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-        if (j * 256 < P) idv[j] = ids[min(tid + j * 256, P - 1)];
-    *(int4 *)(cnt + 4 * tid) = make_int4(0, 0, 0, 0);
-    if (tid == 0) info[4] = 0;
-    __syncthreads();
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-        if (j * 256 < P) {
-            if (tid + j * 256 < P && (unsigned)idv[j] < (unsigned)E) atomicAdd(&cnt[idv[j]], 1);
-        }
-    __syncthreads();
-    // lane l: experts 16 l .. 16 l + 15 (those past E have no pairs)
-    int c[16], n = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int4 v = *(const int4 *)(cnt + 16 * lane + 4 * i);
-        c[4 * i] = v.x, c[4 * i + 1] = v.y, c[4 * i + 2] = v.z, c[4 * i + 3] = v.w;
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) n += (c[i] + CHUNK - 1) / CHUNK;
-    int before = wave_scan(n);
-    const int items = __builtin_amdgcn_readlane(before, 63);
-    before -= n;
-    const int item = pick(items);
-    Mx4Item it = {0, 0, items};
-    if (item < 0 || item >= items) return it;
-    const unsigned long long owner = __ballot(item >= before && item < before + n);
-    int e = 0, chunk = 0, total = 0;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int k = (c[i] + CHUNK - 1) / CHUNK;
-        if (item >= before && item < before + k) e = 16 * lane + i, chunk = item - before, total = c[i];
-        before += k;
-    }
-    const int o = __ffsll((long long)owner) - 1;
-    it.e = __builtin_amdgcn_readlane(e, o);
-    chunk = __builtin_amdgcn_readlane(chunk, o);
-    total = __builtin_amdgcn_readlane(total, o);
-    const int nch = (total + CHUNK - 1) / CHUNK;
-    const int cs = (total + nch - 1) / nch;           // equal chunks
-    it.nv = min(cs, total - chunk * cs);
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 32; ++j)
-        if (j * 256 < P) m |= (uint32_t)(idv[j] == it.e && tid + j * 256 < P) << j;
-    if (nch == 1) {
-        // one chunk: the order of its pairs changes no result
-        for (; m; m &= m - 1) list[atomicAdd(&info[4], 1)] = (uint16_t)(tid + 256 * (__ffs(m) - 1));
-    } else {
-        // the pairs of e in (thread, round) order, the same in every
-        // workgroup: this chunk's ranks
-        n = (int)__popc(m);
-        int rank = wave_scan(n);
-        if (lane == 63) info[w] = rank;
-        __syncthreads();
-        for (int i = 0; i < 4; ++i)
-            if (i < w) rank += info[i];
-        rank -= n + chunk * cs;
-        for (; m; m &= m - 1, ++rank)
-            if (rank >= 0 && rank < it.nv) list[rank] = (uint16_t)(tid + 256 * (__ffs(m) - 1));
-    }
-    __syncthreads();
-    return it;
-}
-
-// The rows [n0, n1) of pairs whose id is outside [0, E) are zeros: of `items`
-// items, item i takes the pairs i, i + items, ...
-__device__ __forceinline__ void mx4_zero_rows(const Args &a, int item, int items, int n0, int n1)
-{
-    int tid = threadIdx.x;
-    asm volatile("" : "+v"(tid));
-    const int lane = tid & 63, w = tid >> 6, P = a.M * a.top_k;
-    for (int p0 = item + items * 16 * w; p0 < P; p0 += items * 16 * kMx4Waves) {
-        const int p = p0 + items * (lane & 15);
-        const bool bad = lane < 16 && p < P && (unsigned)a.ids[min(p, P - 1)] >= (unsigned)a.E;
-        for (unsigned long long m = __ballot(bad); m; m &= m - 1) {
-            float *const yr = a.y + (size_t)(p0 + items * (__ffsll((long long)m) - 1)) * a.N;
-            for (int n = n0 + lane; n < n1; n += 64) yr[n] = 0.0f;
-        }
-    }
-}
 
 // Bytes from row to row of the staged scales of J slabs.
 __host__ __device__ constexpr int mx4_scale_pitch(int J) { return 16 * (J | 1); }
@@ -539,11 +417,11 @@ __global__ __launch_bounds__(64 * kMx4Waves, 2) void qmv_mx4_tile_kernel(const A
     if (gather) {
         // (a call without any id in [0, E) still has its zero rows: one item)
         const int P = a.M * a.top_k;
-        const Mx4Item it = mx4_item<CHUNK>(a.ids, P, a.E, (int *)buf, list, [&](int items) { return pick(max(items, 1)); });
+        const RoutedItem it = routed_item<CHUNK>(a.ids, P, a.E, (int *)buf, list, [&](int items) { return pick(max(items, 1)); });
         if (item < 0) return;
         e = it.e;
         nv = it.nv;
-        mx4_zero_rows(a, item, max(it.items, 1), rt0 * TR, min(rt1 * TR, a.N));
+        routed_zero_rows(a, item, max(it.items, 1), rt0 * TR, min(rt1 * TR, a.N));
         if (nv == 0) return;
     } else {
         if (pick((a.M + CHUNK - 1) / CHUNK) < 0) return;
@@ -634,7 +512,7 @@ __global__ __launch_bounds__(64 * kMx4Waves) void qmv_mx4_few_kernel(const Args 
         if ((m >> lane & 1) && r >= 0 && r < a.bt_vmax) list[r] = (uint16_t)lane;    // (every wave the same)
     } else {
         int item = -1;
-        const Mx4Item it = mx4_item<kMx4Few>(a.ids, P, a.E, (int *)(lds + 64), list, [&](int items) {
+        const RoutedItem it = routed_item<kMx4Few>(a.ids, P, a.E, (int *)(lds + 64), list, [&](int items) {
             const int all = max(items, 1) * a.bt_row_tiles, per_xcd = (all + 7) / 8, i = blockIdx.x >> 3;
             const int r = i < per_xcd ? (int)(blockIdx.x & 7) * per_xcd + i : all;
             if (r < all) {
@@ -646,7 +524,7 @@ __global__ __launch_bounds__(64 * kMx4Waves) void qmv_mx4_few_kernel(const Args 
         if (item < 0) return;
         e = it.e;
         nv = it.nv;
-        mx4_zero_rows(a, item, max(it.items, 1), rt * 16, min(rt * 16 + 16, N));
+        routed_zero_rows(a, item, max(it.items, 1), rt * 16, min(rt * 16 + 16, N));
         if (nv == 0) return;
         __syncthreads();                                       // (the counts lie where the staging goes)
     }

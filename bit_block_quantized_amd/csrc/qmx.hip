@@ -1,132 +1,16 @@
 // qmx.hip -- libqmx.so (include/qmx.h): residual + RMS norm, router, and the
-// MXFP4 / int8 block quantizers, with their C ABI.
+// MXFP4 / int8 / e4m3 block quantizers, with their C ABI.
 //
 // Everything here is bound by the bytes it moves (or, for a few tokens, by a
 // launch): one pass over the data, 16-byte accesses, rows held in registers
 // between the reduction and the output.  Times are a kernel's own: its median in
 // a trace of ten calls with three sets of inputs in turn.
-#include <hip/hip_runtime.h>
-#include <stdint.h>
-
 #include "qmx_host.hpp"
+#include "qmx_values.hpp"
 
 namespace {
 
 using namespace qmx_host;
-
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-
-// ------------------------------------------------------------ 8 values a lane
-// Eight consecutive values of a 32- or 16-bit type as loaded: 32 or 16 bytes.
-struct Raw8 {
-    uint4 a, b;
-};
-
-// (the type is the same for the whole launch: the branches are uniform)
-__device__ __forceinline__ Raw8 load_raw8(const void *base, size_t i, int type)
-{
-    Raw8 r;
-    r.b = make_uint4(0, 0, 0, 0);
-    if (type == QMX_T_F32) {
-        const uint4 *p = (const uint4 *)((const float *)base + i);
-        r.a = p[0];
-        r.b = p[1];
-    } else {
-        r.a = *(const uint4 *)((const uint16_t *)base + i);
-    }
-    return r;
-}
-
-__device__ __forceinline__ void raw_to_f32(const Raw8 &r, int type, float (&v)[8])
-{
-    const uint32_t w[8] = {r.a.x, r.a.y, r.a.z, r.a.w, r.b.x, r.b.y, r.b.z, r.b.w};
-    if (type == QMX_T_F32) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = __uint_as_float(w[j]);
-    } else if (type == QMX_T_BF16) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            v[2 * j] = __uint_as_float(w[j] << 16);
-            v[2 * j + 1] = __uint_as_float(w[j] & 0xFFFF0000u);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const f16x2 h = __builtin_bit_cast(f16x2, w[j]);
-            v[2 * j] = (float)h[0];
-            v[2 * j + 1] = (float)h[1];
-        }
-    }
-}
-
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b)
-{
-    const bf16x2 h = {(__bf16)a, (__bf16)b};                  // nearest, ties to even
-    return __builtin_bit_cast(uint32_t, h);
-}
-
-__device__ __forceinline__ uint32_t pack_f16(float a, float b)
-{
-    const f16x2 h = {(_Float16)a, (_Float16)b};
-    return __builtin_bit_cast(uint32_t, h);
-}
-
-__device__ __forceinline__ void store8(void *base, size_t i, int type, const float (&v)[8])
-{
-    if (type == QMX_T_F32) {
-        float4 *p = (float4 *)((float *)base + i);
-        p[0] = make_float4(v[0], v[1], v[2], v[3]);
-        p[1] = make_float4(v[4], v[5], v[6], v[7]);
-    } else if (type == QMX_T_BF16) {
-        *(uint4 *)((uint16_t *)base + i) =
-            make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-    } else {
-        *(uint4 *)((uint16_t *)base + i) =
-            make_uint4(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]), pack_f16(v[4], v[5]), pack_f16(v[6], v[7]));
-    }
-}
-
-// Values first, first + step, ... of a row of K values of any type, the last
-// one again past the end (P loads with no branch between them, all in flight
-// at once); a value's bits to its value.
-template <int P>
-__device__ __forceinline__ void load_bits(const void *base, size_t row, int first, int step, int K, int type,
-                                          uint32_t (&v)[P])
-{
-    if (type == QMX_T_F32) {
-        const uint32_t *const p = (const uint32_t *)base + row;
-#pragma unroll
-        for (int i = 0; i < P; ++i) v[i] = p[min(first + i * step, K - 1)];
-    } else {
-        const uint16_t *const p = (const uint16_t *)base + row;
-#pragma unroll
-        for (int i = 0; i < P; ++i) v[i] = p[min(first + i * step, K - 1)];
-    }
-}
-
-template <int P>
-__device__ __forceinline__ void bits_to_f32(const uint32_t (&b)[P], int type, float (&v)[P])
-{
-    if (type == QMX_T_F16) {
-#pragma unroll
-        for (int i = 0; i < P; ++i) v[i] = (float)__builtin_bit_cast(_Float16, (uint16_t)b[i]);
-    } else {
-        const int up = type == QMX_T_BF16 ? 16 : 0;
-#pragma unroll
-        for (int i = 0; i < P; ++i) v[i] = __uint_as_float(b[i] << up);
-    }
-}
-
-__device__ __forceinline__ void store1(void *base, size_t i, int type, float v)
-{
-    if (type == QMX_T_F32)
-        ((float *)base)[i] = v;
-    else if (type == QMX_T_BF16)
-        ((uint16_t *)base)[i] = __builtin_bit_cast(uint16_t, (__bf16)v);
-    else
-        ((uint16_t *)base)[i] = __builtin_bit_cast(uint16_t, (_Float16)v);
-}
 
 // ------------------------------------------------------------ block formats
 // Four neighbouring lanes hold a block (8 values each).  The largest
@@ -203,8 +87,20 @@ __device__ __forceinline__ uint2 q8_codes(const float (&v)[8], _Float16 d16)
     return q;
 }
 
-// Write eight values at flat index i (a multiple of 8) of an output in FMT;
-// the four lanes of a block call it together.
+// Write eight values at k (a multiple of 8) of row `row` of K as e4m3 blocks;
+// every lane of the row of 16 calls it, those past the row's end (k >= K) with
+// zeros.
+__device__ __forceinline__ void put8_f8(void *y, void *ys, size_t row, int k, int K, const float (&v)[8])
+{
+    const float d = f8_scale(row16_max(amax_bits8(v)));
+    if (k < K) {
+        *(uint2 *)((uint8_t *)y + row * K + k) = f8_codes(v, d);
+        if ((k & 127) == 0) ((float *)ys)[row * ((K + 127) / 128) + k / 128] = d;
+    }
+}
+
+// Write eight values at flat index i (a multiple of 8) of an output in another
+// FMT; the four lanes of a block call it together.
 template <int FMT>
 __device__ __forceinline__ void put8(void *y, void *ys, size_t i, const float (&v)[8])
 {
@@ -297,8 +193,9 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void qmx_rmsnorm_kernel(const No
 #pragma unroll
     for (int p = 0; p < P; ++p) {
         const int k = 8 * (p * T + tid);
+        float o[8] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f, 0.0f};
         if (k < a.K) {
-            float o[8], w[8];
+            float w[8];
             if (a.w) {
                 raw_to_f32(wr[p], a.wt, w);
             } else {
@@ -307,8 +204,9 @@ __global__ __launch_bounds__(T == 64 ? 256 : T) void qmx_rmsnorm_kernel(const No
             }
 #pragma unroll
             for (int j = 0; j < 8; ++j) o[j] = (float)((double)h[p][j] * r * (double)w[j]);
-            put8<FMT>(a.y, a.ys, base + k, o);
+            if constexpr (FMT != QMX_F8B128) put8<FMT>(a.y, a.ys, base + k, o);
         }
+        if constexpr (FMT == QMX_F8B128) put8_f8(a.y, a.ys, (size_t)row, k, a.K, o);
     }
 }
 
@@ -472,6 +370,98 @@ __global__ __launch_bounds__(256) void qmx_dequantize_kernel(const void *c, cons
             }
         }
     }
+}
+
+// e4m3 blocks of rows of K: 16 lanes take a block of 128 (the row's last one may
+// be short), F8_UNROLL blocks each in flight, a fixed grid's stride on.  A row
+// and block follow from the ones before by addition: one division a thread.
+constexpr int kF8Unroll = 4, kF8Groups = 4096;
+
+struct F8Blocks {
+    long long row;
+    int kb, step_kb, KB;
+    long long step_row;
+
+    __device__ __forceinline__ F8Blocks(int K, long long first, long long step)
+    {
+        KB = (K + 127) / 128;
+        row = first / KB;
+        kb = (int)(first - row * KB);
+        step_row = step / KB;
+        step_kb = (int)(step - step_row * KB);
+    }
+    __device__ __forceinline__ void next()
+    {
+        row += step_row;
+        kb += step_kb;
+        if (kb >= KB) kb -= KB, ++row;
+    }
+};
+
+__global__ __launch_bounds__(256) void qmx_quantize_f8_kernel(const void *x, int xt, void *y, void *ys,
+                                                              long long rows, int K)
+{
+    constexpr int UN = kF8Unroll;
+    const int c = 8 * (threadIdx.x & 15);
+    F8Blocks at(K, (long long)blockIdx.x * 16 + (threadIdx.x >> 4), (long long)gridDim.x * 16);
+    // (the loop's condition is the wave's: all lanes take part in a block's maximum)
+    while (__any(at.row < rows)) {
+        Raw8 r[UN];
+        long long row[UN];
+        int k[UN];
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            row[u] = at.row;
+            k[u] = at.row < rows ? at.kb * 128 + c : K;
+            r[u].a = r[u].b = make_uint4(0, 0, 0, 0);
+            if (k[u] < K) r[u] = load_raw8(x, (size_t)row[u] * K + k[u], xt);
+            at.next();
+        }
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            float v[8];
+            raw_to_f32(r[u], xt, v);
+            put8_f8(y, ys, (size_t)row[u], k[u], K, v);
+        }
+    }
+}
+
+__global__ __launch_bounds__(256) void qmx_dequantize_f8_kernel(const void *c, const void *cs, int yt, void *y,
+                                                                long long rows, int K)
+{
+    constexpr int UN = kF8Unroll;
+    const int l = 8 * (threadIdx.x & 15);
+    F8Blocks at(K, (long long)blockIdx.x * 16 + (threadIdx.x >> 4), (long long)gridDim.x * 16);
+    while (at.row < rows) {
+        uint2 r[UN];
+        float d[UN];
+        size_t i[UN];
+        bool have[UN];
+#pragma unroll
+        for (int u = 0; u < UN; ++u) {
+            const int k = at.kb * 128 + l;
+            have[u] = at.row < rows && k < K;
+            i[u] = (size_t)at.row * K + k;
+            if (have[u]) {
+                r[u] = *(const uint2 *)((const uint8_t *)c + i[u]);
+                d[u] = ((const float *)cs)[(size_t)at.row * at.KB + at.kb];
+            }
+            at.next();
+        }
+#pragma unroll
+        for (int u = 0; u < UN; ++u)
+            if (have[u]) {
+                float v[8];
+                f8_values(r[u], d[u], v);
+                store8(y, i[u], yt, v);
+            }
+    }
+}
+
+long long f8_groups(long long rows, int K)
+{
+    const long long KB = (K + 127) / 128, most = (long long)kF8Groups * 16 * kF8Unroll;
+    return rows > most / KB ? kF8Groups : (rows * KB + 16 * kF8Unroll - 1) / (16 * kF8Unroll);
 }
 
 // ------------------------------------------------------------------- router
@@ -655,6 +645,7 @@ QMX_API qmv_status_t qmx_rmsnorm(qmx_type_t xtype, const void *x, qmx_type_t rty
     const void *fn = K % 8 != 0          ? norm_odd_kernel(K, threads, rows)
                      : fmt == QMX_BF16   ? norm_kernel<QMX_BF16>(M, K, threads, rows)
                      : fmt == QMX_Q8B32  ? norm_kernel<QMX_Q8B32>(M, K, threads, rows)
+                     : fmt == QMX_F8B128 ? norm_kernel<QMX_F8B128>(M, K, threads, rows)
                                          : norm_kernel<QMX_MXFP4>(M, K, threads, rows);
     return go_rows(fn, a, rows, threads, stream);
 }
@@ -676,8 +667,12 @@ QMX_API qmv_status_t qmx_quantize(qmx_type_t xtype, const void *x, qmx_fmt_t fmt
     const qmv_status_t s = check_blocks(xtype, x, fmt, codes, scales, rows, K);
     if (s != QMV_OK)
         return s;
-    long long pieces = rows * (K / 8);
     int xt = (int)xtype;
+    if (fmt == QMX_F8B128) {
+        void *args[] = {&x, &xt, &codes, &scales, &rows, &K};
+        return go((const void *)&qmx_quantize_f8_kernel, f8_groups(rows, K), 256, args, stream);
+    }
+    long long pieces = rows * (K / 8);
     const void *fn = fmt == QMX_MXFP4 ? (const void *)&qmx_quantize_kernel<QMX_MXFP4>
                                       : (const void *)&qmx_quantize_kernel<QMX_Q8B32>;
     void *args[] = {&x, &xt, &codes, &scales, &pieces};
@@ -690,8 +685,12 @@ QMX_API qmv_status_t qmx_dequantize(qmx_fmt_t fmt, const void *codes, const void
     const qmv_status_t s = check_blocks(ytype, y, fmt, codes, scales, rows, K);
     if (s != QMV_OK)
         return s;
-    long long pieces = rows * (K / 8);
     int yt = (int)ytype;
+    if (fmt == QMX_F8B128) {
+        void *args[] = {&codes, &scales, &yt, &y, &rows, &K};
+        return go((const void *)&qmx_dequantize_f8_kernel, f8_groups(rows, K), 256, args, stream);
+    }
+    long long pieces = rows * (K / 8);
     const void *fn = fmt == QMX_MXFP4 ? (const void *)&qmx_dequantize_kernel<QMX_MXFP4>
                                       : (const void *)&qmx_dequantize_kernel<QMX_Q8B32>;
     void *args[] = {&codes, &scales, &yt, &y, &pieces};

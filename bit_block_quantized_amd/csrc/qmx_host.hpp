@@ -14,6 +14,9 @@ constexpr int kMaxTopK = 16;
 
 inline bool aligned(const void *p, uintptr_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
 inline bool type_ok(int t) { return t >= QMX_T_F32 && t <= QMX_T_F16; }
+// the formats of blocks (3 names none)
+inline bool blocks_ok(int f) { return f == QMX_Q8B32 || f == QMX_MXFP4 || f == QMX_F8B128; }
+inline uintptr_t scale_bytes(int f) { return f == QMX_Q8B32 ? 2 : f == QMX_F8B128 ? 4 : 1; }
 inline uintptr_t type_bytes(int t) { return t == QMX_T_F32 ? 4 : 2; }
 
 inline qmv_status_t check_rmsnorm(int xtype, const void *x, int rtype, const void *residual,
@@ -22,8 +25,8 @@ inline qmv_status_t check_rmsnorm(int xtype, const void *x, int rtype, const voi
 {
     if (!x || !y || !residual != !residual_out || M <= 0 || K <= 0 || !(eps >= 0.0f))
         return QMV_EINVAL;
-    if (!type_ok(xtype) || (residual && !type_ok(rtype)) || (weight && !type_ok(wtype)) || fmt < QMX_BF16 ||
-        fmt > QMX_MXFP4 || K > kMaxNormK || (fmt != QMX_BF16 && K % 32 != 0))
+    if (!type_ok(xtype) || (residual && !type_ok(rtype)) || (weight && !type_ok(wtype)) ||
+        (fmt != QMX_BF16 && !blocks_ok(fmt)) || K > kMaxNormK || (fmt != QMX_BF16 && K % 32 != 0))
         return QMV_EUNSUPPORTED;
     if ((fmt == QMX_BF16) != !y_scales)
         return QMV_EINVAL;
@@ -31,7 +34,7 @@ inline qmv_status_t check_rmsnorm(int xtype, const void *x, int rtype, const voi
     if (!aligned(x, vec ? 16 : type_bytes(xtype)) || !aligned(y, vec ? 16 : 2) ||
         (residual && (!aligned(residual, vec ? 16 : type_bytes(rtype)) ||
                       !aligned(residual_out, vec ? 16 : type_bytes(rtype)))) ||
-        (weight && !aligned(weight, vec ? 16 : type_bytes(wtype))) || (fmt == QMX_Q8B32 && !aligned(y_scales, 2)))
+        (weight && !aligned(weight, vec ? 16 : type_bytes(wtype))) || (y_scales && !aligned(y_scales, scale_bytes(fmt))))
         return QMV_EINVAL;
     return QMV_OK;
 }
@@ -56,9 +59,9 @@ inline qmv_status_t check_blocks(int type, const void *values, int fmt, const vo
     if (!values || !codes || !scales || rows <= 0 || K <= 0)
         return QMV_EINVAL;
     // (rows bound: the byte count of 32-bit values stays below 2^62)
-    if (!type_ok(type) || (fmt != QMX_Q8B32 && fmt != QMX_MXFP4) || K % 32 != 0 || rows > (1LL << 60) / K)
+    if (!type_ok(type) || !blocks_ok(fmt) || K % 32 != 0 || rows > (1LL << 60) / K)
         return QMV_EUNSUPPORTED;
-    if (!aligned(values, 16) || !aligned(codes, 16) || (fmt == QMX_Q8B32 && !aligned(scales, 2)))
+    if (!aligned(values, 16) || !aligned(codes, 16) || !aligned(scales, scale_bytes(fmt)))
         return QMV_EINVAL;
     return QMV_OK;
 }

@@ -11,8 +11,9 @@ Argument marshalling only, as for the products: there is no CPU fallback.
     y = qmv.qmv_gather_moe_combine("mxfp4", dc, ds, ids, w, a, as_)
 
 Formats by name: "mxfp4" (uint8 codes [..][K/2], uint8 E8M0 scales
-[..][K/32]), "q8" (int8 codes [..][K], float16 scales [..][K/32]) and, for
-the norm's output, "bf16".  Tensors are C-contiguous and on one GPU; each
+[..][K/32]), "q8" (int8 codes [..][K], float16 scales [..][K/32]), "f8"
+(float8_e4m3fn codes [..][K], float32 scales [..][ceil(K/128)]) and, for the
+norm's output, "bf16".  Tensors are C-contiguous and on one GPU; each
 call runs on that GPU's current stream (or ``stream``).
 """
 from __future__ import annotations
@@ -30,7 +31,8 @@ __all__ = ["qmx_rmsnorm", "qmx_router", "qmx_quantize", "qmx_dequantize", "qmx_s
 QMX_LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqmx.so")
 
 _TYPE = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-_FMT = {"bf16": 0, "q8": 1, "mxfp4": 2}
+_FMT = {"bf16": 0, "q8": 1, "mxfp4": 2, "f8": 4}
+_BLOCKS = ("mxfp4", "q8", "f8")
 _SCORING = {"softmax": 0, "sigmoid": 1}
 
 _lib = None
@@ -98,14 +100,17 @@ def _code_spec(fmt, lead, K):
     """((codes dtype, shape), (scales dtype, shape)) of rows of K values."""
     if fmt == "mxfp4":
         return (torch.uint8, lead + (K // 2,)), (torch.uint8, lead + (K // 32,))
+    if fmt == "f8":
+        return (_q.F8_DT, lead + (K,)), (torch.float32, lead + (_q._blocks128(K),))
     return (torch.int8, lead + (K,)), (torch.float16, lead + (K // 32,))
 
 
 def _out(t, name, spec, device):
-    """The caller's output, checked, or a new one."""
+    """The caller's output, checked, or a new one (of the first of several types)."""
+    dtypes = spec[0] if isinstance(spec[0], tuple) else (spec[0],)
     if t is None:
-        return torch.empty(spec[1], dtype=spec[0], device=device)
-    _tensor(t, name, (spec[0],), device, spec[1])
+        return torch.empty(spec[1], dtype=dtypes[0], device=device)
+    _tensor(t, name, dtypes, device, spec[1])
     return t
 
 
@@ -127,8 +132,8 @@ def qmx_rmsnorm(x, weight=None, eps=1e-5, residual=None, fmt="bf16", y=None, y_s
     returns (y, y_scales, residual_out).
 
     h = x + residual, residual_out = h in the residual's type, y = h /
-    sqrt(mean(h^2) + eps) * weight in ``fmt`` ("bf16", or "q8" / "mxfp4" codes
-    with y_scales).  y_scales is None for "bf16", residual_out without a
+    sqrt(mean(h^2) + eps) * weight in ``fmt`` ("bf16", or "q8" / "mxfp4" / "f8"
+    codes with y_scales).  y_scales is None for "bf16", residual_out without a
     residual; ``residual_out`` may be ``residual`` itself.  x, residual and
     weight are float32, bfloat16 or float16 each."""
     f = _choice(fmt, _FMT, "fmt")
@@ -189,10 +194,10 @@ def qmx_router(logits, top_k, scoring="softmax", normalize=True, scale=1.0, ids=
 
 
 def qmx_quantize(x, fmt="mxfp4", codes=None, scales=None, stream=None):
-    """x [..][K] (float32, bfloat16 or float16; K % 32 == 0) in blocks of 32:
-    (codes, scales) in "mxfp4" or "q8"."""
-    if fmt not in ("mxfp4", "q8"):
-        raise ValueError(f"fmt is {fmt!r}, expected one of ('mxfp4', 'q8')")
+    """x [..][K] (float32, bfloat16 or float16; K % 32 == 0) in blocks of 32
+    ("f8": 128): (codes, scales) in "mxfp4", "q8" or "f8"."""
+    if fmt not in _BLOCKS:
+        raise ValueError(f"fmt is {fmt!r}, expected one of {_BLOCKS}")
     _tensor(x, "x", _TYPE)
     rows, K = _rows(x, "x")
     _q._ints(K)
@@ -207,11 +212,11 @@ def qmx_quantize(x, fmt="mxfp4", codes=None, scales=None, stream=None):
 
 def qmx_dequantize(codes, scales, fmt="mxfp4", dtype=torch.bfloat16, y=None, stream=None):
     """The values [..][K] that (codes, scales) stand for, in ``dtype``."""
-    if fmt not in ("mxfp4", "q8"):
-        raise ValueError(f"fmt is {fmt!r}, expected one of ('mxfp4', 'q8')")
+    if fmt not in _BLOCKS:
+        raise ValueError(f"fmt is {fmt!r}, expected one of {_BLOCKS}")
     if dtype not in _TYPE:
         raise ValueError(f"dtype is {dtype}, expected one of {tuple(_TYPE)}")
-    _tensor(codes, "codes", (torch.uint8 if fmt == "mxfp4" else torch.int8,))
+    _tensor(codes, "codes", _q.F8_DT if fmt == "f8" else (torch.uint8 if fmt == "mxfp4" else torch.int8,))
     rows, n = _rows(codes, "codes")
     K = 2 * n if fmt == "mxfp4" else n
     _q._ints(K)

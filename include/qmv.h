@@ -45,6 +45,15 @@
  *                these codebooks are those tables minus 0.5, and times 0.5
  *                with the second zero taken as -3.)
  *
+ *   QMV_W_F8B128 codes  uint8 [E][N][K]     e4m3: sign, four exponent bits
+ *                                            (bias 7), three mantissa bits;
+ *                                            no infinity, 0x7F and 0xFF are
+ *                                            NaN, the largest value is 448.
+ *                scales fp32 [E][ceil(N/128)][ceil(K/128)]  one scale for
+ *                                            each 128 rows x 128 weights;
+ *                                            the last block of either
+ *                                            direction may be short.
+ *
  * Activations:
  *   QMV_A_BF16   x   bf16 [V][K], x_scales unused (pass NULL).
  *   QMV_A_Q8B32  x   int8 [V][K] with x_scales fp16 [V][K/32]: activation k
@@ -75,8 +84,18 @@
  *                    outputs of its row or vector NaN.  (E8M0 arrays are read
  *                    in whole aligned 4-byte words: up to 3 bytes before the
  *                    first and behind the last byte are read with them.)
+ *   QMV_A_F8B128 x  uint8 [V][K] of e4m3 codes with x_scales fp32
+ *                    [V][ceil(K/128)], a scale for each 128 of k (qmx.h has
+ *                    the quantizer and a norm that write it).  A block's 128
+ *                    products are summed on the matrix cores in fp32, the sum
+ *                    is multiplied by the fp32 product of the two scales and
+ *                    added in fp32.  (So an output need not be finite, or may
+ *                    lose bits, where that product passes fp32's range; a NaN
+ *                    code or scale makes the outputs of its rows or vector
+ *                    NaN.)
  * Supported pairs: (MXFP4, BF16), (MXFP4, Q8B32), (MXFP4, MXFP4),
- * (CB2, Q8B32), (CB3, Q8B32), (CB2, BF16_Q8), (CB3, BF16_Q8).  With
+ * (CB2, Q8B32), (CB3, Q8B32), (CB2, BF16_Q8), (CB3, BF16_Q8),
+ * (F8B128, F8B128).  With
  * (MXFP4, Q8B32) every 32-weight block shares one E8M0 weight scale and one activation scale (both are per 32 of
  * k), and the block's sum of e2m1 x int8 products is formed exactly (it is
  * the integer dot product of the 2*e2m1 values with q, times the weight
@@ -131,8 +150,8 @@
 extern "C" {
 #endif
 
-typedef enum { QMV_W_MXFP4 = 0, QMV_W_CB2 = 1, QMV_W_CB3 = 2 } qmv_wfmt_t;
-typedef enum { QMV_A_BF16 = 0, QMV_A_Q8B32 = 1, QMV_A_BF16_Q8 = 2, QMV_A_MXFP4 = 4 } qmv_afmt_t;
+typedef enum { QMV_W_MXFP4 = 0, QMV_W_CB2 = 1, QMV_W_CB3 = 2, QMV_W_F8B128 = 3 } qmv_wfmt_t;
+typedef enum { QMV_A_BF16 = 0, QMV_A_Q8B32 = 1, QMV_A_BF16_Q8 = 2, QMV_A_MXFP4 = 4, QMV_A_F8B128 = 5 } qmv_afmt_t;
 
 typedef enum {
     QMV_OK = 0,

@@ -6,11 +6,11 @@
  *                   bf16 or directly in an activation format of the products
  *   qmx_router      a token's top_k experts and their weights: the
  *                   expert_ids and route_weights that the gathers read
- *   qmx_quantize    values -> MXFP4 or int8 blocks (activations or weights)
- *   qmx_dequantize  MXFP4 or int8 blocks -> values
+ *   qmx_quantize    values -> MXFP4, int8 or e4m3 blocks
+ *   qmx_dequantize  MXFP4, int8 or e4m3 blocks -> values
  *
  * ------------------------------------------------------------------ formats
- * Blocks are 32 consecutive values of a row; codes and scales are separate
+ * Blocks are 32 (e4m3: 128) consecutive values of a row; codes and scales are separate
  * arrays in the layouts of qmv.h.
  *
  *   QMX_MXFP4  codes uint8 [rows][K/2] (two e2m1 nibbles per byte, the even
@@ -31,6 +31,14 @@
  *              quantizer of qmv.h (QMV_A_BF16_Q8) in fp32:
  *                d16 = fp16(amax / 127), code = clamp(rint(v * (1 / d16)),
  *                -127, 127), 0 where d16 is 0 or infinite.
+ *              A block that holds a NaN or an infinity gets scale NaN and
+ *              codes 0.
+ *   QMX_F8B128 codes e4m3 [rows][K], scales fp32 [rows][ceil(K/128)]: the
+ *              activations of QMV_A_F8B128; the row's last block may be
+ *              short.  With amax = max |v| of a block:
+ *                d    = max(amax / 448, 2^-126), the quotient rounded to fp32,
+ *                code = v / d rounded to the nearest e4m3 value, ties to even
+ *              (of the exact quotient: no rounding before).
  *              A block that holds a NaN or an infinity gets scale NaN and
  *              codes 0.
  *   QMX_BF16   bf16 [rows][K], no scales (the norm's output only).
@@ -58,7 +66,7 @@ extern "C" {
 #endif
 
 typedef enum { QMX_T_F32 = 0, QMX_T_BF16 = 1, QMX_T_F16 = 2 } qmx_type_t;
-typedef enum { QMX_BF16 = 0, QMX_Q8B32 = 1, QMX_MXFP4 = 2 } qmx_fmt_t;
+typedef enum { QMX_BF16 = 0, QMX_Q8B32 = 1, QMX_MXFP4 = 2, QMX_F8B128 = 4 } qmx_fmt_t;
 typedef enum { QMX_SOFTMAX = 0, QMX_SIGMOID = 1 } qmx_scoring_t;
 
 /*
@@ -76,7 +84,7 @@ typedef enum { QMX_SOFTMAX = 0, QMX_SIGMOID = 1 } qmx_scoring_t;
  *              other outputs overlap no input.
  *   weight     wtype [K] or NULL (all ones)
  *   y, y_scales  the output in `fmt`; y_scales NULL exactly for QMX_BF16
- * 1 <= K <= 16384; QMX_Q8B32 and QMX_MXFP4 need K % 32 == 0.  eps >= 0.
+ * 1 <= K <= 16384; QMX_Q8B32, QMX_MXFP4 and QMX_F8B128 need K % 32 == 0.  eps >= 0.
  */
 qmv_status_t qmx_rmsnorm(qmx_type_t xtype, const void *x, qmx_type_t rtype, const void *residual,
                          void *residual_out, qmx_type_t wtype, const void *weight, float eps,
@@ -103,7 +111,7 @@ qmv_status_t qmx_router(qmx_type_t ltype, const void *logits, int M, int E, int 
                         float *weights, hipStream_t stream);
 
 /*
- * Values -> blocks (QMX_MXFP4 or QMX_Q8B32); x is xtype [rows][K] with
+ * Values -> blocks (QMX_MXFP4, QMX_Q8B32 or QMX_F8B128); x is xtype [rows][K] with
  * K % 32 == 0.  rows * K may pass 2^32 (an expert projection of any size).
  */
 qmv_status_t qmx_quantize(qmx_type_t xtype, const void *x, qmx_fmt_t fmt, void *codes,
