@@ -75,10 +75,11 @@ extern const void *const kTableMx4Wide[1];
 }
 
 // e4m3 x e4m3 with a scale per block of 128 (qmv_k_f8.hip): [plain, gate/up,
-// combine], [plain, gate/up].
+// combine], [plain, gate/up], dense.
 namespace qmv {
 extern const void *const kTableF8Few[3];
 extern const void *const kTableF8Tile[2];
+extern const void *const kTableF8Wide[1];
 }
 
 namespace qmv {
@@ -731,7 +732,7 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
                                                                                                   : QMV_EHIP;
 }
 
-LdsLimit g_f8_lds[2], g_f8_few_lds[3];
+LdsLimit g_f8_lds[2], g_f8_few_lds[3], g_f8_wide_lds;
 
 // LDS of a tile workgroup: the chunk's list, two buffers of vector codes (chunk
 // x 128 bytes), the waves' weight pieces (128 rows x 128 bytes), and the scales
@@ -760,6 +761,24 @@ qmv_status_t launch_f8(const void *codes, const void *scales, const void *codes2
     a.expert_sb = (long long)((N + 127) / 128) * a.rsb;
     const int mode = route_w ? 2 : codes2 ? 1 : 0;
     const int pairs = gather ? M * top_k : M;
+    // 256 x 128 tiles once they fill more than half of the CUs and most of their
+    // vectors exist (wide and, after it, the tile kernel's 128 x 64: 7168 -> 7168:
+    // 512 vectors (112 tiles) 84 and 83, 1024 100 and 156; 7168 -> 2048: 2048
+    // (128 tiles) 84 and 81, 4096 108 and 153; 7168 -> 40960: 64 (160 tiles) 96 and 87,
+    // 128 105 and 125).
+    const long long wide_tiles = (long long)((N + 255) / 256) * ((M + 127) / 128);
+    if (!gather && M > 64 && 2 * wide_tiles > cu_count()) {
+        const int lds = 2 * (256 + 128) * 128 + 2 * 128 * 4;
+        a.bt_row_tiles = (N + 255) / 256;
+        a.bt_vmax = 8;
+        a.bt_tiles = (int)wide_tiles;
+        a.bt_per_xcd = (a.bt_tiles + 7) / 8;
+        if (g_f8_wide_lds.set(kTableF8Wide[0], lds) != hipSuccess)
+            return QMV_EHIP;
+        void *kargs[] = {&a};
+        return hipLaunchKernel(kTableF8Wide[0], dim3((unsigned)(8 * a.bt_per_xcd)), dim3(512), kargs, lds, stream) ==
+                       hipSuccess ? QMV_OK : QMV_EHIP;
+    }
     // the few kernel's LDS: weight pieces, the vectors' codes and scales, the rows' scales
     const int h = mode == 1 ? 2 : 1, xp = KB * 128 + 16, sp = 4 * (KB | 1);
     auto few_lds = [&](int vectors) { return 64 + 4 * h * 2048 + vectors * (xp + sp) + h * sp; };

@@ -1,15 +1,15 @@
 // qmv_k_f8.hip -- e4m3 weights with an fp32 scale per 128 x 128 block x e4m3
 // activations with an fp32 scale per 128, on the f16 matrix cores
-// (v_mfma_f32_16x16x32_f16): dense, gather, gate/up with SwiGLU, and the
+// (v_mfma_f32_16x16x32_bf16): dense, gather, gate/up with SwiGLU, and the
 // combine of up to 4 tokens.
 //
 //     y = sum over blocks b of (sw_b * sx_b) * sum_128 e4m3 * e4m3
 //
-// Codes stay e4m3 in memory and LDS and are widened to f16 (which holds every
+// Codes stay e4m3 in memory and LDS and are widened to bf16 (which holds every
 // e4m3 value) in registers.  The f8f6f4 instructions would take them as they
 // are at twice the rate, but they add products eight at a time to 14 bits of
 // the largest: a block of normal values' codes came out 2e-6 of the sum of its
-// magnitudes off (1e-5 of the result), with f16 operands 2e-9.
+// magnitudes off (1e-5 of the result), with bf16 operands 2e-9.
 //
 // Four instructions (16 rows x 32 k of A, 32 k x 16 columns of B) form a
 // block's whole sum in fp32 from zero, which one multiply-add per output adds
@@ -33,12 +33,11 @@ constexpr int kF8Chunk = 64;         // vectors of a tile at most
 constexpr int kF8RF = 2;             // 16-row fragments per wave of a tile
 constexpr int kF8Block = 128;        // weights of a block, and code bytes
 
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 // A lane's 32 codes as operands: two chunks, four instructions' values.
 struct Wide {
-    f16x8 v[4];
+    bf16x8 v[4];
 };
 
 __device__ __forceinline__ Wide widen(const u32x4 (&c)[2])
@@ -50,10 +49,10 @@ __device__ __forceinline__ Wide widen(const u32x4 (&c)[2])
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const uint32_t w = c[i >> 1][2 * (i & 1) + j];
-            h[2 * j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false));
-            h[2 * j + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true));
+            h[2 * j] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false));
+            h[2 * j + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true));
         }
-        r.v[i] = __builtin_bit_cast(f16x8, h);
+        r.v[i] = __builtin_bit_cast(bf16x8, h);
     }
     return r;
 }
@@ -63,7 +62,7 @@ __device__ __forceinline__ f32x4 block_sum(const Wide &a, const Wide &b)
 {
     f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) s = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.v[i], b.v[i], s, 0, 0, 0);
+    for (int i = 0; i < 4; ++i) s = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a.v[i], b.v[i], s, 0, 0, 0);
     return s;
 }
 
@@ -593,6 +592,271 @@ __global__ __launch_bounds__(64 * kF8Waves) void qmv_f8_few_kernel(const Args a)
         }
     }
 }
+
+// ------------------------------------------------------------- wide dense
+// A dense matrix against many vectors is bound by the matrix cores, beside them
+// by the vector ALUs, which widen the operands and scale the block sums, and by
+// the chip's power.  The two units run side by side with the 32 x 32
+// instruction (a product and six vector instructions: 41 cycles of a SIMD with
+// two waves, the product alone 33), hardly with the 16 x 16 one (27 and 17 for
+// half the product and three).  So tiles of 256 rows x 128 vectors, 4 x 2 waves
+// of 64 x 64, in fragments of 32 x 32: lane (n, k) = lane 32 k + n holds
+// chunks k, k + 2, k + 4, k + 6 of row (column) n's 128 bytes, eight
+// instructions' values, and after them rows 8 i + 4 k .. of column n in
+// registers 4 i .. .
+//
+// Both operands' codes go from memory into LDS without passing registers, a
+// block ahead, one load for every second product: given out together they hold
+// up the products behind them (833 us, 903 together, for the 8192 vectors
+// below).  A fragment is widened chunk by chunk into the registers that the one
+// before has left, and its sums are scaled and added while the next one's
+// products run.  One barrier a block, where the last of its codes is read.
+//
+// 8192 vectors, 7168 -> 7168: 713 us a call, 1.18 PFLOP/s, in calls one after
+// another up to 833 (at 1.6 GHz: the power limit); a library's product of bf16
+// matrices of these sizes takes 640, of f16 677.  16 x 16 fragments staged
+// through registers, 256 x 192 tiles: 910; 64 x 96 a wave: 919.
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// A chunk's 16 codes: two instructions' values.
+__device__ __forceinline__ void widen_chunk(u32x4 c, bf16x8 &lo, bf16x8 &hi)
+{
+    u32x4 h[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        h[i >> 1][2 * (i & 1)] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], 1.0f, false));
+        h[i >> 1][2 * (i & 1) + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], 1.0f, true));
+    }
+    lo = __builtin_bit_cast(bf16x8, h[0]);
+    hi = __builtin_bit_cast(bf16x8, h[1]);
+}
+
+// Keeps what forms x here: without it the compiler moves products, conversions
+// and additions to their results' first use, with all their operands held.
+template <class T> __device__ __forceinline__ void pin(T &x) { asm volatile("" : "+v"(x)); }
+
+constexpr int kF8WideRows = 256;
+constexpr int kF8WideCF = 2;         // 32-vector fragments per wave
+constexpr int kF8WideVecs = 64 * kF8WideCF;
+
+__device__ __forceinline__ void f8_wide_tile(const Args &a, uint8_t *lds, int row0, int vec0)
+{
+    constexpr int NWC = 2, NW = 8, RF = 2, CF = kF8WideCF;
+    constexpr int BR = kF8WideRows, BC = kF8WideVecs;   // tile: rows, vectors
+    constexpr int AB = BR * 128, XB = BC * 128;             // bytes of a block's codes
+    constexpr int PA = BR / 8 / NW, PX = BC / 8 / NW;       // staged pieces (8 rows x 128 bytes) a wave
+    typedef __attribute__((address_space(3))) void lds_t;
+    uint8_t *const lx = lds + 2 * AB;                       // [2][XB], behind [2][AB]
+    float *const ls = (float *)(lds + 2 * (AB + XB));       // [2][BC]
+
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wr = w / NWC, wc = w % NWC;
+    const int n = lane & 31, hk = lane >> 5;
+    const int KB = a.units, U = a.K >> 4;
+
+    float acc[RF][CF][16];
+#pragma unroll
+    for (int f = 0; f < RF; ++f)
+#pragma unroll
+        for (int g = 0; g < CF; ++g)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[f][g][i] = 0.0f;
+
+    // wave w stages pieces w, w + NW, ... of each operand; lane l's 16 bytes go
+    // to byte 16 l of the piece, which is the place of chunk l % 8 ^ (row / 2 %
+    // 8) of its row; rows past N and vectors past M lie past the buffers'
+    // ends and read zeros, and so do chunks past the row's end
+    const __amdgpu_buffer_rsrc_t rc = buffer_rsrc(a.codes, a.expert_cb);
+    const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(a.x, (long long)a.M * a.x_vec_bytes);
+    const int lr = 8 * w + (lane >> 3), lc = (lane & 7) ^ (lr >> 1 & 7);
+    const uint32_t oa = (uint32_t)(row0 + lr) * (uint32_t)a.rcb + 16u * lc;
+    const uint32_t ox = (uint32_t)(vec0 + lr) * (uint32_t)a.x_vec_bytes + 16u * lc;
+    const uint32_t step = 8u * NW * (uint32_t)a.rcb;         // (rcb and x_vec_bytes are both K)
+    const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(a.xs, (long long)a.M * KB * 4);
+    const uint32_t os = (uint32_t)(vec0 + tid) * (uint32_t)KB * 4u;
+    uint32_t ta = 0, tx = 0;
+    // piece p of block u: PA of the rows, PX of the vectors, one of these' scales, one a lane
+    auto stage = [&](int u, int h, int p) {
+        if (p == 0) ta = 8 * u + lc < U ? oa + 128u * u : kXPast;
+        if (p == PA) tx = 8 * u + lc < U ? ox + 128u * u : kXPast;
+        if (p < PA)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rc, (lds_t *)(lds + h * AB + (w + NW * p) * 1024), 16, ta, p * step, 0, 0);
+        else if (p < PA + PX)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_t *)(lx + h * XB + (w + NW * (p - PA)) * 1024), 16, tx,
+                                                     (p - PA) * step, 0, 0);
+        else if (p == PA + PX && w < BC / 64)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_t *)(ls + h * BC + 64 * w), 4, u < KB ? os + 4u * u : kXPast, 0, 0, 0);
+    };
+    auto stage_all = [&](int u, int h) {
+#pragma unroll
+        for (int p = 0; p <= PA + PX; ++p) stage(u, h, p);
+    };
+    // (the wave's rows lie in one block row)
+    const float *const swp = (const float *)a.scales + (size_t)(min(row0 + 64 * wr, a.N - 1) / kF8Block) * KB;
+
+    const int rd = n * 128 + 16 * (hk ^ (n >> 1 & 7));
+    const int ra = wr * RF * 4096 + rd, rb = 2 * AB + wc * CF * 4096 + rd;
+    // chunk 2 j + hk of the lane's row, of its column
+    auto read_a = [&](int h, int f, int j) { return *(const u32x4 *)(lds + (ra ^ (32 * j)) + h * AB + f * 4096); };
+    auto read_b = [&](int h, int g, int j) { return *(const u32x4 *)(lds + (rb ^ (32 * j)) + h * XB + g * 4096); };
+    const float *const lsn = ls + 32 * CF * wc + n;
+
+    bf16x8 W[RF][8], B[8];
+    stage_all(0, 0);
+    float sw = swp[0];
+    __builtin_amdgcn_s_waitcnt(0x0F70);                     // vmcnt(0)
+    __syncthreads();
+    stage_all(1, 1);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+#pragma unroll
+        for (int f = 0; f < RF; ++f) widen_chunk(read_a(0, f, j), W[f][2 * j], W[f][2 * j + 1]);
+        widen_chunk(read_b(0, 0, j), B[2 * j], B[2 * j + 1]);
+    }
+    f32x16 sum[RF];
+    float sc = 0.0f, sp = 0.0f;                             // the scales that the sums of this and the last group take
+    u32x4 nb[2], na[2];                                     // chunks on their way: columns, rows
+
+    auto mfma = [](const bf16x8 &x, const bf16x8 &y, const f32x16 &z) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, z, 0, 0, 0);
+    };
+    auto scale = [&](float (&to)[16], const f32x16 &from, float by, int i0, int i1) {
+#pragma unroll
+        for (int i = i0; i < i1; ++i) {
+            to[i] = __builtin_fmaf(from[i], by, to[i]);
+            pin(to[i]);
+        }
+    };
+    auto widen_to = [](u32x4 c, bf16x8 &lo, bf16x8 &hi) {
+        widen_chunk(c, lo, hi);
+        pin(lo);
+        pin(hi);
+    };
+    const f32x16 zero = {};
+    // the sums to add after a pass's product k: from the third on, when the pass before has its last ones
+    auto from_k = [](int k) { return k < 2 ? 0 : k == 8 ? 16 : 3 * k - 6; };
+
+    // Pass (g, 0) multiplies rows 0 .. 31 and adds the sums of the pass before;
+    // pass (g, 1) rows 32 .. 63, and widens the next group's columns.
+    auto block = [&](int u, auto BUF, auto FIRST) {
+        constexpr int h = decltype(BUF)::value;
+        constexpr bool first = decltype(FIRST)::value;
+        const float swn = swp[min(u + 1, KB - 1)];
+        auto group = [&](auto G) {
+            constexpr int g = decltype(G)::value;
+            constexpr bool last = g == CF - 1;
+            sp = sc;
+            sc = sw * lsn[h * BC + 32 * g];
+            if constexpr (last) {
+                // the next block's codes are in LDS, and all of this one's are read
+                __builtin_amdgcn_s_waitcnt(0x0F70);
+                __syncthreads();
+            }
+            constexpr int hb = last ? h ^ 1 : h, gb = last ? 0 : g + 1;
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                sum[0] = mfma(W[0][k], B[k], k ? sum[0] : zero);
+                pin(sum[0]);
+                if constexpr (g > 0) scale(acc[1][g - 1], sum[1], sp, from_k(k), from_k(k + 1));
+                if constexpr (g == 0 && !first) scale(acc[1][CF - 1], sum[1], sp, from_k(k), from_k(k + 1));
+                if (k == 4) nb[0] = read_b(hb, gb, 0);
+                if (k == 6) nb[1] = read_b(hb, gb, 1);
+                if constexpr (last) {
+                    // (given out together, the loads would hold up the products behind them)
+                    if (!(k & 1)) stage(u + 2, h, k >> 1);
+                    if (k == 5) na[0] = read_a(h ^ 1, 0, 0);
+                    if (k == 7) na[1] = read_a(h ^ 1, 0, 1);
+                }
+                if constexpr (g == 0 && !first) {
+                    if (k & 1) {
+                        const int j = k >> 1;
+                        widen_to(na[j & 1], W[1][2 * j], W[1][2 * j + 1]);
+                        if (j + 2 < 4) na[j & 1] = read_a(h, 1, j + 2);
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                sum[1] = mfma(W[1][k], B[k], k ? sum[1] : zero);
+                pin(sum[1]);
+                scale(acc[0][g], sum[0], sc, from_k(k), from_k(k + 1));
+                if (k & 1) {
+                    const int j = k >> 1;
+                    widen_to(nb[j & 1], B[2 * j], B[2 * j + 1]);
+                    if (j + 2 < 4) nb[j & 1] = read_b(hb, gb, j + 2);
+                    if constexpr (last) {
+                        widen_to(na[j & 1], W[0][2 * j], W[0][2 * j + 1]);
+                        na[j & 1] = j + 2 < 4 ? read_a(h ^ 1, 0, j + 2) : read_a(h ^ 1, 1, j - 2);
+                    }
+                }
+                if constexpr (last) {
+                    if (!(k & 1)) stage(u + 2, h, 4 + (k >> 1));
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        };
+        parts(std::make_integer_sequence<int, CF>{}, group);
+        sw = swn;
+    };
+    using I0 = std::integral_constant<int, 0>;
+    using I1 = std::integral_constant<int, 1>;
+    block(0, I0{}, std::true_type{});
+    int u = 1;
+    for (; u + 1 < KB; u += 2) {
+        block(u, I1{}, std::false_type{});
+        block(u + 1, I0{}, std::false_type{});
+    }
+    if (u < KB) block(u, I1{}, std::false_type{});
+    scale(acc[1][CF - 1], sum[1], sc, 0, 16);
+    __builtin_amdgcn_s_waitcnt(0x0F70);                     // (nothing on its way into LDS when the workgroup ends)
+
+    const bool vec4 = (a.N & 3) == 0 && ((uintptr_t)a.y & 15) == 0;
+#pragma unroll
+    for (int g = 0; g < CF; ++g) {
+        const int v = vec0 + 32 * (wc * CF + g) + n;
+        if (v < a.M) {
+            float *const yr = a.y + (size_t)v * a.N;
+#pragma unroll
+            for (int f = 0; f < RF; ++f)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int n0 = row0 + 64 * wr + 32 * f + 8 * i + 4 * hk;
+                    const float(&r)[16] = acc[f][g];
+                    if (n0 < a.N) {
+                        if (vec4) {
+                            *(float4 *)(yr + n0) = make_float4(r[4 * i], r[4 * i + 1], r[4 * i + 2], r[4 * i + 3]);
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                if (n0 + k < a.N) yr[n0 + k] = r[4 * i + k];
+                        }
+                    }
+                }
+        }
+    }
+}
+
+// The tiles lie in groups of bt_vmax vector chunks, chunk-fastest inside, and
+// are dealt to the XCDs in contiguous parts: the tiles an XCD runs at a time
+// share both operands.
+__global__ __launch_bounds__(512, 2) void qmv_f8_wide_kernel(const Args a)
+{
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    constexpr int BC = kF8WideVecs;
+    const int tile = (blockIdx.x & 7) * a.bt_per_xcd + (blockIdx.x >> 3);
+    if (tile >= a.bt_tiles) return;
+    const int chunks = (a.M + BC - 1) / BC, group = a.bt_vmax * a.bt_row_tiles;
+    const int gi = tile / group, in = tile - gi * group, gw = min(a.bt_vmax, chunks - gi * a.bt_vmax);
+    f8_wide_tile(a, lds, in / gw * kF8WideRows, (gi * a.bt_vmax + in % gw) * BC);
+}
+
+extern const void *const kTableF8Wide[1];
+const void *const kTableF8Wide[1] = {
+    (const void *)&qmv_f8_wide_kernel,
+};
 
 // [plain, gate/up, combine]
 extern const void *const kTableF8Few[3];

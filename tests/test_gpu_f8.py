@@ -76,7 +76,8 @@ def untouched(buf, fill=7.0):
 DENSE = [(1, 1, 32), (1, 16, 128), (2, 17, 160), (3, 130, 2880), (4, 300, 16384), (1, 2048, 7168), (5, 128, 128),
          (16, 257, 288), (17, 96, 512), (33, 129, 416), (64, 256, 1024), (65, 384, 160), (130, 200, 7168),
          (64, 4096, 288), (100, 3200, 160), (200, 3210, 416), (20, 8200, 96), (16, 300, 16384), (40, 7000, 2880),
-         (300, 700, 544), (1000, 515, 384)]
+         (300, 700, 544), (1000, 515, 384),
+         (2000, 3101, 160), (1300, 5000, 1056), (200, 17000, 288), (8192, 900, 96)]
 
 
 @pytest.mark.parametrize("M,N,K", DENSE)
@@ -168,7 +169,8 @@ def small_exact(rng, shape):
 
 
 @pytest.mark.parametrize("M,N,K", [(1, 64, 16384), (4, 100, 288), (16, 80, 1024), (64, 4096, 288), (200, 700, 160),
-                                   (130, 3300, 416), (600, 1300, 2080), (2100, 260, 544)])
+                                   (130, 3300, 416), (600, 1300, 2080), (2100, 260, 544),
+                                   (1900, 3400, 544), (700, 9000, 416)])
 def test_dense_exact(M, N, K):
     rng = np.random.default_rng(N)
     wc, wv = small_exact(rng, (N, K))
@@ -196,7 +198,7 @@ def test_gather_and_combine_exact(M, E, top_k, N, K):
     assert np.array_equal(host(c), (rw.astype(np.float64)[:, :, None] * want).sum(1))
 
 
-@pytest.mark.parametrize("M,N,K", [(3, 300, 288), (64, 4096, 288), (600, 1300, 160)])
+@pytest.mark.parametrize("M,N,K", [(3, 300, 288), (64, 4096, 288), (600, 1300, 160), (2000, 3101, 160)])
 def test_nan_reaches_its_own_outputs_only(M, N, K):
     rng = np.random.default_rng(N)
     (wc, ws), (xc, xs) = weights(rng, (), N, K), vectors(rng, (M,), K)
@@ -237,10 +239,10 @@ def test_repeats_replays_and_streams():
         sets.append([dev(a) for a in (wc, ws, uc, us, rng.integers(-1, E, (M, top_k)).astype(np.int32),
                                       rng.standard_normal((M, top_k)).astype(np.float32), xc, xs)])
     dw = [dev(a) for a in weights(rng, (), 4100, 288)]
-    dx = [dev(a) for a in vectors(rng, (300,), 288)]
+    dx = [dev(a) for a in vectors(rng, (1800,), 288)]
 
     def calls(stream=None):
-        out = [q.qmv_dense("f8", *dw, dx[0][:m], dx[1][:m], stream=stream) for m in (1, 40, 300)]
+        out = [q.qmv_dense("f8", *dw, dx[0][:m], dx[1][:m], stream=stream) for m in (1, 40, 300, 1800)]
         for wc, ws, uc, us, ids, rw, xc, xs in sets:
             out.append(q.qmv_gather_moe("f8", wc, ws, ids, xc, xs, stream=stream))
             out.append(q.qmv_gather_moe_swiglu("f8", wc, ws, uc, us, ids, xc, xs, stream=stream))
