@@ -243,9 +243,9 @@ const void *qk_kernel(int D, int &G)
 }
 
 // ------------------------------------------------------- log probabilities
-// One pass over the row: a thread keeps the largest of its logits, m, and the
-// sums of exp(l - m) and exp(l - m) (l - m), which move with it; a wave keeps
-// the top entries it has seen.
+// One pass over the row.  A wave keeps its largest logit so far, m, and each
+// lane the sums of exp(l - m) and exp(l - m) (l - m), which move with it; and
+// the wave keeps the top entries it has seen.
 //
 // An entry is 64 bits, the logit's ordered bits over the inverted index, so
 // that entries are all different and the larger one comes first; 0 is none.
@@ -258,83 +258,137 @@ __device__ __forceinline__ float order_value(uint32_t k)
 {
     return __uint_as_float((k & 0x80000000u) ? k & 0x7FFFFFFFu : ~k);
 }
+// The value below l (there is none of -0's bits).
+__device__ __forceinline__ float below(uint32_t k) { return order_value(k - (k == 0x80000000u ? 2u : 1u)); }
 __device__ __forceinline__ uint64_t entry(float l, int index)
 {
     return (uint64_t)order_bits(l) << 32 | (uint32_t)~index;
 }
 
+// The value of lane ^ J, by the vector ALUs (a sort of 64 by way of LDS took
+// three times as long).
+template <int J> __device__ __forceinline__ uint32_t lane_xor(uint32_t v)
+{
+    if constexpr (J == 1) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true);     // quad_perm
+    if constexpr (J == 2) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true);
+    if constexpr (J == 4)                                     // a half row mirrored (^ 7), a quad mirrored (^ 3)
+        return (uint32_t)__builtin_amdgcn_mov_dpp(__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true), 0x1B, 0xF, 0xF, true);
+    if constexpr (J == 8) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x128, 0xF, 0xF, true);    // row_ror
+    if constexpr (J == 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        return threadIdx.x & 16 ? r[0] : r[1];
+    }
+    if constexpr (J == 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return threadIdx.x & 32 ? r[0] : r[1];
+    }
+}
+template <int J> __device__ __forceinline__ uint64_t lane_xor(uint64_t v)
+{
+    return (uint64_t)lane_xor<J>((uint32_t)(v >> 32)) << 32 | lane_xor<J>((uint32_t)v);
+}
+template <int J> __device__ __forceinline__ double lane_xor(double v)
+{
+    return __builtin_bit_cast(double, lane_xor<J>(__builtin_bit_cast(uint64_t, v)));
+}
+
 template <class T> __device__ __forceinline__ T larger(T a, T b) { return a > b ? a : b; }
 template <class T> __device__ __forceinline__ T smaller(T a, T b) { return a > b ? b : a; }
+
+// Steps of a bitonic sort: lanes L and L ^ J in order, for J, J / 2, .. 1; runs of
+// K lanes alternate in direction.
+template <int K, int J, bool FALLING, class T>
+__device__ __forceinline__ T sort_steps(T v)
+{
+    const T o = lane_xor<J>(v);
+    const bool first = ((threadIdx.x & J) == 0) == (K == 64 || (threadIdx.x & K) == 0);
+    v = first == FALLING ? larger(v, o) : smaller(v, o);
+    if constexpr (J > 1)
+        return sort_steps<K, J / 2, FALLING>(v);
+    else
+        return v;
+}
 
 // The wave's 64 values in order over its lanes: falling, or rising.
 template <bool FALLING, class T>
 __device__ __forceinline__ T wave_sort(T v)
 {
-    const int lane = threadIdx.x & 63;
-#pragma unroll
-    for (int k = 2; k <= 64; k <<= 1)
-#pragma unroll
-        for (int j = k >> 1; j >= 1; j >>= 1) {
-            const T o = __shfl_xor(v, j);
-            const bool first = ((lane & j) == 0) == ((lane & k) == 0 || k == 64);
-            v = first == FALLING ? larger(v, o) : smaller(v, o);
-        }
-    return v;
+    v = sort_steps<2, 1, FALLING>(v);
+    v = sort_steps<4, 2, FALLING>(v);
+    v = sort_steps<8, 4, FALLING>(v);
+    v = sort_steps<16, 8, FALLING>(v);
+    v = sort_steps<32, 16, FALLING>(v);
+    return sort_steps<64, 32, FALLING>(v);
 }
 
 // The larger 64 of two sorted lists (a falling, b rising), falling.
 template <class T>
 __device__ __forceinline__ T wave_merge(T a, T b)
 {
-    const int lane = threadIdx.x & 63;
-    T v = larger(a, b);
-#pragma unroll
-    for (int j = 32; j >= 1; j >>= 1) {
-        const T o = __shfl_xor(v, j);
-        v = (lane & j) == 0 ? larger(v, o) : smaller(v, o);
-    }
-    return v;
+    return sort_steps<64, 32, true>(larger(a, b));
 }
 
-// A wave's top entries, falling over the lanes, and entries waiting (in LDS,
-// less than 64 between calls) to be merged with them 64 at a time.
+template <class T, class F>
+__device__ __forceinline__ T wave_reduce(T v, F f)
+{
+    v = f(v, lane_xor<1>(v));
+    v = f(v, lane_xor<2>(v));
+    v = f(v, lane_xor<4>(v));
+    v = f(v, lane_xor<8>(v));
+    v = f(v, lane_xor<16>(v));
+    return f(v, lane_xor<32>(v));
+}
+
+template <class T> __device__ __forceinline__ T lane_value(T v, int lane);
+template <> __device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane)
+{
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
+template <> __device__ __forceinline__ uint64_t lane_value(uint64_t v, int lane)
+{
+    return (uint64_t)lane_value((uint32_t)(v >> 32), lane) << 32 | lane_value((uint32_t)v, lane);
+}
+
+// How many of the lanes below this one have their bit in m.
+__device__ __forceinline__ int lanes_below(unsigned long long m)
+{
+    return (int)__builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+}
+
+// A wave's top entries, falling over the lanes, and entries waiting (in LDS)
+// to be merged with them 64 at a time.
 struct TopList {
     uint64_t kept;
-    volatile uint64_t *wait;     // [128]
+    volatile uint64_t *wait;
     int waiting;
 
     __device__ __forceinline__ TopList(uint64_t *lds) : kept(0), wait(lds), waiting(0) {}
 
-    __device__ __forceinline__ void merge()
-    {
-        const int lane = threadIdx.x & 63;
-        asm volatile("" ::: "memory");
-        const uint64_t v = lane < waiting ? wait[lane] : 0;
-        kept = wave_merge(kept, wave_sort<false>(v));
-        waiting -= 64;
-        if (waiting > 0) {
-            const uint64_t rest = wait[64 + lane];
-            if (lane < waiting) wait[lane] = rest;
-        } else {
-            waiting = 0;
-        }
-        asm volatile("" ::: "memory");
-    }
-    // (all lanes call it)
+    // (all lanes call these)
     __device__ __forceinline__ void add(bool have, uint64_t e)
     {
         const unsigned long long m = __ballot(have);
         if (m == 0) return;
-        const int before = __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
-        if (have) wait[waiting + before] = e;
+        if (have) wait[waiting + lanes_below(m)] = e;
         waiting += (int)__popcll(m);
-        if (waiting >= 64) merge();
     }
-    __device__ __forceinline__ void finish()
+    // Merges until less than `left` wait (64 at least but for the last).
+    __device__ __forceinline__ void merge(int left)
     {
-        if (waiting > 0) merge();
+        const int lane = threadIdx.x & 63;
+        while (waiting >= left && waiting > 0) {
+            asm volatile("" ::: "memory");
+            const int from = waiting > 64 ? waiting - 64 : 0;
+            const uint64_t v = from + lane < waiting ? wait[from + lane] : 0;
+            kept = wave_merge(kept, wave_sort<false>(v));
+            waiting = from;
+            asm volatile("" ::: "memory");
+        }
     }
 };
+
+// exp(z), z <= 0 (1 for 0).
+__device__ __forceinline__ float exp_below(float z) { return __builtin_amdgcn_exp2f(z * 1.4426950408889634f); }
 
 // The largest logit and the sums relative to it.
 struct Sums {
@@ -344,27 +398,23 @@ struct Sums {
     // relative to a larger (or equal) maximum
     __device__ __forceinline__ void move(float to)
     {
-        const float d = m > -__builtin_inff() ? m - to : 0.0f;        // (nothing so far: sums are 0)
-        const double c = m > -__builtin_inff() ? (double)exp2f(d * 1.4426950408889634f) : 0.0;
+        // (nothing so far: sums are 0; below -200 nothing of them is left, and
+        // the difference may be infinite)
+        const float d = m > -__builtin_inff() ? fmaxf(m - to, -200.0f) : 0.0f;
+        const double c = m > -__builtin_inff() ? (double)exp_below(d) : 0.0;
         u = c * (u + s * (double)d);
         s *= c;
         m = to;
     }
-};
-
-__device__ __forceinline__ Sums wave_sums(Sums a)
-{
-    float m = a.m;
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
-    a.move(m);
-#pragma unroll
-    for (int d = 32; d >= 1; d >>= 1) {
-        a.s += __shfl_xor(a.s, d);
-        a.u += __shfl_xor(a.u, d);
+    __device__ __forceinline__ void join(Sums o)
+    {
+        const float to = fmaxf(m, o.m);
+        move(to);
+        o.move(to);
+        s += o.s;
+        u += o.u;
     }
-    return a;
-}
+};
 
 struct LogArgs {
     const void *logits;
@@ -376,41 +426,6 @@ struct LogArgs {
     long long first;     // workgroup 0's place in the call
 };
 
-constexpr int kLogWaves = 4;
-
-struct LogShared {
-    uint64_t wait[kLogWaves][128];
-    uint64_t lists[kLogWaves][64];
-    Sums sums[kLogWaves];
-};
-
-// The waves' sums and lists -> the workgroup's, in wave 0.
-template <bool TOP>
-__device__ __forceinline__ void join_waves(LogShared &sh, Sums &a, uint64_t &kept)
-{
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    if (lane == 0) sh.sums[w] = a;
-    if constexpr (TOP) sh.lists[w][lane] = kept;
-    __syncthreads();
-    if (w != 0) return;
-    a = sh.sums[0];
-    float m = a.m;
-#pragma unroll
-    for (int i = 1; i < kLogWaves; ++i) m = fmaxf(m, sh.sums[i].m);
-    a.move(m);
-#pragma unroll
-    for (int i = 1; i < kLogWaves; ++i) {
-        Sums o = sh.sums[i];
-        o.move(m);
-        a.s += o.s;
-        a.u += o.u;
-    }
-    if constexpr (TOP) {
-#pragma unroll
-        for (int i = 1; i < kLogWaves; ++i) kept = wave_merge(kept, sh.lists[i][63 - lane]);
-    }
-}
-
 __device__ __forceinline__ float logit_at(const void *base, size_t i, int type)
 {
     if (type == QMX_T_F32) return ((const float *)base)[i];
@@ -418,191 +433,452 @@ __device__ __forceinline__ float logit_at(const void *base, size_t i, int type)
     return type == QMX_T_BF16 ? __uint_as_float(h << 16) : (float)__builtin_bit_cast(_Float16, (uint16_t)h);
 }
 
-// Row `row`'s outputs from its sums and list (wave 0).
-__device__ __forceinline__ void put_row(const LogArgs &a, int row, const Sums &s, uint64_t kept)
+// The row's token and its logit, both on their way long before they are needed.
+struct Given {
+    bool inside;
+    float l;
+
+    __device__ __forceinline__ Given(const LogArgs &a, int row) : inside(false), l(0.0f)
+    {
+        if (a.logprobs) {
+            const int t = a.tokens[row];
+            inside = (unsigned)t < (unsigned)a.V;
+            l = logit_at(a.logits, (size_t)row * a.V + (inside ? t : 0), a.lt);
+        }
+    }
+};
+
+// Row `row`'s outputs from its sums and list (one wave).
+__device__ __forceinline__ void put_row(const LogArgs &a, int row, const Given &g, const Sums &s, uint64_t kept)
 {
     const int lane = threadIdx.x & 63;
-    const double inf = __builtin_inf();
     const bool none = !(s.m > -__builtin_inff());
     const double logs = none ? 0.0 : s.m == __builtin_inff() ? __builtin_nan("") : log(s.s);
     auto logprob = [&](float l) { return l > -__builtin_inff() ? (float)((double)l - (double)s.m - logs) : -__builtin_inff(); };
     if (lane < a.top_k) {
         const uint32_t k = (uint32_t)(kept >> 32);
         a.top_ids[(size_t)row * a.top_k + lane] = kept ? (int)~(uint32_t)kept : -1;
-        a.top_logprobs[(size_t)row * a.top_k + lane] = kept ? logprob(order_value(k)) : (float)-inf;
+        a.top_logprobs[(size_t)row * a.top_k + lane] = kept ? logprob(order_value(k)) : -__builtin_inff();
     }
     if (lane == 0) {
         if (a.entropy) a.entropy[row] = none ? 0.0f : (float)(logs - s.u / s.s);
-        if (a.logprobs) {
-            const int t = a.tokens[row];
-            a.logprobs[row] = (unsigned)t < (unsigned)a.V ? logprob(logit_at(a.logits, (size_t)row * a.V + t, a.lt)) : 0.0f;
-        }
+        if (a.logprobs) a.logprobs[row] = g.inside ? logprob(g.l) : 0.0f;
     }
 }
 
+// A row's logits of a type: `groups` of 8 from its first whole 16 bytes on, and up
+// to 7 before and 7 behind them, the rest.
+template <int TYPE>
+struct LogRow {
+    static constexpr int SIZE = TYPE == QMX_T_F32 ? 4 : 2;
+    const uint8_t *base;
+    int head, groups, V;
+
+    __device__ __forceinline__ LogRow(const LogArgs &a, int row) : V(a.V)
+    {
+        base = (const uint8_t *)a.logits + (size_t)row * a.V * SIZE;
+        head = min((int)((16 - ((uintptr_t)base & 15)) & 15) / SIZE, V);
+        groups = (V - head) / 8;
+    }
+    // index of group g's first logit
+    __device__ __forceinline__ int at(int g) const { return head + 8 * g; }
+    // group g's logits; masked ones behind the last
+    __device__ __forceinline__ Raw8 load(int g) const
+    {
+        constexpr uint32_t masked = TYPE == QMX_T_F32 ? 0xFF800000u : TYPE == QMX_T_BF16 ? 0xFF80FF80u : 0xFC00FC00u;
+        Raw8 r;
+        r.a = r.b = make_uint4(masked, masked, masked, masked);
+        if (g < groups) {
+            const uint4 *const p = (const uint4 *)(base + (long long)at(g) * SIZE);
+            r.a = p[0];
+            if constexpr (SIZE == 4) r.b = p[1];
+        }
+        return r;
+    }
+    // lane i < 14 of a wave: the i-th of the rest, and its index
+    __device__ __forceinline__ float rest(int i, int &index) const
+    {
+        index = i < head ? i : at(groups) + i - head;
+        return i < 14 && index < V ? logit_at(base, index, TYPE) : -__builtin_inff();
+    }
+};
+
+__device__ __forceinline__ double add(double x, double y) { return x + y; }
+
+// What a workgroup leaves of a part for the join: its sums (wave 0, any lane) and 64 entries.
 template <bool TOP>
-__global__ __launch_bounds__(64 * kLogWaves) void qmt_logprobs_kernel(const LogArgs a)
+__device__ __forceinline__ void put_part(const LogArgs &a, long long place, const Sums &s, uint64_t e)
 {
-    __shared__ LogShared sh;
-    constexpr int UN = 4;
+    const int lane = threadIdx.x & 63;
+    if (lane == 0) {
+        double *const out = (double *)(a.work + place * kListSums);
+        out[0] = s.s;
+        out[1] = s.u;
+        *(float *)(out + 2) = s.m;
+    }
+    if constexpr (TOP) ((uint64_t *)(a.work + (long long)a.M * a.parts * kListSums))[place * 64 + lane] = e;
+}
+
+// A short part of a row, a group of 8 for each lane of 4 waves: first the
+// largest logit of the workgroup and a bound of its top entries -- of the waves'
+// 16 largest lanes the top_k-th: as many logits are at least that -- then the
+// sums and what is no smaller than the bound, hardly more than top_k entries.
+template <int TYPE, bool TOP>
+__global__ __launch_bounds__(256) void qmt_logprobs_part_kernel(const LogArgs a)
+{
+    constexpr int NW = 4;
+    __shared__ uint64_t few[64], wait[NW][128];
+    __shared__ uint32_t lanes[64];
+    __shared__ double part_s[NW], part_u[NW];
+    __shared__ int count;
     const float low = -__builtin_inff();
     const long long place = a.first + blockIdx.x;
     const int row = (int)(place / a.parts), part = (int)(place - (long long)row * a.parts);
-    const int size = a.lt == QMX_T_F32 ? 4 : 2;
-    const uint8_t *const base = (const uint8_t *)a.logits + (size_t)row * a.V * size;
-    // groups of 8 start at whole 16 bytes, the first one up to 7 logits before the row
-    const int head = (int)((uintptr_t)base & 15) / size;
-    const int tid = threadIdx.x, w = tid >> 6;
-    const int s0 = part * a.steps, s1 = s0 + a.steps;
-    auto load = [&](int i, Raw8 &r) {
-        r.b = make_uint4(0, 0, 0, 0);
-        if (i >= 0 && i + 8 <= a.V) {
-            const uint4 *const p = (const uint4 *)(base + (long long)i * size);
-            r.a = p[0];
-            if (size == 4) r.b = p[1];
-        } else {
-            // a group over the row's border: its logits one at a time, the others masked
-            uint32_t v[8];
+    const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
+    const LogRow<TYPE> r(a, row);
+    const int g = part * (64 * NW) + tid;
+    const Raw8 raw = r.load(g);
+    // (the rest: with the last wave of the first part)
+    int rest_at = 0;
+    const float rest = part == 0 && w == NW - 1 ? r.rest(lane, rest_at) : low;
+    if (tid == 0) count = 0;
+    float l[8], big = rest > low ? rest : low;
+    raw_to_f32(raw, TYPE, l);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) big = l[j] > big ? l[j] : big;                 // (NaN is no maximum)
+    const uint32_t mine = big > low ? order_bits(big) : 0u;
+    if constexpr (TOP) {
+        const uint32_t order = wave_sort<true>(mine);
+        if (lane < 16) lanes[16 * w + lane] = order;
+    } else {
+        const uint32_t m = wave_reduce(mine, larger<uint32_t>);
+        if (lane < 16) lanes[16 * w + lane] = m;
+    }
+    __syncthreads();
+    const uint32_t sorted = TOP ? wave_sort<true>(lanes[lane]) : wave_reduce(lanes[lane], larger<uint32_t>);
+    const uint32_t top = lane_value(sorted, 0);
+    const float m = top ? order_value(top) : low;
+    double s = 0.0;
+    float u = 0.0f;
+    auto term = [&](float v) {
+        // (below -200 the exponential is 0 in fp32; NaN, both -infinity among it, gives -200 too)
+        const float z = __builtin_amdgcn_fmed3f(v - m, -200.0f, 0.0f), e = exp_below(z);
+        s += (double)e;                                       // (a largest logit's 1 would take the digits of an fp32 sum)
+        u = __builtin_fmaf(e, z, u);
+    };
+    term(rest);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) term(l[j]);
+    s = wave_reduce(s, add);
+    const double su = wave_reduce((double)u, add);
+    if (lane == 0) part_s[w] = s, part_u[w] = su;
+    uint64_t mine64 = 0;
+    float tau = low;
+    if constexpr (TOP) {
+        const uint32_t bound = lane_value(sorted, a.top_k - 1);
+        tau = bound ? order_value(bound) : -__FLT_MAX__;
+        auto put = [&](float v, int index) {
+            const bool have = v >= tau;
+            const unsigned long long b = __ballot(have);
+            if (b != 0) {
+                int at = 0;
+                if (lane == 0) at = atomicAdd(&count, (int)__popcll(b));
+                at = __builtin_amdgcn_readfirstlane(at) + lanes_below(b);
+                if (have && at < 64) few[at] = entry(v, index);
+            }
+        };
+        put(rest, rest_at);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) put(l[j], r.at(g) + j);
+    }
+    __syncthreads();
+    if constexpr (TOP) {
+        const int n = count;
+        if (n > 64) {
+            // (many logits that are all alike)
+            TopList list(wait[w]);
+            list.add(rest >= tau, entry(rest, rest_at));
+#pragma unroll 1
+            for (int j = 0; j < 8; ++j) {
+                float v = l[0];
+#pragma unroll
+                for (int q = 1; q < 8; ++q) v = q == j ? l[q] : v;
+                list.add(v >= tau, entry(v, r.at(g) + j));
+                list.merge(64);
+            }
+            list.merge(1);
+            wait[w][lane] = list.kept;
+            __syncthreads();
+            if (w == 0) {
+                mine64 = list.kept;
+                for (int i = 1; i < NW; ++i) mine64 = wave_merge(mine64, wait[i][63 - lane]);
+            }
+        } else if (w == 0) {
+            mine64 = lane < n ? few[lane] : 0;
+        }
+    }
+    if (w == 0) {
+        Sums all = {m, 0.0, 0.0};
+        for (int i = 0; i < NW; ++i) all.s += part_s[i], all.u += part_u[i];
+        put_part<TOP>(a, place, all, mine64);
+    }
+}
+
+// A row, or a long part of one: 8 waves, `steps` groups of 8 logits a lane of
+// them, two always on their way; the rest of the row is one more step, the last,
+// of the first part's first wave.  2 steps at least.
+template <int TYPE, bool TOP>
+__global__ __launch_bounds__(512) void qmt_logprobs_kernel(const LogArgs a)
+{
+    constexpr int NW = 8;
+    __shared__ uint64_t wait[NW][64 + 4 * 64];
+    __shared__ uint32_t first_top[NW * 8];
+    __shared__ Sums part_sums[NW];
+    const float low = -__builtin_inff();
+    const long long place = a.first + blockIdx.x;
+    const int row = (int)(place / a.parts), part = (int)(place - (long long)row * a.parts);
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const LogRow<TYPE> r(a, row);
+    const Given given(a, row);
+    auto uniform = [](float v) { return __uint_as_float((uint32_t)__builtin_amdgcn_readfirstlane(__float_as_uint(v))); };
+    Sums sums = {low, 0.0, 0.0};                               // m is the wave's
+    TopList top(wait[w]);
+    float tau = low;                                           // only logits above it can be among the top
+    auto largest = [&](const float (&l)[8]) {                  // (NaN is no maximum)
+        float big = low;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) big = l[j] > big ? l[j] : big;
+        return big > low ? order_bits(big) : 0u;
+    };
+    auto step = [&](const float (&l)[8], int index) {
+        float z[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) z[j] = l[j] - sums.m;
+        const float top_z = fmaxf(fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])), fmaxf(fmaxf(z[4], z[5]), fmaxf(z[6], z[7])));
+        if (__any(top_z >= 0.0f)) {
+            // a logit as large as the largest so far: its 1 would take the digits
+            // of the others in an fp32 sum, so it is added here and the others
+            // as ever
+            const uint32_t k = wave_reduce(largest(l), larger<uint32_t>);
+            sums.move(uniform(larger(sums.m, order_value(k))));
+            int ones = 0;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const bool in = i + j >= 0 && i + j < a.V;
-                const uint32_t masked = a.lt == QMX_T_F32 ? 0xFF800000u : a.lt == QMX_T_BF16 ? 0xFF80u : 0xFC00u;
-                v[j] = !in ? masked : size == 4 ? ((const uint32_t *)base)[i + j] : ((const uint16_t *)base)[i + j];
+                z[j] = l[j] - sums.m;
+                ones += z[j] == 0.0f;
+                z[j] = z[j] == 0.0f ? low : z[j];
             }
-            if (size == 4) {
-                r.a = make_uint4(v[0], v[1], v[2], v[3]);
-                r.b = make_uint4(v[4], v[5], v[6], v[7]);
-            } else {
-                r.a = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+            sums.s += (double)ones;
+        }
+        float e[8], u = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            // (below -200 the exponential is 0 in fp32; NaN gives -200 too)
+            z[j] = __builtin_amdgcn_fmed3f(z[j], -200.0f, 0.0f);
+            e[j] = exp_below(z[j]);
+            u = __builtin_fmaf(e[j], z[j], u);
+        }
+        sums.s += (double)(((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7])));
+        sums.u += (double)u;
+        if constexpr (TOP) {
+            // (rounded differences keep the order, equal ones may stand for
+            // unequal logits; from +infinity there are none)
+            const float zz = top_z < 0.0f ? top_z : 0.0f;
+            if (sums.m == -low || __any(zz > low && zz >= tau - sums.m)) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) top.add(l[j] > tau, entry(l[j], index + j));
+                if (top.waiting >= 64) top.merge(64);
+#pragma unroll
+                for (int j = 4; j < 8; ++j) top.add(l[j] > tau, entry(l[j], index + j));
+                if (top.waiting >= 32) {
+                    top.merge(32);
+                    // (not within a step: the same logit at a lower index may come after)
+                    const uint32_t k = (uint32_t)(lane_value(top.kept, a.top_k - 1) >> 32);
+                    if (k) tau = uniform(fmaxf(tau, order_value(k)));
+                }
             }
         }
     };
-    Sums sums = {low, 0.0, 0.0};
-    TopList top(sh.wait[w]);
-    float tau = low;                                           // only logits above it can be among the top
-    bool first = true;
-    for (int s = s0; s < s1; s += UN) {
-        Raw8 raw[UN];
-#pragma unroll
-        for (int n = 0; n < UN; ++n) load(s + n < s1 ? (s + n) * kStep - head + 8 * tid : a.V, raw[n]);
-#pragma unroll
-        for (int n = 0; n < UN; ++n) {
-            float l[8];
-            raw_to_f32(raw[n], a.lt, l);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) l[j] = l[j] > low ? l[j] : low;      // NaN too
-            const float big = fmaxf(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])), fmaxf(fmaxf(l[4], l[5]), fmaxf(l[6], l[7])));
-            if (big > sums.m) sums.move(big);
-            double e[8];
-            float u = 0.0f;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                // (below -200 the exponential is 0 in fp32; both -infinity: NaN, which gives -200)
-                const float z = fmaxf(l[j] - sums.m, -200.0f);
-                const float x = exp2f(z * 1.4426950408889634f);
-                u = __builtin_fmaf(x, z, u);
-                e[j] = (double)x;
-            }
-            sums.s += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-            sums.u += (double)u;
-            if constexpr (TOP) {
-                if (first) {
-                    // the top_k-th largest of the lanes' largest: as many logits are at least that
-                    first = false;
-                    const uint32_t k = __shfl(wave_sort<true>(big > low ? order_bits(big) : 0u), a.top_k - 1);
-                    // the value below it (there is none of -0's bits)
-                    tau = k == 0u ? low : order_value(k - (k == 0x80000000u ? 2u : 1u));
-                }
-                if (__any(big > tau)) {
-                    const int i = (s + n) * kStep - head + 8 * tid;
-#pragma unroll 1
-                    for (int j = 0; j < 8; ++j) {
-                        float v = l[0];
-#pragma unroll
-                        for (int q = 1; q < 8; ++q) v = q == j ? l[q] : v;
-                        top.add(v > tau, entry(v, i + j));
-                    }
-                    // (not within a step: the same logit at a lower index may come after)
-                    const uint32_t k = (uint32_t)(__shfl(top.kept, a.top_k - 1) >> 32);
-                    if (k) tau = fmaxf(tau, order_value(k));
-                }
-            }
-        }
+    const int s0 = part * a.steps, s1 = s0 + a.steps;
+    auto load = [&](int s) { return r.load(s < s1 ? s * (NW * 64) + tid : r.groups); };
+    auto at = [&](int s) { return r.at(s * (NW * 64) + tid); };
+    Raw8 raw0 = load(s0), raw1 = load(s0 + 1);
+    if constexpr (TOP) {
+        // the top_k-th largest of the waves' 8 largest lanes of the first step:
+        // as many logits of the row are at least that
+        float l[8];
+        raw_to_f32(raw0, TYPE, l);
+        const uint32_t order = wave_sort<true>(largest(l));
+        if (lane < 8) first_top[8 * w + lane] = order;
+        __syncthreads();
+        const uint32_t k = lane_value(wave_sort<true>(first_top[lane]), a.top_k - 1);
+        tau = k == 0u ? low : uniform(below(k));
     }
-    if constexpr (TOP) top.finish();
-    Sums all = wave_sums(sums);
-    uint64_t kept = top.kept;
-    join_waves<TOP>(sh, all, kept);
+    for (int s = s0; s < s1; s += 2) {
+        float l[8];
+        raw_to_f32(raw0, TYPE, l);
+        raw0 = load(s + 2);
+        step(l, at(s));
+        raw_to_f32(raw1, TYPE, l);
+        raw1 = load(s + 3);
+        if (s + 1 < s1) step(l, at(s + 1));
+    }
+    if (part == 0 && w == 0) {
+        int index = 0;
+        const float odd = r.rest(lane, index);
+        const float l[8] = {odd, low, low, low, low, low, low, low};
+        // (these may have the same logit at a lower index)
+        if (TOP && tau > low) tau = uniform(below(order_bits(tau)));
+        step(l, index);
+    }
+    sums.s = wave_reduce(sums.s, add);
+    sums.u = wave_reduce(sums.u, add);
+    if (lane == 0) part_sums[w] = sums;
+    uint64_t kept = 0;
+    if constexpr (TOP) {
+        top.merge(1);
+        kept = top.kept;
+        wait[w][lane] = kept;
+    }
+    __syncthreads();
     if (w != 0) return;
-    if (a.parts == 1) {
-        put_row(a, row, all, kept);
-        return;
-    }
-    uint8_t *const out = a.work + place * part_bytes(a.top_k);
-    if (tid == 0) {
-        *(double *)out = all.s;
-        *(double *)(out + 8) = all.u;
-        *(float *)(out + 16) = all.m;
-    }
-    if (TOP && tid < a.top_k) *(uint64_t *)(out + 32 + 8 * tid) = kept;
+    Sums all = part_sums[0];
+    for (int i = 1; i < NW; ++i) all.join(part_sums[i]);
+    if constexpr (TOP)
+        for (int i = 1; i < NW; ++i) kept = wave_merge(kept, wait[i][63 - lane]);
+    if (a.parts == 1)
+        put_row(a, row, given, all, kept);
+    else
+        put_part<TOP>(a, place, all, kept);
 }
 
-// The parts of a row joined: one workgroup a row.
+// The parts of a row joined: one workgroup a row, all entries in registers.  The
+// top_k-th largest of the parts' maxima (of fewer parts, of a wave's lanes, the
+// largest such) bounds the row's top_k-th logit from below, and what is no
+// smaller is hardly more than top_k entries, which one wave sorts.
 template <bool TOP>
-__global__ __launch_bounds__(64 * kLogWaves) void qmt_logprobs_join_kernel(const LogArgs a)
+__global__ __launch_bounds__(64 * kJoinWaves) void qmt_logprobs_join_kernel(const LogArgs a)
 {
-    __shared__ LogShared sh;
-    const float low = -__builtin_inff();
+    constexpr int NW = kJoinWaves, PER = kMaxParts / NW;       // lists a wave takes at most
+    __shared__ uint64_t few[64], wait[TOP ? NW : 1][128];
+    __shared__ uint32_t bound[NW];
+    __shared__ int count;
     const int row = (int)(a.first + blockIdx.x), tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
-    const long long bytes = part_bytes(a.top_k);
-    const uint8_t *const work = a.work + (long long)row * a.parts * bytes;
-    Sums sums = {low, 0.0, 0.0};
-    for (int p = tid; p < a.parts; p += 64 * kLogWaves) {
-        const uint8_t *const at = work + p * bytes;
-        Sums o = {*(const float *)(at + 16), *(const double *)at, *(const double *)(at + 8)};
-        const float m = fmaxf(sums.m, o.m);
-        sums.move(m);
-        o.move(m);
-        sums.s += o.s;
-        sums.u += o.u;
-    }
-    TopList top(sh.wait[w]);
+    const long long list0 = (long long)row * a.parts;
+    uint64_t e[PER];
     if constexpr (TOP) {
-        // at least top_k entries are no smaller than the top_k-th largest of 64 lanes' largest
-        uint64_t big = 0;
-        for (int p = lane; p < a.parts; p += 64) big = larger(big, *(const uint64_t *)(work + p * bytes + 32));
-        const uint64_t tau = __shfl(wave_sort<true>(big), a.top_k - 1);
-        const int n = a.parts * a.top_k;
-        for (int i0 = w * 64; i0 < n; i0 += 64 * kLogWaves) {
-            const int i = i0 + lane, p = i / a.top_k;
-            const uint64_t e = i < n ? *(const uint64_t *)(work + p * bytes + 32 + 8 * (i - p * a.top_k)) : 0;
-            top.add(e != 0 && e >= tau, e);
-        }
-        top.finish();
+        const uint64_t *const in = (const uint64_t *)(a.work + (long long)a.M * a.parts * kListSums) + list0 * 64;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) e[i] = w + NW * i < a.parts ? in[(w + NW * i) * 64 + lane] : 0;
     }
-    Sums all = wave_sums(sums);
-    uint64_t kept = top.kept;
-    join_waves<TOP>(sh, all, kept);
-    if (w == 0) put_row(a, row, all, kept);
+    // (only wave 0 needs these; they are loaded here, before anything is waited for)
+    Sums half[kMaxParts / 64];                                 // lane l's parts l, l + 64, ..
+#pragma unroll
+    for (int i = 0; i < kMaxParts / 64; ++i) {
+        const int p = min(lane + 64 * i, a.parts - 1);
+        const double *const at = (const double *)(a.work + (list0 + p) * kListSums);
+        half[i] = Sums{*(const float *)(at + 2), at[0], at[1]};
+    }
+    const Given given(a, row);
+    if (tid == 0) count = 0;
+    uint64_t kept = 0;
+    if constexpr (TOP) {
+        uint32_t big = 0;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) big = larger(big, (uint32_t)(e[i] >> 32));
+        if (a.parts >= a.top_k) {
+            float m = -__builtin_inff();
+#pragma unroll
+            for (int i = 0; i < kMaxParts / 64; ++i)
+                if (lane + 64 * i < a.parts) m = fmaxf(m, half[i].m);
+            big = m > -__builtin_inff() ? order_bits(m) : 0u;
+        }
+        big = wave_sort<true>(big);
+        if (lane == a.top_k - 1) bound[w] = big;
+        __syncthreads();
+        uint32_t tau = 1;                                      // (0 is no entry)
+#pragma unroll
+        for (int i = 0; i < NW; ++i) tau = larger(tau, bound[i]);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+            const bool have = (uint32_t)(e[i] >> 32) >= tau;
+            const unsigned long long m = __ballot(have);
+            if (m != 0) {
+                int at = 0;
+                if (lane == 0) at = atomicAdd(&count, (int)__popcll(m));
+                at = __builtin_amdgcn_readfirstlane(at) + lanes_below(m);
+                if (have && at < 64) few[at] = e[i];
+            }
+        }
+        __syncthreads();
+        const int n = count;
+        if (n <= 64) {
+            if (w == 0) kept = wave_sort<true>(lane < n ? few[lane] : 0);
+        } else {
+            // (many logits that are all alike, or the top ones all in one lane's)
+            TopList top(wait[w]);
+#pragma unroll 1
+            for (int i = 0; i < PER; ++i) {
+                uint64_t v = e[0];
+#pragma unroll
+                for (int q = 1; q < PER; ++q) v = q == i ? e[q] : v;
+                top.add((uint32_t)(v >> 32) >= tau, v);
+                top.merge(64);
+            }
+            top.merge(1);
+            kept = top.kept;
+            wait[w][lane] = kept;
+            __syncthreads();
+            if (w == 0)
+                for (int i = 1; i < NW; ++i) kept = wave_merge(kept, wait[i][63 - lane]);
+        }
+    }
+    if (w != 0) return;
+    Sums sums = {-__builtin_inff(), 0.0, 0.0};
+#pragma unroll
+    for (int i = 0; i < kMaxParts / 64; ++i)
+        if (lane + 64 * i < a.parts) sums.join(half[i]);
+    const float m = order_value(wave_reduce(order_bits(sums.m), larger<uint32_t>));
+    sums.move(m);
+    sums.s = wave_reduce(sums.s, add);
+    sums.u = wave_reduce(sums.u, add);
+    put_row(a, row, given, sums, kept);
+}
+
+template <int TYPE, bool TOP>
+const void *logprobs_kernel(const LogprobPlan &p)
+{
+    return p.part ? (const void *)&qmt_logprobs_part_kernel<TYPE, TOP> : (const void *)&qmt_logprobs_kernel<TYPE, TOP>;
+}
+
+template <bool TOP>
+const void *logprobs_kernel(int type, const LogprobPlan &p)
+{
+    return type == QMX_T_F32    ? logprobs_kernel<QMX_T_F32, TOP>(p)
+           : type == QMX_T_BF16 ? logprobs_kernel<QMX_T_BF16, TOP>(p)
+                                : logprobs_kernel<QMX_T_F16, TOP>(p);
 }
 
 // HIP limits a launch to 2^32 threads: beyond this many workgroups a kernel
 // loops or is launched again.
 constexpr long long kMaxGroups = 1LL << 20;
 
-qmv_status_t go(const void *fn, long long groups, void **args, hipStream_t stream)
+qmv_status_t go(const void *fn, long long groups, void **args, hipStream_t stream, int threads = 256)
 {
-    return hipLaunchKernel(fn, dim3((unsigned)groups), dim3(256), args, 0, stream) == hipSuccess ? QMV_OK : QMV_EHIP;
+    return hipLaunchKernel(fn, dim3((unsigned)groups), dim3((unsigned)threads), args, 0, stream) == hipSuccess
+               ? QMV_OK
+               : QMV_EHIP;
 }
 
 // Workgroups 0 .. n - 1 of a kernel whose first one's number is a.*FIRST times `unit`.
 template <class Args>
-qmv_status_t go_all(const void *fn, Args &a, long long Args::*first, long long unit, long long n, hipStream_t stream)
+qmv_status_t go_all(const void *fn, Args &a, long long Args::*first, long long unit, long long n, hipStream_t stream,
+                    int threads = 256)
 {
     void *args[] = {&a};
     for (long long g = 0; g < n; g += kMaxGroups) {
         a.*first = g * unit;
-        const qmv_status_t s = go(fn, n - g < kMaxGroups ? n - g : kMaxGroups, args, stream);
+        const qmv_status_t s = go(fn, n - g < kMaxGroups ? n - g : kMaxGroups, args, stream, threads);
         if (s != QMV_OK)
             return s;
     }
@@ -670,17 +946,17 @@ QMT_API qmv_status_t qmt_logprobs(qmx_type_t ltype, const void *logits, int M, i
     if (s != QMV_OK)
         return s;
     const LogprobPlan p = plan_logprobs(M, V);
-    if (p.parts > 1 && (!workspace || !aligned(workspace, 16)))
+    if (p.join && (!workspace || !aligned(workspace, 16)))
         return QMV_EINVAL;
     LogArgs a = {logits, tokens, logprobs, entropy, top_logprobs, top_ids, (uint8_t *)workspace, (int)ltype, M, V,
                  top_k, p.parts, p.steps, 0};
-    const void *fn = top_k ? (const void *)&qmt_logprobs_kernel<true> : (const void *)&qmt_logprobs_kernel<false>;
+    const void *fn = top_k ? logprobs_kernel<true>(ltype, p) : logprobs_kernel<false>(ltype, p);
     const void *join = top_k ? (const void *)&qmt_logprobs_join_kernel<true>
                              : (const void *)&qmt_logprobs_join_kernel<false>;
-    const qmv_status_t st = go_all(fn, a, &LogArgs::first, 1, (long long)M * p.parts, stream);
-    if (st != QMV_OK || p.parts == 1)
+    const qmv_status_t st = go_all(fn, a, &LogArgs::first, 1, (long long)M * p.parts, stream, p.threads);
+    if (st != QMV_OK || !p.join)
         return st;
-    return go_all(join, a, &LogArgs::first, 1, M, stream);
+    return go_all(join, a, &LogArgs::first, 1, M, stream, 64 * kJoinWaves);
 }
 
 QMT_API const char *qmt_strerror(qmv_status_t status) { return status_text(status); }

@@ -65,30 +65,38 @@ inline qmv_status_t check_logprobs(int ltype, const void *logits, int M, int V, 
     return QMV_OK;
 }
 
-// A row of V logits is cut into `parts`, a workgroup each, of `steps` steps of
-// kStep logits.
-constexpr int kStep = 2048;          // 256 threads of 8
-struct LogprobPlan { int parts, steps; };
+// A row of V logits is cut into `parts` (at most kMaxParts), a workgroup of
+// `threads` each that takes `steps` times 8 logits a thread: one step where all
+// parts of the call find a place on the chip at a time (part).  Unless one
+// long part is the row (join), each part leaves its sums (kListSums bytes) and a
+// list of 64 entries for a second launch, a workgroup a row.
+constexpr int kMaxParts = 128, kJoinWaves = 8, kListSums = 32;
+struct LogprobPlan {
+    int parts, threads, steps;
+    bool part, join;
+};
 
 inline LogprobPlan plan_logprobs(int M, int V)
 {
-    const int all = (V + 7 + kStep - 1) / kStep;      // (a row may start up to 7 logits inside a group of 8)
-    // workgroups for four places on each of 256 CUs, as far as the row goes
-    int parts = 1024 / M;
-    parts = parts < 1 ? 1 : parts > all ? all : parts;
-    const int steps = (all + parts - 1) / parts;
-    return {(all + steps - 1) / steps, steps};
+    auto cut = [](int of, int n) { return n / of + (n % of != 0); };
+    // (up to 14 logits before and behind whole groups of 8 go with the first part)
+    const int shorts = cut(2048, V);
+    if (shorts <= kMaxParts && (long long)shorts * M <= 1024)
+        return {shorts, 256, 1, true, true};
+    const int steps = cut(4096, V);
+    int parts = 512 / M;                              // two for each of 256 CUs, as far as the row goes
+    parts = parts < 1 ? 1 : parts > kMaxParts ? kMaxParts : parts > steps ? steps : parts;
+    const int each = cut(parts, steps);
+    parts = cut(each, steps);
+    return {parts, 512, each, false, parts > 1};
 }
-
-// Bytes of one part's result: its maximum and sums, and its top entries.
-constexpr long long part_bytes(int top_k) { return 32 + 8LL * ((top_k + 1) & ~1); }
 
 inline long long logprobs_workspace(int M, int V, int top_k)
 {
     if (M <= 0 || V <= 0 || top_k < 0 || V >= 1 << 30 || M >= 1 << 24 || top_k > kMaxTop)
         return 0;
     const LogprobPlan p = plan_logprobs(M, V);
-    return p.parts == 1 ? 0 : (long long)M * p.parts * part_bytes(top_k);
+    return p.join ? (long long)M * p.parts * (kListSums + (top_k ? 512 : 0)) : 0;
 }
 
 inline const char *status_text(int status)

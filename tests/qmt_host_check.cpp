@@ -34,11 +34,13 @@ int main()
         else if (what == "workspace")
             s = qmt_host::logprobs_workspace(i(0), i(1), i(2));
         else if (what == "covered") {
-            // every logit of a row lies in one step of one part, wherever the row starts in a group of 8
+            // every group of 8 logits of a row lies in one step of one part
             const int V = i(1);
             const qmt_host::LogprobPlan l = qmt_host::plan_logprobs(i(0), V);
-            s = l.parts >= 1 && l.steps >= 1 && (long long)l.parts * l.steps * qmt_host::kStep >= (long long)V + 7 &&
-                (long long)(l.parts - 1) * l.steps * qmt_host::kStep < (long long)V + 7;
+            const long long step = 8 * l.threads;
+            s = l.parts >= 1 && l.parts <= qmt_host::kMaxParts && l.steps >= 1 && l.threads <= 1024 &&
+                (l.part ? l.steps == 1 : l.threads == 512) && (l.join || l.parts == 1) &&
+                l.parts * l.steps * step >= V && (l.parts - 1) * l.steps * step < V;
         }
         std::printf("%lld\n", s);
     }
