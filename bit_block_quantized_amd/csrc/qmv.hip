@@ -75,10 +75,10 @@ extern const void *const kTableMx4Wide[1];
 }
 
 // e4m3 x e4m3 with a scale per block of 128 (qmv_k_f8.hip): [plain, gate/up,
-// combine], [plain, gate/up], dense.
+// combine], [whole K, halves][plain, gate/up], dense.
 namespace qmv {
 extern const void *const kTableF8Few[3];
-extern const void *const kTableF8Tile[2];
+extern const void *const kTableF8Tile[2][2];
 extern const void *const kTableF8Wide[1];
 }
 
@@ -671,7 +671,15 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
     // 28.7 and 28.1, 64 109 and 84; gate/up 8 25 and 27; 4096 -> 14336 of 8: 2
     // pairs 14.4 and 15.8).
     const long long row_tiles = (N + 15) / 16;
-    const bool many = gather ? pairs * row_tiles * h > 7 * cu_count() : M > kMaxM && (M + 15) / 16 * row_tiles > 3 * cu_count();
+    // The few kernel while the chip holds at least 2 in 5 of its workgroups at a time, by LDS and
+    // registers (us, few and after it the tile kernel: 7168 -> 7168: 8 vectors (0.9 of what the
+    // chip holds) 15 and 26, 24 (3.5) 47 and 27; 2880 -> 2880: 64 (1.4) 18 and 19, 128 (2.8) 27 and
+    // 20; 32 experts top 4, 2880 -> 2880: 2 tokens (1.4) 18 and 20, 3 (2.8) 25 and 23; gate/up: 2 (1.9)
+    // 30 and 33, 3 (2.8) 41 and 38; 256 top 8, 7168 -> 2048: 1 token (2) 26 and 35, gate/up 44
+    // and 50, 2 tokens (8) 67 and 49, gate/up 95 and 89).
+    const long long few_groups = gather ? pairs * row_tiles : (M + 15) / 16 * row_tiles;
+    const int by_regs = mode == 1 ? 3 : 5, by_lds = kLdsPerCU / few_lds(most);
+    const bool many = 2 * few_groups > 5ll * cu_count() * (by_lds < by_regs ? by_lds : by_regs);
     // (the tile kernel counts the pairs of up to 1023 experts)
     if (mode != 2 && (!gather || E <= kMaxEBatched) && (many || few_lds(most) > kLdsPerCU)) {
         const int rows = mode == 1 ? 64 : 128;
@@ -732,16 +740,14 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
                                                                                                   : QMV_EHIP;
 }
 
-LdsLimit g_f8_lds[2], g_f8_few_lds[3], g_f8_wide_lds;
+LdsLimit g_f8_lds[2][2], g_f8_few_lds[3], g_f8_wide_lds;
 
-// LDS of a tile workgroup: the chunk's list, two buffers of vector codes (chunk
-// x 128 bytes), the waves' weight pieces (128 rows x 128 bytes), and the scales
-// of the rows' one or two block rows and of the vectors.
-int f8_tile_lds(int K, int chunk)
-{
-    const int KB = (K + 127) / 128;
-    return 2 * chunk + 2 * chunk * 128 + 128 * 128 + 4 * ((2 * KB + 3) & ~3) + 4 * chunk * KB;
-}
+// LDS of a tile workgroup: the list of its vectors, and for all of K or each
+// half two blocks' codes and scales of the vectors and three blocks' codes of
+// 128 rows.
+constexpr int kF8Chunk = 96;
+constexpr int f8_tile_lds(int halves) { return 2 * kF8Chunk + halves * (2 * kF8Chunk * (128 + 4) + 3 * 128 * 128); }
+static_assert(2 * f8_tile_lds(1) <= kLdsPerCU && f8_tile_lds(2) <= kLdsPerCU, "8 waves a CU");
 
 // e4m3 x e4m3.  route_w non-null: the combine of up to 4 tokens.
 qmv_status_t launch_f8(const void *codes, const void *scales, const void *codes2, const void *scales2, int E,
@@ -762,10 +768,10 @@ qmv_status_t launch_f8(const void *codes, const void *scales, const void *codes2
     const int mode = route_w ? 2 : codes2 ? 1 : 0;
     const int pairs = gather ? M * top_k : M;
     // 256 x 128 tiles once they fill more than half of the CUs and most of their
-    // vectors exist (wide and, after it, the tile kernel's 128 x 64: 7168 -> 7168:
-    // 512 vectors (112 tiles) 84 and 83, 1024 100 and 156; 7168 -> 2048: 2048
-    // (128 tiles) 84 and 81, 4096 108 and 153; 7168 -> 40960: 64 (160 tiles) 96 and 87,
-    // 128 105 and 125).
+    // vectors exist (us, wide and after it the tile kernel: 7168 -> 7168: 512 vectors (112
+    // tiles) 84 and 89, 1024 (224) 99 and 147; 7168 -> 2048: 1024 (64) 79 and 50, 2048 (128)
+    // 82 and 88; 2880 -> 2880: 1024 (96) 40 and 28, 2048 (192) 45 and 47; 7168 -> 40960 (160): 64
+    // 96 and 88, 128 105 and 122).
     const long long wide_tiles = (long long)((N + 255) / 256) * ((M + 127) / 128);
     if (!gather && M > 64 && 2 * wide_tiles > cu_count()) {
         const int lds = 2 * (256 + 128) * 128 + 2 * 128 * 4;
@@ -789,20 +795,18 @@ qmv_status_t launch_f8(const void *codes, const void *scales, const void *codes2
     if (mode != 2 && (!gather || E <= kMaxEBatched) && (many || few_lds(most) > kLdsPerCU)) {
         const int rows = mode == 1 ? 64 : 128;
         a.bt_row_tiles = (N + rows - 1) / rows;
-        const int chunk = 64;
         // items at most: a whole chunk each and a rest per expert
-        const long long items = gather ? (pairs < E ? pairs : E) + pairs / chunk : (M + chunk - 1) / chunk;
-        // runs of row tiles: about 8 workgroups for each that the chip holds at a time
-        const int lds = f8_tile_lds(K, chunk);
-        const long long slots = (long long)cu_count() * (lds * 2 <= kLdsPerCU ? 2 : 1);
-        const long long run = items * a.bt_row_tiles / (8 * slots);
-        a.bt_chunk = run < 1 ? 1 : run > a.bt_row_tiles ? a.bt_row_tiles : (int)run;
-        const long long groups = items * ((a.bt_row_tiles + a.bt_chunk - 1) / a.bt_chunk);
-        if (g_f8_lds[mode].set(kTableF8Tile[mode], f8_tile_lds(kMaxK, chunk)) != hipSuccess)
+        const long long items = gather ? (pairs < E ? pairs : E) + pairs / kF8Chunk : (M + kF8Chunk - 1) / kF8Chunk;
+        const long long groups = items * a.bt_row_tiles;
+        // K in two halves while that leaves no CU a second tile (whole and halves: 7168 -> 7168, 8
+        // vectors (56 tiles) 37 and 26, 256 (168) 60 and 52, 512 (336) 89 and 99; 32 experts top 4,
+        // 2880 -> 2880, 2 tokens (184) 22 and 20, 4 (368) 28 and 38)
+        const int hv = groups <= cu_count() ? 1 : 0;
+        if (g_f8_lds[hv][mode].set(kTableF8Tile[hv][mode], f8_tile_lds(hv + 1)) != hipSuccess)
             return QMV_EHIP;
         void *kargs[] = {&a};
-        return hipLaunchKernel(kTableF8Tile[mode], dim3((unsigned)(8 * ((groups + 7) / 8))), dim3(256), kargs, lds,
-                               stream) == hipSuccess ? QMV_OK : QMV_EHIP;
+        return hipLaunchKernel(kTableF8Tile[hv][mode], dim3((unsigned)(8 * ((groups + 7) / 8))), dim3(256 * (hv + 1)), kargs,
+                               f8_tile_lds(hv + 1), stream) == hipSuccess ? QMV_OK : QMV_EHIP;
     }
     // few vectors: 16-row tiles, K split over the waves
     a.bt_row_tiles = (int)row_tiles;

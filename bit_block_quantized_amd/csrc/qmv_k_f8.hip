@@ -1,7 +1,6 @@
 // qmv_k_f8.hip -- e4m3 weights with an fp32 scale per 128 x 128 block x e4m3
-// activations with an fp32 scale per 128, on the f16 matrix cores
-// (v_mfma_f32_16x16x32_bf16): dense, gather, gate/up with SwiGLU, and the
-// combine of up to 4 tokens.
+// activations with an fp32 scale per 128, on the matrix cores' bf16 products:
+// dense, gather, gate/up with SwiGLU, and the combine of up to 4 tokens.
 //
 //     y = sum over blocks b of (sw_b * sx_b) * sum_128 e4m3 * e4m3
 //
@@ -11,12 +10,12 @@
 // the largest: a block of normal values' codes came out 2e-6 of the sum of its
 // magnitudes off (1e-5 of the result), with bf16 operands 2e-9.
 //
-// Four instructions (16 rows x 32 k of A, 32 k x 16 columns of B) form a
-// block's whole sum in fp32 from zero, which one multiply-add per output adds
-// to the result with the product of the block's two scales.  A lane holds 32
-// bytes of its row (column): lane (c, q) = lane 16 q + c takes chunks q and q +
-// 4 (16 bytes each) of row c's 128.  (A sum does not care which k a lane
-// holds, as long as both operands agree.)
+// The products of a block form its whole sum in fp32 from zero, which one
+// multiply-add per output adds to the result with the product of the block's two
+// scales: four 16 x 16 x 32 instructions, or eight of 32 x 32 x 16.  With the
+// former a lane holds 32 bytes of its row (column): lane (c, q) = lane 16 q + c
+// takes chunks q and q + 4 (16 bytes each) of row c's 128.  (A sum does not care
+// which k a lane holds, as long as both operands agree.)
 //
 // Times here are a kernel's own: its median in a trace of ten calls with three
 // sets of weights and vectors in turn.
@@ -29,8 +28,7 @@ namespace qmv {
 
 constexpr int kF8Few = 16;           // vectors of a few-vector workgroup
 constexpr int kF8Waves = kRoutedWaves;
-constexpr int kF8Chunk = 64;         // vectors of a tile at most
-constexpr int kF8RF = 2;             // 16-row fragments per wave of a tile
+constexpr int kF8Chunk = 96;         // vectors of a tile at most
 constexpr int kF8Block = 128;        // weights of a block, and code bytes
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -72,85 +70,108 @@ __device__ __forceinline__ void add_scaled(f32x4 &acc, f32x4 part, float s)
     for (int k = 0; k < 4; ++k) acc[k] = __builtin_fmaf(part[k], s, acc[k]);
 }
 
-// ------------------------------------------------------------- many vectors
-// A tile is (expert, 128 weight rows; gate/up: 64 of each) against a chunk of
-// its vectors (up to 64), 4 waves of 2 x CF fragments each.  K goes in
-// units of one block.
-//
-// Codes are loaded as they lie -- 8 lanes take a row's 128 bytes, 8 rows a
-// load -- and turned into operand order by a pass through LDS (swz_chunk):
-//   codes of the rows   through a piece of LDS of the wave's own (LDS keeps a
-//                       wave's accesses in order: no barrier), two units ahead
-//                       in registers
-//   codes of the vectors  staged by all waves, double-buffered, one unit ahead
-//   scales              of the tile's block row(s) and of all the vectors,
-//                       staged once for all of K
-// One barrier per unit; two workgroups of 4 waves share a CU.
-//
+// The 32 x 32 instruction: lane (n, k) = lane 32 k + n holds chunks k, k + 2, k +
+// 4, k + 6 of row (column) n's 128 bytes, eight instructions' values, and of
+// the products rows 8 i + 4 k .. of column n in registers 4 i .. .
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// A chunk's 16 codes: two instructions' values.
+__device__ __forceinline__ void widen_chunk(u32x4 c, bf16x8 &lo, bf16x8 &hi)
+{
+    u32x4 h[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        h[i >> 1][2 * (i & 1)] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], 1.0f, false));
+        h[i >> 1][2 * (i & 1) + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], 1.0f, true));
+    }
+    lo = __builtin_bit_cast(bf16x8, h[0]);
+    hi = __builtin_bit_cast(bf16x8, h[1]);
+}
+
+// Keeps what forms x here: without it the compiler moves products, conversions
+// and additions to their results' first use, with all their operands held.
+template <class T> __device__ __forceinline__ void pin(T &x) { asm volatile("" : "+v"(x)); }
+
+__device__ __forceinline__ f32x16 mfma32(const bf16x8 &x, const bf16x8 &y, const f32x16 &z)
+{
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, z, 0, 0, 0);
+}
+
+// Waits until at most N of the wave's loads (and stores) are on their way and
+// its reads of LDS are done, then for the workgroup.  (A barrier of the
+// compiler's waits for every load into LDS.)
+template <int N> __device__ __forceinline__ void wait_loads_barrier()
+{
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" ::"n"(N) : "memory");
+}
+
+typedef __attribute__((address_space(3))) void lds_t;
+
 template <int... I, class Part>
 __device__ __forceinline__ void parts(std::integer_sequence<int, I...>, Part part)
 {
     (part(std::integral_constant<int, I>{}), ...);
 }
 
-// Row tiles rt0 .. rt1 - 1 of expert e against nv vectors: pairs vecs[0..nv)
-// of a routed call, vectors vstart .. of a dense one (vecs null).
-template <int MODE, int CF>
-__device__ __forceinline__ void f8_tile_run(const Args &a, uint8_t *lds, int e, int rt0, int rt1,
-                                            const uint16_t *vecs, int vstart, int nv)
+// The sums to add after product k of eight: from the third on, when the last product before has them.
+constexpr __host__ __device__ int from_k(int k) { return k < 2 ? 0 : k == 8 ? 16 : 3 * k - 6; }
+
+// ------------------------------------------------------------- many vectors
+// A tile is (expert, 128 weight rows; gate/up: 64 of each) against a chunk of
+// its vectors (up to 32 CF): 4 waves of 32 rows -- gate/up has the gate's 16 in
+// registers 0 .. 7 of the products and the up projection's in 8 .. 15 -- for
+// all of K, two such workgroups a CU, or for each of two halves of K (HV), the
+// even and the odd blocks, where there are no more tiles than CUs.
+//
+// Codes go from memory into LDS without passing registers, 8 rows of 128 bytes
+// a load, and the place of a lane's 16 bytes (byte 16 l of the piece) is that
+// of chunk l % 8 ^ (row / 2 % 8) of its row, so that 16 lanes that read a chunk of
+// 16 rows touch 16 different bank groups.  While a block is multiplied, the
+// rows' codes of a half's next two are on their way and the vectors' of the
+// next.  A wave's rows are its own; a half's vectors are staged by its four waves,
+// one barrier a block.
+//
+// Bound by the weight bytes (gate/up of 32 experts top 4, 2880 -> 2880, 531 MB:
+// 64 tokens 124 us, 4.3 TB/s; with rows of 2816 109, 4.8 TB/s: their blocks do not
+// straddle cache lines), with many vectors by what a block costs beside them (512
+// tokens 153 us, 700 170; without any load from memory 109 and 133 with rows of
+// 2816).  Fragments of 16 x 16 staged through registers, 64 vectors a tile: 512
+// tokens of popular and unpopular experts 185 us, so 181; 7168 -> 7168, 1024 vectors
+// 156 us, so 147.  All tiles in two halves: 227 and 153.  Runs of row tiles that
+// share the counting of the pairs: 2 187 us, 3 215.
+constexpr int kF8Ring = 3;           // blocks of the rows' codes in LDS
+
+// Row tile rt of expert e against nv vectors: pairs vecs[0..nv) of a routed
+// call, vectors vstart .. of a dense one (vecs null).
+template <int MODE, int HV, int CF>
+__device__ __forceinline__ void f8_tile(const Args &a, uint8_t *lds, int e, int rt, const uint16_t *vecs, int vstart, int nv)
 {
-    constexpr int NW = kF8Waves, RF = kF8RF;
-    constexpr int RH = MODE == 1 ? RF / 2 : RF;      // output row fragments per wave
-    constexpr int TR = 16 * RH * NW;                 // output rows of a tile
-    constexpr int XU = (2 * CF + NW - 1) / NW;       // staged pieces (8 vectors x 128 bytes) per wave and unit
-    constexpr int XB = CF * 2048;                    // bytes of one vector buffer
-    constexpr int GB = CF < 2 ? 1 : 2, HG = CF / GB; // vector fragments read at a time; groups of them
+    constexpr int R = kF8Ring;
+    constexpr int TR = MODE == 1 ? 64 : 128;         // output rows of a tile
+    constexpr int PX = CF;                           // pieces of the vectors a wave stages
+    constexpr int HALF = 2 * CF * 4096 + 2 * CF * 128 + 4 * R * 4096;
     int tid = threadIdx.x;
-    asm volatile("" : "+v"(tid));                    // (keeps the offsets below out of the caller's loop head)
+    asm volatile("" : "+v"(tid));                    // (keeps the offsets below out of the caller's registers)
     const int lane = tid & 63;
-    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
-    uint8_t *const lx = lds;                                      // [2][CF][16 vectors x 128 bytes]
-    uint8_t *const la = lds + 2 * kF8Chunk * 128 + w * (RF * 2048);     // [RF][16 rows x 128 bytes], this wave's
-    float *const lw = (float *)(lds + 2 * kF8Chunk * 128 + NW * RF * 2048);   // [MODE == 1 ? 2 : 1][KB]
-    const int c = lane & 15, q = lane >> 4;
-    const int lr = lane >> 3, lc = lane & 7;         // row and chunk of a load
+    const int half = HV == 2 ? __builtin_amdgcn_readfirstlane(tid >> 8) : 0, w = __builtin_amdgcn_readfirstlane(tid >> 6 & 3);
+    const int n = lane & 31, hk = lane >> 5;
+    const int lr = lane >> 3, lc = (lane & 7) ^ (lr >> 1);           // row and chunk of a load's even pieces; odd: ^ 4
     const bool gather = vecs != nullptr;
     const int N = a.N;
     const int KB = a.units, U = a.K >> 4;            // blocks, 16-byte chunks of a row
-    float *const ls = lw + ((2 * KB + 3) & ~3);      // [KB][16][CF]
+    uint8_t *const lx = lds + half * HALF;                            // [2][CF][32 vectors x 128 bytes]
+    float *const ls = (float *)(lx + 2 * CF * 4096);                  // [2][32 CF]
+    uint8_t *const lw = lx + 2 * CF * 4096 + 2 * CF * 128 + w * (R * 4096);   // this wave's: [R][32 rows x 128 bytes]
 
+    // rows past N repeat the last one and are not stored
     const __amdgpu_buffer_rsrc_t rc0 = buffer_rsrc(a.codes + e * a.expert_cb, a.expert_cb);
     const __amdgpu_buffer_rsrc_t rc1 = buffer_rsrc((MODE == 1 ? a.codes2 : a.codes) + e * a.expert_cb, a.expert_cb);
-    // rows past N repeat the last one and are not stored
-    uint32_t oc[RF][2];
-    auto set_rows = [&](int row_base) {
+    uint32_t oc[4];
 #pragma unroll
-        for (int f = 0; f < RF; ++f)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int n = min(row_base + 16 * RH * w + 16 * (MODE == 1 ? f % RH : f) + 8 * i + lr, N - 1);
-                oc[f][i] = (uint32_t)n * (uint32_t)a.rcb + 16u * lc;
-            }
-    };
-    // (chunks past the row's end read zeros: the bytes there are another row's)
-    auto load_a = [&](int u, u32x4 (&A)[RF][2]) {
-        const uint32_t so = 8 * u + lc < U ? 128u * u : kXPast;      // (oc < 2^31: the sum does not wrap)
-#pragma unroll
-        for (int f = 0; f < RF; ++f)
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                A[f][i] = __builtin_amdgcn_raw_buffer_load_b128(MODE == 1 && f >= RH ? rc1 : rc0, oc[f][i] + so, 0, 0);
-    };
-    const int wst = swz_chunk(lr, lc);               // rows 8 further: + 1024, ^ 64
-    auto store_a = [&](const u32x4 (&A)[RF][2]) {
-#pragma unroll
-        for (int f = 0; f < RF; ++f) {
-            *(u32x4 *)(la + f * 2048 + wst) = A[f][0];
-            *(u32x4 *)(la + f * 2048 + 1024 + (wst ^ 64)) = A[f][1];
-        }
-    };
-
-    // staged vectors: piece p = vectors 8 p .. 8 p + 7; wave w takes pieces w, w + NW, ...
+    for (int p = 0; p < 4; ++p) {
+        const int row = rt * TR + (MODE == 1 ? 16 * w + 8 * (p & 1) : 32 * w + 8 * p) + lr;
+        oc[p] = (uint32_t)min(row, N - 1) * (uint32_t)a.rcb + 16u * (lc ^ (4 * (p & 1)));
+    }
     const int top_k = a.top_k;
     const bool by_token = gather && !a.x_per_slot;
     auto vec_row = [&](int v) -> uint32_t {
@@ -159,211 +180,223 @@ __device__ __forceinline__ void f8_tile_run(const Args &a, uint8_t *lds, int e, 
     };
     const int x_rows = gather && a.x_per_slot ? a.M * a.top_k : a.M;
     const __amdgpu_buffer_rsrc_t rx = buffer_rsrc(a.x, (long long)x_rows * a.x_vec_bytes);
-    uint32_t ox[XU];
+    const __amdgpu_buffer_rsrc_t rs = buffer_rsrc(a.xs, (long long)x_rows * KB * 4);
+    uint32_t ox[PX];                                 // wave w stages pieces w, w + 4: vectors 8 w .. of a fragment
 #pragma unroll
-    for (int k = 0; k < XU; ++k) {
-        const int v = 8 * (w + NW * k) + lr;
-        ox[k] = v < nv ? vec_row(v) * (uint32_t)a.x_vec_bytes + 16u * lc : kXPast;
+    for (int k = 0; k < PX; ++k) {
+        const int v = 32 * k + 8 * w + lr;
+        ox[k] = v < nv ? vec_row(v) * (uint32_t)a.x_vec_bytes + 16u * (lc ^ (4 * (w & 1))) : kXPast;
     }
-    auto load_x = [&](int u, u32x4 (&X)[XU]) {
+    const int sv = 64 * w + lane;                    // the vector whose scale this lane stages
+    const uint32_t os = sv < nv ? vec_row(sv) * (uint32_t)KB * 4u : kXPast;
+    // the blocks that are loaded next, rows' and vectors': number, place
+    // (chunks past the row's end read zeros: the bytes there are another row's;
+    // as many loads past the last block as before it, of zeros)
+    int u_l = half, at_l = 0, u_x = half, at_x = 0;
+    auto load_rows = [&] {
+        const uint32_t past0 = 8 * u_l + lc < U ? 128u * u_l : kXPast;
+        const uint32_t past1 = 8 * u_l + (lc ^ 4) < U ? 128u * u_l : kXPast;
 #pragma unroll
-        for (int k = 0; k < XU; ++k) {
-            const bool ok = 8 * u + lc < U && ox[k] != kXPast;
-            X[k] = __builtin_amdgcn_raw_buffer_load_b128(rx, ok ? ox[k] + 128u * u : kXPast, 0, 0);
-        }
+        for (int p = 0; p < 4; ++p)                                  // (oc < 2^31: the sum does not wrap)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(MODE == 1 && p >= 2 ? rc1 : rc0, (lds_t *)(lw + at_l * 4096 + p * 1024), 16,
+                                                     oc[p] + (p & 1 ? past1 : past0), 0, 0, 0);
+        at_l = at_l == R - 1 ? 0 : at_l + 1;
+        u_l += HV;
     };
-    auto store_x = [&](int buf, const u32x4 (&X)[XU]) {
+    auto load_vecs = [&] {
+        const uint32_t past = 8 * u_x + (w & 1 ? lc ^ 4 : lc) < U ? 128u * u_x : kXPast;
 #pragma unroll
-        for (int k = 0; k < XU; ++k) {
-            const int p = w + NW * k;
-            if (2 * CF >= NW || w < 2 * CF)
-                *(u32x4 *)(lx + buf * XB + p * 1024 + (wst ^ ((p & 1) << 6))) = X[k];
-        }
+        for (int k = 0; k < PX; ++k)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_t *)(lx + at_x * (CF * 4096) + k * 4096 + w * 1024), 16,
+                                                     past == kXPast ? kXPast : ox[k] + past, 0, 0, 0);
+        if (w < (CF + 1) / 2 && sv < 32 * CF)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_t *)(ls + at_x * (32 * CF) + 64 * w), 4,
+                                                     u_x < KB ? os + 4u * u_x : kXPast, 0, 0, 0);
+        at_x ^= 1;
+        u_x += HV;
     };
-    // scales: the tile's rows lie in one block row
-    auto stage_rows = [&](int row_base) {
-        const float *const s0 = (const float *)(a.scales + e * a.expert_sb) + (size_t)(row_base / kF8Block) * KB;
-        const float *const s1 = (const float *)((MODE == 1 ? a.scales2 : a.scales) + e * a.expert_sb) +
-                                (size_t)(row_base / kF8Block) * KB;
-        if (tid < KB) {
-            lw[tid] = s0[tid];
-            if constexpr (MODE == 1) lw[KB + tid] = s1[tid];
-        }
+    // the tile's rows lie in one block row of the scales
+    typedef const __attribute__((address_space(4))) float scalar_float;
+    auto row_scale = [&](const uint8_t *base, int u) {
+        const long long at = (long long)(rt * TR / kF8Block) * KB + min(u, KB - 1);
+        const float s = *(scalar_float *)(uintptr_t)(base + e * a.expert_sb + 4 * at);
+        return u < KB ? s : 0.0f;
     };
-    auto stage_vecs = [&] {
-        const float *const xs = (const float *)a.xs;
-#pragma unroll 4
-        for (int t = tid; t < 16 * CF * KB; t += 64 * NW) {
-            const int v = t / KB, u = t - v * KB;
-            ls[(u * 16 + (v & 15)) * CF + (v >> 4)] = v < nv ? xs[(size_t)vec_row(v) * KB + u] : 0.0f;
-        }
-    };
-    const int rd = c * 128 + 16 * (q ^ ((c >> 1) & 7));         // chunk q of row c; chunk q + 4: ^ 64
-    const bool vec4 = (N & 3) == 0 && ((uintptr_t)a.y & 15) == 0;
+    const int rd = n * 128 + 16 * (hk ^ (n >> 1 & 7));
 
-    // While unit u multiplies, its codes stand in LDS and those of units u + 1
-    // and u + 2 are on their way to A[(u + 1) % 2], A[u % 2] and X likewise:
-    // every load has a whole unit's time before its registers are needed.
-    u32x4 A0[RF][2], A[2][RF][2], X[2][XU];
-    auto first_loads = [&](int row_base) {
-        set_rows(row_base);
-        load_a(0, A0);
-        load_x(0, X[0]);
-        load_x(1, X[1]);
-        load_a(1, A[1]);
-        load_a(2, A[0]);
-    };
-    first_loads(rt0 * TR);
-    for (int rt = rt0; rt < rt1; ++rt) {
-        const int row_base = rt * TR;
-        if (rt == rt0) stage_vecs();
-        stage_rows(row_base);
-        store_a(A0);
-        store_x(0, X[0]);
-        f32x4 acc[RF][CF];
+    float acc[CF][16];
+    f32x16 sum[CF];
+    float by0[CF], by1[CF];                          // the scales that the sums take: registers 0 .. 7, 8 .. 15
 #pragma unroll
-        for (int f = 0; f < RF; ++f)
+    for (int g = 0; g < CF; ++g) {
+        by0[g] = by1[g] = 0.0f;
 #pragma unroll
-            for (int g = 0; g < CF; ++g) acc[f][g] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        __syncthreads();
-        auto unit = [&](auto HALF, int u) {
-            constexpr int h = decltype(HALF)::value;            // the unit's vector buffer too
-            u32x4 F[RF][2], B[2][GB][2];
-            auto read_b = [&](int i, u32x4 (&b)[GB][2]) {
+        for (int i = 0; i < 16; ++i) acc[g][i] = sum[g][i] = 0.0f;
+    }
+    auto scale = [&](int g, int i0, int i1) {
 #pragma unroll
-                for (int g = 0; g < GB; ++g)
-#pragma unroll
-                    for (int s = 0; s < 2; ++s)
-                        b[g][s] = *(const u32x4 *)(lx + h * XB + (i * GB + g) * 2048 + (rd ^ (64 * s)));
-            };
-#pragma unroll
-            for (int f = 0; f < RF; ++f)
-#pragma unroll
-                for (int s = 0; s < 2; ++s) F[f][s] = *(const u32x4 *)(la + f * 2048 + (rd ^ (64 * s)));
-            read_b(0, B[0]);
-            const float sw0 = lw[u], sw1 = MODE == 1 ? lw[KB + u] : 0.0f;
-            load_x(u + 2, X[h]);
-            asm volatile("" ::: "memory");                      // (the next unit's codes go where these were)
-            store_a(A[h ^ 1]);
-            load_a(u + 3, A[h ^ 1]);
-            Wide W[RF];
-#pragma unroll
-            for (int f = 0; f < RF; ++f) W[f] = widen(F[f]);
-            auto part = [&](auto IDX) {
-                constexpr int i = decltype(IDX)::value;
-                __builtin_amdgcn_sched_barrier(0);
-                if constexpr (i + 1 < HG) read_b(i + 1, B[(i + 1) & 1]);
-                f32x4 sum[RF][GB];
-                Wide b[GB];
-                float sx[GB];
-#pragma unroll
-                for (int g = 0; g < GB; ++g) b[g] = widen(B[i & 1][g]);
-#pragma unroll
-                for (int g = 0; g < GB; ++g) sx[g] = ls[(u * 16 + c) * CF + i * GB + g];
-#pragma unroll
-                for (int g = 0; g < GB; ++g)
-#pragma unroll
-                    for (int f = 0; f < RF; ++f) sum[f][g] = block_sum(W[f], b[g]);
-#pragma unroll
-                for (int g = 0; g < GB; ++g)
-#pragma unroll
-                    for (int f = 0; f < RF; ++f)
-                        add_scaled(acc[f][i * GB + g], sum[f][g], (MODE == 1 && f >= RH ? sw1 : sw0) * sx[g]);
-                // (keeps the products on this side of the barrier)
-#pragma unroll
-                for (int g = 0; g < GB; ++g)
-#pragma unroll
-                    for (int f = 0; f < RF; ++f) asm volatile("" : "+v"(acc[f][i * GB + g]));
-            };
-            parts(std::make_integer_sequence<int, HG>{}, part);
-            store_x(h ^ 1, X[h ^ 1]);
-            __syncthreads();
-        };
-        int u = 0;
-        for (; u + 1 < KB; u += 2) {
-            unit(std::integral_constant<int, 0>{}, u);
-            unit(std::integral_constant<int, 1>{}, u + 1);
+        for (int i = i0; i < i1; ++i) {
+            acc[g][i] = __builtin_fmaf(sum[g][i], MODE == 1 && i >= 8 ? by1[g] : by0[g], acc[g][i]);
+            pin(acc[g][i]);
         }
-        if (u < KB) unit(std::integral_constant<int, 0>{}, u);
+    };
+    const f32x16 zero = {};
 
-        // the next tile's first loads go out before this tile's results
-        if (rt + 1 < rt1) first_loads(row_base + TR);
-        // lane (c, q) holds rows 4 q .. 4 q + 3 of vector c of each fragment
-        int vc = c;
-        asm volatile("" : "+v"(vc));                                // (the rows' addresses are formed here, not kept)
+    load_rows();
+    load_vecs();
+    load_rows();
+    float sw0 = row_scale(a.scales, half), sw1 = MODE == 1 ? row_scale(a.scales2, half) : 0.0f;
+    int at = 0, ax = 0;
+    for (int u = half; u < KB + half; u += HV) {     // (both halves as often)
+        // this block's codes are here (the last loads are the next one's
+        // rows), and the places of the one before are free
+        wait_loads_barrier<4>();
+        load_vecs();
+        load_rows();
+        const uint8_t *const pa = lw + at * 4096, *const pb = lx + ax * (CF * 4096);
+        auto chunk = [&](const uint8_t *base, int j) { return *(const u32x4 *)(base + (rd ^ (32 * j))); };
+        u32x4 ra[4], rb[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) ra[j] = chunk(pa, j), rb[j] = chunk(pb, j);
+        float sx[CF];
+#pragma unroll
+        for (int g = 0; g < CF; ++g) sx[g] = ls[ax * (32 * CF) + 32 * g + n];
+        const float sn0 = row_scale(a.scales, u + HV), sn1 = MODE == 1 ? row_scale(a.scales2, u + HV) : 0.0f;
+        bf16x8 W[8], B[8];
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            widen_chunk(ra[j], W[2 * j], W[2 * j + 1]);
+            widen_chunk(rb[j], B[2 * j], B[2 * j + 1]);
+        }
+        if constexpr (CF == 1) scale(0, 0, 16);
 #pragma unroll
         for (int g = 0; g < CF; ++g) {
-            const int v = 16 * g + vc;
-            if (v < nv) {
-                float *const yr = a.y + (size_t)(gather ? (int)vecs[v] : vstart + v) * N;
+            if (g + 1 < CF) {
 #pragma unroll
-                for (int f = 0; f < RH; ++f) {
-                    const int n0 = row_base + 16 * RH * w + 16 * f + 4 * q;
-                    float r[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        r[k] = MODE == 1 ? swiglu(acc[f][g][k], acc[f + RF - RH][g][k]) : acc[f][g][k];
-                    if (n0 < N) {
-                        if (vec4) {
-                            *(float4 *)(yr + n0) = make_float4(r[0], r[1], r[2], r[3]);
-                        } else {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                if (n0 + k < N) yr[n0 + k] = r[k];
-                        }
-                    }
-                }
+                for (int j = 0; j < 4; ++j) rb[j] = chunk(pb + (g + 1) * 4096, j);
             }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                sum[g] = mfma32(W[k], B[k], k ? sum[g] : zero);
+                pin(sum[g]);
+                // (the sums of the fragment before, of the block before)
+                if constexpr (CF > 1) scale(g ? g - 1 : CF - 1, from_k(k), from_k(k + 1));
+                if (g + 1 < CF && (k & 1)) {
+                    widen_chunk(rb[k >> 1], B[k - 1], B[k]);
+                    pin(B[k - 1]);
+                    pin(B[k]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            by0[g] = sw0 * sx[g];
+            by1[g] = sw1 * sx[g];
+        }
+        sw0 = sn0, sw1 = sn1;
+        at = at == R - 1 ? 0 : at + 1;
+        ax ^= 1;
+    }
+    scale(CF - 1, 0, 16);
+
+    const bool vec4 = (N & 3) == 0 && ((uintptr_t)a.y & 15) == 0;
+    auto store = [&](int v, int n0, const float (&r)[4]) {
+        if (v < nv && n0 < N) {
+            float *const yr = a.y + (size_t)(gather ? (int)vecs[v] : vstart + v) * N + n0;
+            if (vec4) {
+                *(float4 *)yr = make_float4(r[0], r[1], r[2], r[3]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (n0 + k < N) yr[k] = r[k];
+            }
+        }
+    };
+    const int row0 = rt * TR + (MODE == 1 ? 16 : 32) * w + 4 * hk;   // registers 4 i ..: rows row0 + 8 i ..
+    wait_loads_barrier<0>();                         // (nothing on its way into LDS; all its codes are read)
+    if constexpr (HV == 1) {
+#pragma unroll
+        for (int g = 0; g < CF; ++g)
+#pragma unroll
+            for (int i = 0; i < (MODE == 1 ? 2 : 4); ++i) {
+                float q[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    q[k] = MODE == 1 ? swiglu(acc[g][4 * i + k], acc[g][(4 * i + 8 + k) & 15]) : acc[g][4 * i + k];
+                store(32 * g + n, row0 + 8 * i, q);
+            }
+        return;
+    }
+    // Each half gives the other one half of its registers (gate/up: of the
+    // gate's and of the up projection's), and stores the rest.
+    float *const give = (float *)lds + (4 * half + w) * (CF * 512) + lane;
+    const float *const take = (const float *)lds + (4 * (half ^ 1) + w) * (CF * 512) + lane;
+    // registers of the part that half h keeps
+    auto reg = [](int h, int i) { return MODE == 1 ? 8 * (i >> 2) + 4 * h + (i & 3) : 8 * h + i; };
+#pragma unroll
+    for (int g = 0; g < CF; ++g)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) give[(8 * g + i) * 64] = half ? acc[g][reg(0, i)] : acc[g][reg(1, i)];
+    __syncthreads();
+#pragma unroll
+    for (int g = 0; g < CF; ++g) {
+        float r[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)                  // (two terms: the same sum in either order)
+            r[i] = (half ? acc[g][reg(1, i)] : acc[g][reg(0, i)]) + take[(8 * g + i) * 64];
+#pragma unroll
+        for (int i = 0; i < (MODE == 1 ? 1 : 2); ++i) {
+            float q[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) q[k] = MODE == 1 ? swiglu(r[k], r[4 + k]) : r[4 * i + k];
+            store(32 * g + n, row0 + (MODE == 1 ? 8 * half : 16 * half + 8 * i), q);
         }
     }
 }
 
-// A workgroup takes a run of up to bt_chunk row tiles of one item.  Workgroup
-// b runs on XCD b % 8; the runs (item-major) are dealt to the XCDs in
-// contiguous parts, so that an XCD's L2 holds the vectors of a few experts,
-// and an expert's second chunk finds its weights there.
-template <int MODE>
-__global__ __launch_bounds__(64 * kF8Waves, 2) void qmv_f8_tile_kernel(const Args a)
+// Workgroup b runs on XCD b % 8; the tiles (item-major) are dealt to the XCDs
+// in contiguous parts, so that an XCD's L2 holds the vectors of a few experts.
+template <int MODE, int HV>
+__global__ __launch_bounds__(64 * kF8Waves * HV, 2) void qmv_f8_tile_kernel(const Args a)
 {
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-    constexpr int CHUNK = kF8Chunk, TR = 16 * kF8RF * kF8Waves / (MODE == 1 ? 2 : 1);
+    constexpr int CHUNK = kF8Chunk, TR = MODE == 1 ? 64 : 128;
     uint16_t *const list = (uint16_t *)lds;           // [CHUNK]
-    uint8_t *const buf = lds + 2 * CHUNK;
-    const int runs = (a.bt_row_tiles + a.bt_chunk - 1) / a.bt_chunk;   // per item
-    int item = -1, rt0 = 0, rt1 = 0;
+    uint8_t *const buf = lds + 2 * CHUNK;             // (16-byte aligned)
+    int item = -1, rt = 0;
     auto pick = [&](int items) {
-        const int all = items * runs, per_xcd = (all + 7) / 8, i = blockIdx.x >> 3;
+        const int all = items * a.bt_row_tiles, per_xcd = (all + 7) / 8, i = blockIdx.x >> 3;
         const int r = i < per_xcd ? (int)(blockIdx.x & 7) * per_xcd + i : all;
         if (r < all) {
-            item = r / runs;
-            rt0 = (r - item * runs) * a.bt_chunk;
-            rt1 = min(rt0 + a.bt_chunk, a.bt_row_tiles);
+            item = r / a.bt_row_tiles;
+            rt = r - item * a.bt_row_tiles;
         }
         return item;
     };
     int e = 0, nv, vstart = 0;
     const bool gather = a.ids != nullptr;
     if (gather) {
-        // (a call without any id in [0, E) still has its zero rows: one item)
-        const int P = a.M * a.top_k;
+        // (a call without any id in [0, E) still has its zero rows: one item.
+        // The first half counts; the other has no pairs)
+        const int P = threadIdx.x < 64 * kRoutedWaves ? a.M * a.top_k : 0;
         const RoutedItem it = routed_item<CHUNK>(a.ids, P, a.E, (int *)buf, list, [&](int items) { return pick(max(items, 1)); });
         if (item < 0) return;
         e = it.e;
         nv = it.nv;
-        routed_zero_rows(a, item, max(it.items, 1), rt0 * TR, min(rt1 * TR, a.N));
+        if (threadIdx.x < 64 * kRoutedWaves) routed_zero_rows(a, item, max(it.items, 1), rt * TR, min(rt * TR + TR, a.N));
         if (nv == 0) return;
     } else {
-        if (pick((a.M + CHUNK - 1) / CHUNK) < 0) return;
-        vstart = item * CHUNK;
-        nv = min(CHUNK, a.M - vstart);
+        const int chunks = (a.M + CHUNK - 1) / CHUNK, cs = (a.M + chunks - 1) / chunks;   // equal chunks
+        if (pick(chunks) < 0) return;
+        vstart = item * cs;
+        nv = min(cs, a.M - vstart);
     }
     const uint16_t *const vecs = gather ? list : nullptr;
-    if (nv > 32)
-        f8_tile_run<MODE, 4>(a, buf, e, rt0, rt1, vecs, vstart, nv);
-    else if (nv > 16)
-        f8_tile_run<MODE, 2>(a, buf, e, rt0, rt1, vecs, vstart, nv);
+    if (nv > 64)
+        f8_tile<MODE, HV, 3>(a, buf, e, rt, vecs, vstart, nv);
+    else if (nv > 32)
+        f8_tile<MODE, HV, 2>(a, buf, e, rt, vecs, vstart, nv);
     else
-        f8_tile_run<MODE, 1>(a, buf, e, rt0, rt1, vecs, vstart, nv);
+        f8_tile<MODE, HV, 1>(a, buf, e, rt, vecs, vstart, nv);
 }
 
 // -------------------------------------------------------------- few vectors
@@ -616,25 +649,6 @@ __global__ __launch_bounds__(64 * kF8Waves) void qmv_f8_few_kernel(const Args a)
 // another up to 833 (at 1.6 GHz: the power limit); a library's product of bf16
 // matrices of these sizes takes 640, of f16 677.  16 x 16 fragments staged
 // through registers, 256 x 192 tiles: 910; 64 x 96 a wave: 919.
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
-// A chunk's 16 codes: two instructions' values.
-__device__ __forceinline__ void widen_chunk(u32x4 c, bf16x8 &lo, bf16x8 &hi)
-{
-    u32x4 h[2];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        h[i >> 1][2 * (i & 1)] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], 1.0f, false));
-        h[i >> 1][2 * (i & 1) + 1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(c[i], 1.0f, true));
-    }
-    lo = __builtin_bit_cast(bf16x8, h[0]);
-    hi = __builtin_bit_cast(bf16x8, h[1]);
-}
-
-// Keeps what forms x here: without it the compiler moves products, conversions
-// and additions to their results' first use, with all their operands held.
-template <class T> __device__ __forceinline__ void pin(T &x) { asm volatile("" : "+v"(x)); }
-
 constexpr int kF8WideRows = 256;
 constexpr int kF8WideCF = 2;         // 32-vector fragments per wave
 constexpr int kF8WideVecs = 64 * kF8WideCF;
@@ -645,7 +659,6 @@ __device__ __forceinline__ void f8_wide_tile(const Args &a, uint8_t *lds, int ro
     constexpr int BR = kF8WideRows, BC = kF8WideVecs;   // tile: rows, vectors
     constexpr int AB = BR * 128, XB = BC * 128;             // bytes of a block's codes
     constexpr int PA = BR / 8 / NW, PX = BC / 8 / NW;       // staged pieces (8 rows x 128 bytes) a wave
-    typedef __attribute__((address_space(3))) void lds_t;
     uint8_t *const lx = lds + 2 * AB;                       // [2][XB], behind [2][AB]
     float *const ls = (float *)(lds + 2 * (AB + XB));       // [2][BC]
 
@@ -718,9 +731,6 @@ __device__ __forceinline__ void f8_wide_tile(const Args &a, uint8_t *lds, int ro
     float sc = 0.0f, sp = 0.0f;                             // the scales that the sums of this and the last group take
     u32x4 nb[2], na[2];                                     // chunks on their way: columns, rows
 
-    auto mfma = [](const bf16x8 &x, const bf16x8 &y, const f32x16 &z) {
-        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(x, y, z, 0, 0, 0);
-    };
     auto scale = [&](float (&to)[16], const f32x16 &from, float by, int i0, int i1) {
 #pragma unroll
         for (int i = i0; i < i1; ++i) {
@@ -734,8 +744,6 @@ __device__ __forceinline__ void f8_wide_tile(const Args &a, uint8_t *lds, int ro
         pin(hi);
     };
     const f32x16 zero = {};
-    // the sums to add after a pass's product k: from the third on, when the pass before has its last ones
-    auto from_k = [](int k) { return k < 2 ? 0 : k == 8 ? 16 : 3 * k - 6; };
 
     // Pass (g, 0) multiplies rows 0 .. 31 and adds the sums of the pass before;
     // pass (g, 1) rows 32 .. 63, and widens the next group's columns.
@@ -757,7 +765,7 @@ __device__ __forceinline__ void f8_wide_tile(const Args &a, uint8_t *lds, int ro
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                sum[0] = mfma(W[0][k], B[k], k ? sum[0] : zero);
+                sum[0] = mfma32(W[0][k], B[k], k ? sum[0] : zero);
                 pin(sum[0]);
                 if constexpr (g > 0) scale(acc[1][g - 1], sum[1], sp, from_k(k), from_k(k + 1));
                 if constexpr (g == 0 && !first) scale(acc[1][CF - 1], sum[1], sp, from_k(k), from_k(k + 1));
@@ -780,7 +788,7 @@ __device__ __forceinline__ void f8_wide_tile(const Args &a, uint8_t *lds, int ro
             }
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                sum[1] = mfma(W[1][k], B[k], k ? sum[1] : zero);
+                sum[1] = mfma32(W[1][k], B[k], k ? sum[1] : zero);
                 pin(sum[1]);
                 scale(acc[0][g], sum[0], sc, from_k(k), from_k(k + 1));
                 if (k & 1) {
@@ -866,11 +874,11 @@ const void *const kTableF8Few[3] = {
     (const void *)&qmv_f8_few_kernel<2>,
 };
 
-// [plain, gate/up]
-extern const void *const kTableF8Tile[2];
-const void *const kTableF8Tile[2] = {
-    (const void *)&qmv_f8_tile_kernel<0>,
-    (const void *)&qmv_f8_tile_kernel<1>,
+// [whole K, halves][plain, gate/up]
+extern const void *const kTableF8Tile[2][2];
+const void *const kTableF8Tile[2][2] = {
+    {(const void *)&qmv_f8_tile_kernel<0, 1>, (const void *)&qmv_f8_tile_kernel<1, 1>},
+    {(const void *)&qmv_f8_tile_kernel<0, 2>, (const void *)&qmv_f8_tile_kernel<1, 2>},
 };
 
 }  // namespace qmv
