@@ -19,6 +19,7 @@ stream (or ``stream``).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -32,8 +33,11 @@ __all__ = ["qmt_quantize_weights", "qmt_dequantize_weights", "qmt_qk_norm_rope",
 QMT_LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libqmt.so")
 
 _STYLE = {"half": 0, "pairs": 1}
+_F = torch.float32
+_F32, _I32 = (torch.float32,), (torch.int32,)
 
 _lib = None
+_fn = {}                    # the library's entries by name
 
 
 def qmt_lib():
@@ -52,6 +56,7 @@ def qmt_lib():
                        ("qmt_logprobs", [I, P, I, I, P, I, P, P, P, P, P, P])):
         f = getattr(L, name)
         f.restype, f.argtypes = I, args
+        _fn[name] = f
     L.qmt_logprobs_workspace.restype, L.qmt_logprobs_workspace.argtypes = ctypes.c_longlong, [I, I, I]
     L.qmt_strerror.restype, L.qmt_strerror.argtypes = ctypes.c_char_p, [I]
     _lib = L
@@ -64,7 +69,9 @@ def qmt_strerror(status: int) -> str:
 
 def _run(entry, device, stream, *args):
     """Call a library entry on the tensors' GPU and stream."""
-    status = _q._on_device(getattr(_lib or qmt_lib(), entry), device, stream, *args)
+    if _lib is None:
+        qmt_lib()
+    status = _q._on_device(_fn[entry], device, stream, *args)
     if status != 0:
         raise _q.QmvError(status, qmt_strerror(status))
 
@@ -117,6 +124,33 @@ def qmt_dequantize_weights(codes, scales, dtype=torch.bfloat16, y=None, stream=N
     return y
 
 
+# Sizes and options of the two small calls: checked once for each set of them,
+# the tensors themselves each time (a call of one token is over in less time
+# than its checks take).
+
+@functools.lru_cache(maxsize=256)
+def _qk_plan(x_shape, table_shape, heads, kv_heads, head_dim, style, dtype):
+    """(M, row, H, Hk, D, P, R, rotation, ytype; shape and strides of q, of k)"""
+    rotation = _choice(style, _STYLE, "style")
+    if dtype not in _TYPE:
+        raise ValueError(f"dtype is {dtype}, expected one of {tuple(_TYPE)}")
+    H, Hk, D = int(heads), int(kv_heads), int(head_dim)
+    if len(x_shape) != 2 or 0 in x_shape:
+        raise ValueError(f"x has shape {tuple(x_shape)}, expected [M][row]")
+    M, row = x_shape
+    if H < 1 or Hk < 0 or D < 8 or D % 8 or D > 512:
+        raise ValueError(f"{H} heads and {Hk} key heads of {D}: expected at least 1, at least 0, and a multiple of 8 "
+                         "up to 512")
+    if row < (H + Hk) * D or row % 4:
+        raise ValueError(f"x has rows of {row} values, expected at least {(H + Hk) * D} and a multiple of 4")
+    if len(table_shape) != 2 or 0 in table_shape or table_shape[1] % 8 or table_shape[1] > D:
+        raise ValueError(f"table has shape {tuple(table_shape)}, expected [P][R] with R % 8 == 0 and 8 <= R <= {D}")
+    P, R = table_shape
+    _q._ints(M, row, P)
+    return (M, row, H, Hk, D, P, R, rotation, _TYPE[dtype],
+            ((M, H, D), (H * D, D, 1)), ((M, Hk, D), (Hk * D, D, 1)))
+
+
 def qmt_qk_norm_rope(x, heads, kv_heads, head_dim, table, positions, q_weight=None, k_weight=None, eps=1e-5,
                      style="half", dtype=torch.bfloat16, q=None, k=None, stream=None):
     """Root-mean-square norm of each query and key head and the rotation by
@@ -129,41 +163,42 @@ def qmt_qk_norm_rope(x, heads, kv_heads, head_dim, table, positions, q_weight=No
     [0, P) gives zeros; ``q_weight`` and ``k_weight`` [D], of one type.
     ``style`` "half" rotates values i and i + R / 2, "pairs" values 2 i and 2 i
     + 1."""
-    rotation = _choice(style, _STYLE, "style")
-    if dtype not in _TYPE:
-        raise ValueError(f"dtype is {dtype}, expected one of {tuple(_TYPE)}")
     _tensor(x, "x", _TYPE)
-    H, Hk, D = int(heads), int(kv_heads), int(head_dim)
-    if x.dim() != 2 or x.numel() < 1:
-        raise ValueError(f"x has shape {tuple(x.shape)}, expected [M][row]")
-    M, row = x.shape
-    if H < 1 or Hk < 0 or D < 8 or D % 8 or D > 512:
-        raise ValueError(f"{H} heads and {Hk} key heads of {D}: expected at least 1, at least 0, and a multiple of 8 "
-                         "up to 512")
-    if row < (H + Hk) * D or row % 4:
-        raise ValueError(f"x has rows of {row} values, expected at least {(H + Hk) * D} and a multiple of 4")
     dev = x.device
-    _tensor(table, "table", (torch.float32,), dev)
-    if table.dim() != 2 or table.numel() < 1 or table.shape[1] % 8 or table.shape[1] > D:
-        raise ValueError(f"table has shape {tuple(table.shape)}, expected [P][R] with R % 8 == 0 and 8 <= R <= {D}")
-    P, R = table.shape
-    _q._ints(M, row, P)
-    _tensor(positions, "positions", (torch.int32,), dev, (M,))
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _tensor(w, name, _TYPE, dev, (D,))
+    _tensor(table, "table", _F32, dev)
+    M, row, H, Hk, D, P, R, rotation, ytype, qs, ks = _qk_plan(x.shape, table.shape, heads, kv_heads, head_dim, style,
+                                                               dtype)
+    _tensor(positions, "positions", _I32, dev, (M,))
+    if q_weight is not None:
+        _tensor(q_weight, "q_weight", _TYPE, dev, (D,))
+    if k_weight is not None:
+        _tensor(k_weight, "k_weight", _TYPE, dev, (D,))
     if q_weight is not None and k_weight is not None and q_weight.dtype != k_weight.dtype:
         raise TypeError(f"q_weight has dtype {q_weight.dtype}, k_weight {k_weight.dtype}; expected one type")
     if k is not None and Hk == 0:
         raise ValueError("k needs key heads")
     _gpu(x, "qmt_qk_norm_rope")
-    q = _out(q, "q", (dtype, (M, H, D)), dev)
-    k = _out(k, "k", (dtype, (M, Hk, D)), dev) if Hk else None
+    q = torch.empty_strided(*qs, dtype=dtype, device=dev) if q is None else _out(q, "q", (dtype, qs[0]), dev)
+    if Hk:
+        k = torch.empty_strided(*ks, dtype=dtype, device=dev) if k is None else _out(k, "k", (dtype, ks[0]), dev)
     w = q_weight if q_weight is not None else k_weight
     _run("qmt_qk_norm_rope", dev, stream, _TYPE[x.dtype], x.data_ptr(), row, H, Hk, D, table.data_ptr(), P, R,
          positions.data_ptr(), 0 if w is None else _TYPE[w.dtype], _ptr(q_weight), _ptr(k_weight), eps, rotation,
-         _TYPE[dtype], q.data_ptr(), _ptr(k), M)
+         ytype, q.data_ptr(), _ptr(k), M)
     return q, k
+
+
+@functools.lru_cache(maxsize=256)
+def _logprobs_plan(shape, top_k):
+    """(M, V, top_k, bytes of the workspace)"""
+    if len(shape) != 2 or 0 in shape:
+        raise ValueError(f"logits has shape {tuple(shape)}, expected [M][V]")
+    M, V = shape
+    _q._ints(M, V)
+    top_k = int(top_k)
+    if not 0 <= top_k <= 32:
+        raise ValueError(f"top_k is {top_k}, expected 0 to 32")
+    return M, V, top_k, qmt_lib().qmt_logprobs_workspace(M, V, top_k)
 
 
 def qmt_logprobs(logits, tokens=None, top_k=0, logprobs=None, entropy=None, top_ids=None, top_logprobs=None,
@@ -179,16 +214,10 @@ def qmt_logprobs(logits, tokens=None, top_k=0, logprobs=None, entropy=None, top_
     least qmt_lib().qmt_logprobs_workspace(M, V, top_k) bytes, is taken from
     torch where it is not given."""
     _tensor(logits, "logits", _TYPE)
-    if logits.dim() != 2 or logits.numel() < 1:
-        raise ValueError(f"logits has shape {tuple(logits.shape)}, expected [M][V]")
-    M, V = logits.shape
-    _q._ints(M, V)
-    top_k = int(top_k)
-    if not 0 <= top_k <= 32:
-        raise ValueError(f"top_k is {top_k}, expected 0 to 32")
+    M, V, top_k, need = _logprobs_plan(logits.shape, top_k)
     dev = logits.device
     if tokens is not None:
-        _tensor(tokens, "tokens", (torch.int32,), dev, (M,))
+        _tensor(tokens, "tokens", _I32, dev, (M,))
     elif logprobs is not None:
         raise ValueError("logprobs needs tokens")
     if top_k == 0 and (top_ids is not None or top_logprobs is not None):
@@ -197,19 +226,22 @@ def qmt_logprobs(logits, tokens=None, top_k=0, logprobs=None, entropy=None, top_
         _tensor(workspace, "workspace", (torch.uint8,), dev)
     _gpu(logits, "qmt_logprobs")
     if tokens is not None:
-        logprobs = _out(logprobs, "logprobs", (torch.float32, (M,)), dev)
-    entropy = _out(entropy, "entropy", (torch.float32, (M,)), dev)
+        logprobs = torch.empty_strided((M,), (1,), dtype=_F, device=dev) if logprobs is None else \
+            _out(logprobs, "logprobs", (_F, (M,)), dev)
+    entropy = torch.empty_strided((M,), (1,), dtype=_F, device=dev) if entropy is None else \
+        _out(entropy, "entropy", (_F, (M,)), dev)
     if top_k:
-        top_ids = _out(top_ids, "top_ids", (torch.int32, (M, top_k)), dev)
-        top_logprobs = _out(top_logprobs, "top_logprobs", (torch.float32, (M, top_k)), dev)
-    need = (_lib or qmt_lib()).qmt_logprobs_workspace(M, V, top_k)
+        top_ids = torch.empty_strided((M, top_k), (top_k, 1), dtype=torch.int32, device=dev) if top_ids is None else \
+            _out(top_ids, "top_ids", (torch.int32, (M, top_k)), dev)
+        top_logprobs = torch.empty_strided((M, top_k), (top_k, 1), dtype=_F, device=dev) if top_logprobs is None else \
+            _out(top_logprobs, "top_logprobs", (_F, (M, top_k)), dev)
     if workspace is not None:
         if workspace.numel() < need:
             raise ValueError(f"workspace has {workspace.numel()} bytes, expected at least {need}")
     elif need:
         # (given back to the stream that used it, not to the one that is current here)
         if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace = torch.empty_strided((need,), (1,), dtype=torch.uint8, device=dev)
         else:
             with torch.cuda.stream(stream):
                 workspace = torch.empty(need, dtype=torch.uint8, device=dev)

@@ -63,8 +63,15 @@ def qmx_strerror(status: int) -> str:
     return qmx_lib().qmx_strerror(int(status)).decode()
 
 
+_Tensor = torch.Tensor
+
+
 def _tensor(t, name, dtypes, device=None, shape=None):
     """``t`` is a contiguous tensor of one of ``dtypes`` (on ``device``, of ``shape``)."""
+    # (one test for the calls that are right)
+    if type(t) is _Tensor and t.dtype in dtypes and t.is_contiguous() and (shape is None or t.shape == shape) and \
+            (device is None or t.device == device):
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in dtypes:
