@@ -14,7 +14,13 @@ using namespace qmt_host;
 
 // ----------------------------------------------------------- square blocks
 // One workgroup takes a block of 128 x 128: 16 lanes a row, 16 rows at a time,
-// the whole block in registers between the maximum and the codes.
+// the whole block in registers between the maximum and the codes.  (A kernel for
+// each type: 16-bit values take half the registers, and twice the waves are
+// there to wait for memory.)  32 matrices of 2880 x 2880 from bf16 (797 MB) 183
+// us, 4.4 TB/s, and back 145, 5.5 TB/s; with one kernel for all types, a
+// maximum in fp32 and 64-bit quotients of all values below the normal range 257.
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
 struct SquareBlock {
     long long at;        // of the thread's first value
     int k, row, N, K;    // its column and row in the matrix
@@ -33,7 +39,8 @@ struct SquareBlock {
     __device__ __forceinline__ size_t index(int p) const { return (size_t)(at + (long long)(16 * p) * K); }
 };
 
-__global__ __launch_bounds__(256) void qmt_quantize_weights_kernel(const void *x, int xt, void *codes, float *scales,
+template <int XT>
+__global__ __launch_bounds__(256) void qmt_quantize_weights_kernel(const void *x, void *codes, float *scales,
                                                                    long long blocks, int N, int K)
 {
     __shared__ uint32_t part[2][16];
@@ -44,15 +51,27 @@ __global__ __launch_bounds__(256) void qmt_quantize_weights_kernel(const void *x
 #pragma unroll
         for (int p = 0; p < 8; ++p) {
             r[p].a = r[p].b = make_uint4(0, 0, 0, 0);
-            if (s.has(p)) r[p] = load_raw8(x, s.index(p), xt);
+            if (s.has(p)) r[p] = load_raw8(x, s.index(p), XT);
         }
         uint32_t m = 0;
+        if constexpr (XT == QMX_T_F32) {
 #pragma unroll
-        for (int p = 0; p < 8; ++p) {
-            float v[8];
-            raw_to_f32(r[p], xt, v);
-            const uint32_t o = amax_bits8(v);
-            m = m > o ? m : o;
+            for (int p = 0; p < 8; ++p) {
+                float v[8];
+                raw_to_f32(r[p], XT, v);
+                const uint32_t o = amax_bits8(v);
+                m = m > o ? m : o;
+            }
+        } else {
+            // of the 16-bit patterns, two at a time
+            u16x2 h = {0, 0};
+#pragma unroll
+            for (int p = 0; p < 8; ++p)
+#pragma unroll
+                for (const uint32_t w : {r[p].a.x, r[p].a.y, r[p].a.z, r[p].a.w})
+                    h = __builtin_elementwise_max(h, __builtin_bit_cast(u16x2, w & 0x7FFF7FFFu));
+            const uint16_t o = h[0] > h[1] ? h[0] : h[1];
+            m = __float_as_uint(XT == QMX_T_BF16 ? __uint_as_float((uint32_t)o << 16) : (float)__builtin_bit_cast(_Float16, o));
         }
         m = row16_max(m);
         if ((threadIdx.x & 15) == 0) part[turn][threadIdx.x >> 4] = m;
@@ -65,7 +84,7 @@ __global__ __launch_bounds__(256) void qmt_quantize_weights_kernel(const void *x
         for (int p = 0; p < 8; ++p)
             if (s.has(p)) {
                 float v[8];
-                raw_to_f32(r[p], xt, v);
+                raw_to_f32(r[p], XT, v);
                 *(uint2 *)((uint8_t *)codes + s.index(p)) = f8_codes(v, d);
             }
     }
@@ -91,6 +110,34 @@ __global__ __launch_bounds__(256) void qmt_dequantize_weights_kernel(const void 
                 store8(y, s.index(p), yt, v);
             }
     }
+}
+
+// ------------------------------------------------------ values of other lanes
+// The value of lane ^ J, by the vector ALUs (a sort of 64 by way of LDS took
+// three times as long).
+template <int J> __device__ __forceinline__ uint32_t lane_xor(uint32_t v)
+{
+    if constexpr (J == 1) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true);     // quad_perm
+    if constexpr (J == 2) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true);
+    if constexpr (J == 4)                                     // a half row mirrored (^ 7), a quad mirrored (^ 3)
+        return (uint32_t)__builtin_amdgcn_mov_dpp(__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true), 0x1B, 0xF, 0xF, true);
+    if constexpr (J == 8) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x128, 0xF, 0xF, true);    // row_ror
+    if constexpr (J == 16) {
+        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+        return threadIdx.x & 16 ? r[0] : r[1];
+    }
+    if constexpr (J == 32) {
+        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+        return threadIdx.x & 32 ? r[0] : r[1];
+    }
+}
+template <int J> __device__ __forceinline__ uint64_t lane_xor(uint64_t v)
+{
+    return (uint64_t)lane_xor<J>((uint32_t)(v >> 32)) << 32 | lane_xor<J>((uint32_t)v);
+}
+template <int J> __device__ __forceinline__ double lane_xor(double v)
+{
+    return __builtin_bit_cast(double, lane_xor<J>(__builtin_bit_cast(uint64_t, v)));
 }
 
 // ------------------------------------------------- norm and rotation of heads
@@ -126,6 +173,16 @@ __device__ __forceinline__ void store4(void *base, size_t i, int type, const flo
         *(uint2 *)((uint16_t *)base + i) = make_uint2(pack_f16(v[0], v[1]), pack_f16(v[2], v[3]));
 }
 
+// 1 / sqrt(m) to 2^-45 of itself: the instruction's 2^-23 or better, and one step of
+// Newton's method.  (A square root and a division in 64 bits took as many
+// instructions as all the rest of a head.)  0 and infinity have no step.
+__device__ __forceinline__ double inverse_root(double m)
+{
+    const double r = __builtin_amdgcn_rsq(m);
+    const double e = __builtin_fma(-m * r, r, 1.0);
+    return r > 0.0 && r < __builtin_inf() ? __builtin_fma(0.5 * r, e, r) : r;
+}
+
 struct QkArgs {
     const void *x, *qw, *kw;
     const float *table;
@@ -135,6 +192,7 @@ struct QkArgs {
     int xt, wt, yt, row, heads, all_heads, D, P, R, pairs, M;
     int per_token;       // groups of lanes a token takes
     long long group0;
+    double inv_d;        // 1 / D
 };
 
 // G lanes take a head, lane j of them its values a = A .. A + 3 and b = B ..
@@ -142,24 +200,36 @@ struct QkArgs {
 // in a and in b (QMT_PAIRS): no value crosses lanes.  A group takes UN heads of
 // its token, all their loads given out at once; the lane's cosines, sines and
 // weights serve them all.
-template <int G, int UN>
+//
+// 8192 tokens of 40 heads of 128, bf16 (168 MB): 40 us, 4.2 TB/s; of that a SIMD
+// issues 13400 vector instructions, 34 of a head's 130 in 64 bits, and is never
+// without one.  A square root and a division in 64 bits, sums by way of LDS, and
+// types looked up at every load 52.  (XT, YT, PAIRS: the types and the rotation,
+// or -1 for those of the arguments, which serve calls of few heads: a launch's
+// time whatever they do.)
+template <int G, int UN, int XT, int YT, int PAIRS>
 __global__ __launch_bounds__(256) void qmt_qk_norm_rope_kernel(const QkArgs a)
 {
+    const int xt = XT < 0 ? a.xt : XT, yt = YT < 0 ? a.yt : YT;
+    const bool pairs = PAIRS < 0 ? a.pairs != 0 : PAIRS != 0;
     const int j = threadIdx.x & (G - 1);
     const long long g = a.group0 + (long long)blockIdx.x * (256 / G) + threadIdx.x / G;
     const unsigned t = (unsigned)g / (unsigned)a.per_token, h0 = (unsigned)g - t * (unsigned)a.per_token;
     if (t >= (unsigned)a.M) return;                            // whole groups
-    const bool mine = 8 * j < a.D, turned = 8 * j < a.R, halves = turned && !a.pairs;
+    const bool mine = 8 * j < a.D, turned = 8 * j < a.R, halves = turned && !pairs;
     const int A = halves ? 4 * j : 8 * j, B = halves ? A + a.R / 2 : A + 4;
+    const int xs = xt == QMX_T_F32 ? 4 : 2, ys = yt == QMX_T_F32 ? 4 : 2;
+    const uint8_t *const xr = (const uint8_t *)a.x + (size_t)t * a.row * xs;
+    uint8_t *const qr = (uint8_t *)a.q + (size_t)t * (a.heads * a.D) * ys;
+    uint8_t *const kr = (uint8_t *)a.k + (size_t)t * ((a.all_heads - a.heads) * a.D) * ys;
     uint4 xa[UN], xb[UN];
 #pragma unroll
     for (int u = 0; u < UN; ++u) {
         const int h = h0 + u * a.per_token;
         xa[u] = xb[u] = make_uint4(0, 0, 0, 0);
         if (mine && h < a.all_heads) {
-            const size_t at = (size_t)t * a.row + (size_t)h * a.D;
-            xa[u] = load_raw4(a.x, at + A, a.xt);
-            xb[u] = load_raw4(a.x, at + B, a.xt);
+            xa[u] = load_raw4(xr, (unsigned)(h * a.D + A), xt);
+            xb[u] = load_raw4(xr, (unsigned)(h * a.D + B), xt);
         }
     }
     const int p = a.positions[t];
@@ -187,29 +257,33 @@ __global__ __launch_bounds__(256) void qmt_qk_norm_rope_kernel(const QkArgs a)
         const int h = h0 + u * a.per_token;
         if (h >= a.all_heads) break;                           // whole groups
         float va[4], vb[4];
-        raw4_to_f32(xa[u], a.xt, va);
-        raw4_to_f32(xb[u], a.xt, vb);
+        raw4_to_f32(xa[u], xt, va);
+        raw4_to_f32(xb[u], xt, vb);
         double s = 0.0;
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
             s = __builtin_fma((double)va[n], (double)va[n], s);
             s = __builtin_fma((double)vb[n], (double)vb[n], s);
         }
-#pragma unroll
-        for (int d = G / 2; d >= 1; d >>= 1) s += __shfl_xor(s, d);
-        const double r = 1.0 / __builtin_sqrt(s / (double)a.D + (double)a.eps);
+        s += lane_xor<1>(s);
+        s += lane_xor<2>(s);
+        if constexpr (G > 4) s += lane_xor<4>(s);
+        if constexpr (G > 8) s += lane_xor<8>(s);
+        if constexpr (G > 16) s += lane_xor<16>(s);
+        if constexpr (G > 32) s += lane_xor<32>(s);
+        const double r = inverse_root(__builtin_fma(s, a.inv_d, (double)a.eps));
         const bool key = h >= a.heads;
 #pragma unroll
         for (int n = 0; n < 4; ++n) {
-            va[n] = (float)((double)va[n] * r * (double)(key ? w[1][0][n] : w[0][0][n]));
-            vb[n] = (float)((double)vb[n] * r * (double)(key ? w[1][1][n] : w[0][1][n]));
+            va[n] = (float)((double)va[n] * r) * (key ? w[1][0][n] : w[0][0][n]);
+            vb[n] = (float)((double)vb[n] * r) * (key ? w[1][1][n] : w[0][1][n]);
         }
         auto turn = [&](float &x, float &y, int i) {
             const float u0 = __builtin_fmaf(x, cs[i], -(y * sn[i])), v0 = __builtin_fmaf(y, cs[i], x * sn[i]);
             x = u0, y = v0;
         };
         if (turned) {
-            if (a.pairs) {
+            if (pairs) {
                 turn(va[0], va[1], 0), turn(va[2], va[3], 1);
                 turn(vb[0], vb[1], 2), turn(vb[2], vb[3], 3);
             } else {
@@ -222,24 +296,43 @@ __global__ __launch_bounds__(256) void qmt_qk_norm_rope_kernel(const QkArgs a)
             for (int n = 0; n < 4; ++n) va[n] = vb[n] = 0.0f;
         }
         if (mine) {
-            void *const base = key ? a.k : a.q;
-            const int H = key ? a.all_heads - a.heads : a.heads;
-            const size_t at = ((size_t)t * H + (key ? h - a.heads : h)) * a.D;
-            store4(base, at + A, a.yt, va);
-            store4(base, at + B, a.yt, vb);
+            const unsigned at = (unsigned)((key ? h - a.heads : h) * a.D);
+            store4(key ? kr : qr, at + A, yt, va);
+            store4(key ? kr : qr, at + B, yt, vb);
         }
     }
 }
 
-template <int UN>
-const void *qk_kernel(int D, int &G)
+// A head each of any types, or 4 of these.
+template <int G, int XT, int YT>
+const void *qk_kernel4(bool pairs)
 {
-    if (D <= 32) { G = 4; return (const void *)&qmt_qk_norm_rope_kernel<4, UN>; }
-    if (D <= 64) { G = 8; return (const void *)&qmt_qk_norm_rope_kernel<8, UN>; }
-    if (D <= 128) { G = 16; return (const void *)&qmt_qk_norm_rope_kernel<16, UN>; }
-    if (D <= 256) { G = 32; return (const void *)&qmt_qk_norm_rope_kernel<32, UN>; }
-    G = 64;
-    return (const void *)&qmt_qk_norm_rope_kernel<64, UN>;
+    return pairs ? (const void *)&qmt_qk_norm_rope_kernel<G, 4, XT, YT, 1>
+                 : (const void *)&qmt_qk_norm_rope_kernel<G, 4, XT, YT, 0>;
+}
+template <int G, int XT>
+const void *qk_kernel4(int yt, bool pairs)
+{
+    return yt == QMX_T_F32    ? qk_kernel4<G, XT, QMX_T_F32>(pairs)
+           : yt == QMX_T_BF16 ? qk_kernel4<G, XT, QMX_T_BF16>(pairs)
+                              : qk_kernel4<G, XT, QMX_T_F16>(pairs);
+}
+template <int G>
+const void *qk_kernel(bool many, int xt, int yt, bool pairs)
+{
+    if (!many) return (const void *)&qmt_qk_norm_rope_kernel<G, 1, -1, -1, -1>;
+    return xt == QMX_T_F32    ? qk_kernel4<G, QMX_T_F32>(yt, pairs)
+           : xt == QMX_T_BF16 ? qk_kernel4<G, QMX_T_BF16>(yt, pairs)
+                              : qk_kernel4<G, QMX_T_F16>(yt, pairs);
+}
+const void *qk_kernel(int D, bool many, int xt, int yt, bool pairs, int &G)
+{
+    G = D <= 32 ? 4 : D <= 64 ? 8 : D <= 128 ? 16 : D <= 256 ? 32 : 64;
+    return G == 4    ? qk_kernel<4>(many, xt, yt, pairs)
+           : G == 8  ? qk_kernel<8>(many, xt, yt, pairs)
+           : G == 16 ? qk_kernel<16>(many, xt, yt, pairs)
+           : G == 32 ? qk_kernel<32>(many, xt, yt, pairs)
+                     : qk_kernel<64>(many, xt, yt, pairs);
 }
 
 // ------------------------------------------------------- log probabilities
@@ -263,33 +356,6 @@ __device__ __forceinline__ float below(uint32_t k) { return order_value(k - (k =
 __device__ __forceinline__ uint64_t entry(float l, int index)
 {
     return (uint64_t)order_bits(l) << 32 | (uint32_t)~index;
-}
-
-// The value of lane ^ J, by the vector ALUs (a sort of 64 by way of LDS took
-// three times as long).
-template <int J> __device__ __forceinline__ uint32_t lane_xor(uint32_t v)
-{
-    if constexpr (J == 1) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0xB1, 0xF, 0xF, true);     // quad_perm
-    if constexpr (J == 2) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x4E, 0xF, 0xF, true);
-    if constexpr (J == 4)                                     // a half row mirrored (^ 7), a quad mirrored (^ 3)
-        return (uint32_t)__builtin_amdgcn_mov_dpp(__builtin_amdgcn_mov_dpp((int)v, 0x141, 0xF, 0xF, true), 0x1B, 0xF, 0xF, true);
-    if constexpr (J == 8) return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, 0x128, 0xF, 0xF, true);    // row_ror
-    if constexpr (J == 16) {
-        const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
-        return threadIdx.x & 16 ? r[0] : r[1];
-    }
-    if constexpr (J == 32) {
-        const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
-        return threadIdx.x & 32 ? r[0] : r[1];
-    }
-}
-template <int J> __device__ __forceinline__ uint64_t lane_xor(uint64_t v)
-{
-    return (uint64_t)lane_xor<J>((uint32_t)(v >> 32)) << 32 | lane_xor<J>((uint32_t)v);
-}
-template <int J> __device__ __forceinline__ double lane_xor(double v)
-{
-    return __builtin_bit_cast(double, lane_xor<J>(__builtin_bit_cast(uint64_t, v)));
 }
 
 template <class T> __device__ __forceinline__ T larger(T a, T b) { return a > b ? a : b; }
@@ -900,9 +966,11 @@ QMT_API qmv_status_t qmt_quantize_weights(qmx_type_t xtype, const void *x, void 
     if (s != QMV_OK)
         return s;
     long long blocks = (long long)E * ((N + 127) / 128) * ((K + 127) / 128);
-    int xt = (int)xtype;
-    void *args[] = {&x, &xt, &codes, &scales, &blocks, &N, &K};
-    return go((const void *)&qmt_quantize_weights_kernel, square_groups(blocks), args, stream);
+    void *args[] = {&x, &codes, &scales, &blocks, &N, &K};
+    const void *const fn = xtype == QMX_T_F32 ? (const void *)&qmt_quantize_weights_kernel<QMX_T_F32>
+                           : xtype == QMX_T_BF16 ? (const void *)&qmt_quantize_weights_kernel<QMX_T_BF16>
+                                                 : (const void *)&qmt_quantize_weights_kernel<QMX_T_F16>;
+    return go(fn, square_groups(blocks), args, stream);
 }
 
 QMT_API qmv_status_t qmt_dequantize_weights(const void *codes, const float *scales, qmx_type_t ytype, void *y, int E,
@@ -928,10 +996,10 @@ QMT_API qmv_status_t qmt_qk_norm_rope(qmx_type_t xtype, const void *x, int row, 
         return s;
     const int all = heads + kv_heads;
     QkArgs a = {x, q_weight, k_weight, table, positions, q, k, eps, (int)xtype, (int)wtype, (int)ytype, row, heads, all,
-                D, P, R, rotation == QMT_PAIRS ? 1 : 0, M, all, 0};
+                D, P, R, rotation == QMT_PAIRS ? 1 : 0, M, all, 0, 1.0 / D};
     int G;
     const bool many = (long long)M * all >= 16384;
-    const void *fn = many ? qk_kernel<4>(D, G) : qk_kernel<1>(D, G);
+    const void *fn = qk_kernel(D, many, (int)xtype, (int)ytype, rotation == QMT_PAIRS, G);
     if (many) a.per_token = (all + 3) / 4;
     return go_all(fn, a, &QkArgs::group0, 256 / G, ((long long)M * a.per_token * G + 255) / 256, stream);
 }

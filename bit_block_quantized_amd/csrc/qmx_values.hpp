@@ -133,25 +133,39 @@ __device__ __forceinline__ float f8_scale(uint32_t amax)
 
 // Eight e4m3 codes of v / d, value j in byte j: the nearest of the exact
 // quotient, ties to even.  v times the reciprocal is off by at most 2^-22 of
-// itself, so only a product that lies next to a border between two codes (20
-// bits below e4m3's last one: all ones or a half, plus or minus 4), or is below
-// the normal range and has its border elsewhere, is formed again: in 64 bits,
-// cut to 32 with the last bit set where anything was cut, which the conversion
-// then rounds as it would the quotient.  (About one wave in 20 has such a
-// value; correctly rounded divisions for all of them bound the quantizer.)
+// itself, so only a product that lies next to a border between two codes is
+// formed again: in 64 bits, cut to 32 with the last bit set where anything was
+// cut, which the conversion then rounds as it would the quotient.  20 bits below
+// e4m3's last one a border is all ones or a half, plus or minus 4; below the
+// normal range, 2^-6, codes are as far apart as above it, so 2^-6 more has the same
+// bits there (off by another half at most).  About one wave in 200 has such a
+// value; correctly rounded divisions for all of them, or for the values below
+// the normal range (one wave in 15), bound the quantizers.
 __device__ __forceinline__ uint2 f8_codes(const float (&v)[8], float d)
 {
     if (!(d < __builtin_inff())) return make_uint2(0, 0);
     const float r = 1.0f / d;
-    float t[8];
-    bool near = false;
+    float t[8], low = __builtin_inff();
+    uint32_t border = ~0u;                                    // the smallest distance to a border, plus 4, << 12
+    auto test = [&](float f) {
+        const uint32_t o = (__float_as_uint(f) << 12) + ((0x80000u + 4u) << 12);
+        border = border < o ? border : o;
+    };
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         t[j] = v[j] * r;
-        const uint32_t b = __float_as_uint(t[j]) & 0x7FFFFFFFu;
-        near |= ((b + (0x80000u + 4u)) & 0xFFFFFu) <= 8u || b - 1u < 0x3C7FFFFFu;
+        test(t[j]);
+        low = __builtin_fminf(low, __builtin_fabsf(t[j]));
     }
-    if (near) {
+    if (low < 0x1p-6f) {
+        border = ~0u;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float m = __builtin_fabsf(t[j]);
+            test(m < 0x1p-6f ? m + 0x1p-6f : m);
+        }
+    }
+    if (border < 9u << 12) {
         const double d64 = (double)d;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -186,8 +200,8 @@ __device__ __forceinline__ void f8_values(uint2 c, float d, float (&v)[8])
     }
 }
 
-// The largest magnitude of eight values as its bit pattern (every NaN and
-// infinity is at or above 0x7F800000), and of the 16 lanes of a row, which
+// The largest magnitude of eight values as its bit pattern in fp32 (every NaN
+// and infinity is at or above 0x7F800000), and of the 16 lanes of a row, which
 // hold a block's 128.  All lanes of the row take part.
 __device__ __forceinline__ uint32_t amax_bits8(const float (&v)[8])
 {
