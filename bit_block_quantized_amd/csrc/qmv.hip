@@ -671,15 +671,7 @@ qmv_status_t launch_mx4(const void *codes, const void *scales, const void *codes
     // 28.7 and 28.1, 64 109 and 84; gate/up 8 25 and 27; 4096 -> 14336 of 8: 2
     // pairs 14.4 and 15.8).
     const long long row_tiles = (N + 15) / 16;
-    // The few kernel while the chip holds at least 2 in 5 of its workgroups at a time, by LDS and
-    // registers (us, few and after it the tile kernel: 7168 -> 7168: 8 vectors (0.9 of what the
-    // chip holds) 15 and 26, 24 (3.5) 47 and 27; 2880 -> 2880: 64 (1.4) 18 and 19, 128 (2.8) 27 and
-    // 20; 32 experts top 4, 2880 -> 2880: 2 tokens (1.4) 18 and 20, 3 (2.8) 25 and 23; gate/up: 2 (1.9)
-    // 30 and 33, 3 (2.8) 41 and 38; 256 top 8, 7168 -> 2048: 1 token (2) 26 and 35, gate/up 44
-    // and 50, 2 tokens (8) 67 and 49, gate/up 95 and 89).
-    const long long few_groups = gather ? pairs * row_tiles : (M + 15) / 16 * row_tiles;
-    const int by_regs = mode == 1 ? 3 : 5, by_lds = kLdsPerCU / few_lds(most);
-    const bool many = 2 * few_groups > 5ll * cu_count() * (by_lds < by_regs ? by_lds : by_regs);
+    const bool many = gather ? pairs * row_tiles * h > 7 * cu_count() : M > kMaxM && (M + 15) / 16 * row_tiles > 3 * cu_count();
     // (the tile kernel counts the pairs of up to 1023 experts)
     if (mode != 2 && (!gather || E <= kMaxEBatched) && (many || few_lds(most) > kLdsPerCU)) {
         const int rows = mode == 1 ? 64 : 128;
@@ -790,7 +782,15 @@ qmv_status_t launch_f8(const void *codes, const void *scales, const void *codes2
     auto few_lds = [&](int vectors) { return 64 + 4 * h * 2048 + vectors * (xp + sp) + h * sp; };
     int most = pairs < 16 ? pairs : 16;
     const long long row_tiles = (N + 15) / 16;
-    const bool many = gather ? pairs * row_tiles * h > 7 * cu_count() : M > kMaxM && (M + 15) / 16 * row_tiles > 3 * cu_count();
+    // The few kernel while the chip holds at least 2 in 5 of its workgroups at a time, by LDS and
+    // registers (us, few and after it the tile kernel: 7168 -> 7168: 8 vectors (0.9 of what the
+    // chip holds) 15 and 26, 24 (3.5) 47 and 27; 2880 -> 2880: 64 (1.4) 18 and 19, 128 (2.8) 27 and
+    // 20; 32 experts top 4, 2880 -> 2880: 2 tokens (1.4) 18 and 20, 3 (2.8) 25 and 23; gate/up: 2 (1.9)
+    // 30 and 33, 3 (2.8) 41 and 38; 256 top 8, 7168 -> 2048: 1 token (2) 26 and 35, gate/up 44
+    // and 50, 2 tokens (8) 67 and 49, gate/up 95 and 89).
+    const long long few_groups = gather ? pairs * row_tiles : (M + 15) / 16 * row_tiles;
+    const int by_regs = mode == 1 ? 3 : 5, by_lds = kLdsPerCU / few_lds(most);
+    const bool many = 2 * few_groups > 5ll * cu_count() * (by_lds < by_regs ? by_lds : by_regs);
     // (the tile kernel counts the pairs of up to 1023 experts)
     if (mode != 2 && (!gather || E <= kMaxEBatched) && (many || few_lds(most) > kLdsPerCU)) {
         const int rows = mode == 1 ? 64 : 128;

@@ -20,8 +20,10 @@ HALVES, HALVES_GU = "qmv_f8_tile_kernel<0, 2>", "qmv_f8_tile_kernel<1, 2>"
 WIDE = "qmv_f8_wide_kernel"
 
 # rows that end inside a wave's 32, a tile's 128, and on them
-DENSE = [(HALVES, 31, 16400, 160), (HALVES, 33, 9000, 32), (HALVES, 64, 8190, 288), (HALVES, 65, 7168, 416),
-         (HALVES, 96, 6500, 128), (HALVES, 97, 8193, 544), (HALVES, 256, 4100, 672),
+DENSE = [(FEW, 31, 16400, 160), (FEW, 33, 9000, 32), (FEW, 64, 8190, 288), (FEW, 65, 7168, 416),
+         (FEW, 96, 6500, 128), (HALVES, 97, 8193, 544), (HALVES, 256, 4100, 672),
+         (HALVES, 31, 30000, 160), (HALVES, 40, 32700, 32), (HALVES, 32, 32700, 64), (HALVES, 65, 14000, 416),
+         (HALVES, 96, 12000, 128), (HALVES, 64, 16390, 800), (HALVES, 40, 32700, 288), (HALVES, 180, 16300, 160),
          (TILE, 32, 33000, 160), (TILE, 64, 32897, 96), (TILE, 200, 11000, 32), (TILE, 97, 16513, 160),
          (TILE, 200, 11100, 288), (TILE, 256, 11000, 544),
          (WIDE, 97, 32800, 160), (WIDE, 129, 16500, 288), (WIDE, 1030, 3700, 96),
