@@ -16,11 +16,9 @@ using namespace qmt_host;
 // One workgroup takes a block of 128 x 128: 16 lanes a row, 16 rows at a time,
 // the whole block in registers between the maximum and the codes.  (A kernel for
 // each type: 16-bit values take half the registers, and twice the waves are
-// there to wait for memory.)  32 matrices of 2880 x 2880 from bf16 (797 MB) 183
-// us, 4.4 TB/s, and back 145, 5.5 TB/s; with one kernel for all types, a
+// there to wait for memory.)  32 matrices of 2880 x 2880 from bf16 (797 MB) 174
+// us, 4.6 TB/s, and back 145, 5.5 TB/s; with one kernel for all types, a
 // maximum in fp32 and 64-bit quotients of all values below the normal range 257.
-typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-
 struct SquareBlock {
     long long at;        // of the thread's first value
     int k, row, N, K;    // its column and row in the matrix
@@ -54,24 +52,10 @@ __global__ __launch_bounds__(256) void qmt_quantize_weights_kernel(const void *x
             if (s.has(p)) r[p] = load_raw8(x, s.index(p), XT);
         }
         uint32_t m = 0;
-        if constexpr (XT == QMX_T_F32) {
 #pragma unroll
-            for (int p = 0; p < 8; ++p) {
-                float v[8];
-                raw_to_f32(r[p], XT, v);
-                const uint32_t o = amax_bits8(v);
-                m = m > o ? m : o;
-            }
-        } else {
-            // of the 16-bit patterns, two at a time
-            u16x2 h = {0, 0};
-#pragma unroll
-            for (int p = 0; p < 8; ++p)
-#pragma unroll
-                for (const uint32_t w : {r[p].a.x, r[p].a.y, r[p].a.z, r[p].a.w})
-                    h = __builtin_elementwise_max(h, __builtin_bit_cast(u16x2, w & 0x7FFF7FFFu));
-            const uint16_t o = h[0] > h[1] ? h[0] : h[1];
-            m = __float_as_uint(XT == QMX_T_BF16 ? __uint_as_float((uint32_t)o << 16) : (float)__builtin_bit_cast(_Float16, o));
+        for (int p = 0; p < 8; ++p) {
+            const uint32_t o = amax_bits8<XT>(r[p]);
+            m = m > o ? m : o;
         }
         m = row16_max(m);
         if ((threadIdx.x & 15) == 0) part[turn][threadIdx.x >> 4] = m;
@@ -585,10 +569,11 @@ __device__ __forceinline__ void put_part(const LogArgs &a, long long place, cons
     if constexpr (TOP) ((uint64_t *)(a.work + (long long)a.M * a.parts * kListSums))[place * 64 + lane] = e;
 }
 
-// A short part of a row, a group of 8 for each lane of 4 waves: first the
+// A short part of a row, a group of 8 for each lane of 4 waves at most: first the
 // largest logit of the workgroup and a bound of its top entries -- of the waves'
 // 16 largest lanes the top_k-th: as many logits are at least that -- then the
 // sums and what is no smaller than the bound, hardly more than top_k entries.
+// (201088 logits, top 20, in 99 parts: 4.8 us, and 3.0 without a top.)
 template <int TYPE, bool TOP>
 __global__ __launch_bounds__(256) void qmt_logprobs_part_kernel(const LogArgs a)
 {
@@ -602,7 +587,10 @@ __global__ __launch_bounds__(256) void qmt_logprobs_part_kernel(const LogArgs a)
     const int row = (int)(place / a.parts), part = (int)(place - (long long)row * a.parts);
     const int tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const LogRow<TYPE> r(a, row);
-    const int g = part * (64 * NW) + tid;
+    // (as many for each part, and for each of its waves: with all of a part's few in one wave the bound
+    // would be that wave's 16 lanes only, or none)
+    const int per = (r.groups + a.parts - 1) / a.parts, each = (per + NW - 1) / NW;
+    const int g = lane < each && w * each + lane < per ? part * per + w * each + lane : r.groups;
     const Raw8 raw = r.load(g);
     // (the rest: with the last wave of the first part)
     int rest_at = 0;
@@ -692,7 +680,9 @@ __global__ __launch_bounds__(256) void qmt_logprobs_part_kernel(const LogArgs a)
 
 // A row, or a long part of one: 8 waves, `steps` groups of 8 logits a lane of
 // them, two always on their way; the rest of the row is one more step, the last,
-// of the first part's first wave.  2 steps at least.
+// of the first part's first wave.  2 steps at least.  1024 rows of 131071 bf16
+// logits, top 5 (268 MB): 76 us, 3.5 TB/s; the exponentials and their sums, not
+// memory, bound it.
 template <int TYPE, bool TOP>
 __global__ __launch_bounds__(512) void qmt_logprobs_kernel(const LogArgs a)
 {
@@ -819,15 +809,16 @@ __global__ __launch_bounds__(512) void qmt_logprobs_kernel(const LogArgs a)
 }
 
 // The parts of a row joined: one workgroup a row, all entries in registers.  The
-// top_k-th largest of the parts' maxima (of fewer parts, of a wave's lanes, the
-// largest such) bounds the row's top_k-th logit from below, and what is no
-// smaller is hardly more than top_k entries, which one wave sorts.
+// top_k-th largest of the parts' maxima (of fewer parts, of the waves' 8 largest
+// lanes, or of a wave's lanes) bounds the row's top_k-th logit from below, and
+// what is no smaller is hardly more than top_k entries, which one wave sorts: 5.0
+// us for 99 parts and top 20.  (With each wave's own bound only, 11.4.)
 template <bool TOP>
 __global__ __launch_bounds__(64 * kJoinWaves) void qmt_logprobs_join_kernel(const LogArgs a)
 {
     constexpr int NW = kJoinWaves, PER = kMaxParts / NW;       // lists a wave takes at most
     __shared__ uint64_t few[64], wait[TOP ? NW : 1][128];
-    __shared__ uint32_t bound[NW];
+    __shared__ uint32_t bound[NW], lanes[64];
     __shared__ int count;
     const int row = (int)(a.first + blockIdx.x), tid = threadIdx.x, lane = tid & 63, w = tid >> 6;
     const long long list0 = (long long)row * a.parts;
@@ -861,8 +852,10 @@ __global__ __launch_bounds__(64 * kJoinWaves) void qmt_logprobs_join_kernel(cons
         }
         big = wave_sort<true>(big);
         if (lane == a.top_k - 1) bound[w] = big;
+        if (lane < 64 / NW) lanes[64 / NW * w + lane] = big;
         __syncthreads();
         uint32_t tau = 1;                                      // (0 is no entry)
+        if (a.parts < a.top_k) tau = larger(tau, lane_value(wave_sort<true>(lanes[lane]), a.top_k - 1));
 #pragma unroll
         for (int i = 0; i < NW; ++i) tau = larger(tau, bound[i]);
 #pragma unroll
@@ -998,7 +991,8 @@ QMT_API qmv_status_t qmt_qk_norm_rope(qmx_type_t xtype, const void *x, int row, 
     QkArgs a = {x, q_weight, k_weight, table, positions, q, k, eps, (int)xtype, (int)wtype, (int)ytype, row, heads, all,
                 D, P, R, rotation == QMT_PAIRS ? 1 : 0, M, all, 0, 1.0 / D};
     int G;
-    const bool many = (long long)M * all >= 16384;
+    // (one head a group and four, us: 40 heads of 128, bf16: 512 tokens 6.0 and 6.3, 1024 10.4 and 8.9)
+    const bool many = (long long)M * all >= 32768;
     const void *fn = qk_kernel(D, many, (int)xtype, (int)ytype, rotation == QMT_PAIRS, G);
     if (many) a.per_token = (all + 3) / 4;
     return go_all(fn, a, &QkArgs::group0, 256 / G, ((long long)M * a.per_token * G + 255) / 256, stream);

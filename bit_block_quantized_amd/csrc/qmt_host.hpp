@@ -66,10 +66,14 @@ inline qmv_status_t check_logprobs(int ltype, const void *logits, int M, int V, 
 }
 
 // A row of V logits is cut into `parts` (at most kMaxParts), a workgroup of
-// `threads` each that takes `steps` times 8 logits a thread: one step where all
-// parts of the call find a place on the chip at a time (part).  Unless one
-// long part is the row (join), each part leaves its sums (kListSums bytes) and a
-// list of 64 entries for a second launch, a workgroup a row.
+// `threads` each that takes `steps` times 8 logits a thread: one step where the
+// call has no more than kMaxShort parts (part).  Unless one long part is the row
+// (join), each part leaves its sums (kListSums bytes) and a list of 64 entries for
+// a second launch, a workgroup a row.  (Top 20, us in short parts and in long
+// ones: 201088 fp32 logits: 1 row 10 and 18, 16 16 and 20, 32 (3168 parts) 21 and
+// 23, 64 30 and 27; 131071 bf16: 1 10 and 13, 32 (2048) 16 and 19, 64 (4096) 23 and
+// 23, 128 36 and 28; 32000 fp32: 1 10 and 13, 128 (2048) 17 and 20.)
+constexpr int kMaxShort = 4096;
 constexpr int kMaxParts = 128, kJoinWaves = 8, kListSums = 32;
 struct LogprobPlan {
     int parts, threads, steps;
@@ -81,7 +85,7 @@ inline LogprobPlan plan_logprobs(int M, int V)
     auto cut = [](int of, int n) { return n / of + (n % of != 0); };
     // (up to 14 logits before and behind whole groups of 8 go with the first part)
     const int shorts = cut(2048, V);
-    if (shorts <= kMaxParts && (long long)shorts * M <= 1024)
+    if (shorts <= kMaxParts && (long long)shorts * M <= kMaxShort)
         return {shorts, 256, 1, true, true};
     const int steps = cut(4096, V);
     int parts = 512 / M;                              // two for each of 256 CUs, as far as the row goes

@@ -124,27 +124,31 @@ __device__ __forceinline__ void store1(void *base, size_t i, int type, float v)
 }
 
 // ---------------------------------------------------------- blocks of 128
-// The scale of an e4m3 block from its largest magnitude's bits.
+// The scale of an e4m3 block from its largest magnitude's bits.  The quotient by
+// 448 is rounded as a division's: the product with the reciprocal's nearest is
+// off by a last place at most, its remainder is exact, and a constant's nearest
+// reciprocal then rounds right (Markstein's theorem).
 __device__ __forceinline__ float f8_scale(uint32_t amax)
 {
     if (amax >= 0x7F800000u) return __builtin_nanf("");
-    return fmaxf(__uint_as_float(amax) / 448.0f, 0x1p-126f);
+    const float a = __uint_as_float(amax), q = a * (1.0f / 448.0f);
+    return fmaxf(__builtin_fmaf(__builtin_fmaf(-448.0f, q, a), 1.0f / 448.0f, q), 0x1p-126f);
 }
 
 // Eight e4m3 codes of v / d, value j in byte j: the nearest of the exact
 // quotient, ties to even.  v times the reciprocal is off by at most 2^-22 of
-// itself, so only a product that lies next to a border between two codes is
-// formed again: in 64 bits, cut to 32 with the last bit set where anything was
-// cut, which the conversion then rounds as it would the quotient.  20 bits below
-// e4m3's last one a border is all ones or a half, plus or minus 4; below the
-// normal range, 2^-6, codes are as far apart as above it, so 2^-6 more has the same
-// bits there (off by another half at most).  About one wave in 200 has such a
-// value; correctly rounded divisions for all of them, or for the values below
-// the normal range (one wave in 15), bound the quantizers.
+// itself, so only a product that lies next to a border between two codes may
+// round to the wrong one, and on which side the quotient lies is the sign of v -
+// border d, which one multiply-add gives.  20 bits below e4m3's last one a border
+// is a half, plus or minus 4; below the normal range, 2^-6, codes are as far apart
+// as above it, so 2^-6 more has the same bits there (off by another half at
+// most).  (The quotients in 64 bits of every group of 8 with such a value, with 8-bit
+// values of 8-bit largest ones many: 92160 rows of 2880 from bf16 226 us, so 175;
+// divisions rounded right for all of them bound the quantizers.)
 __device__ __forceinline__ uint2 f8_codes(const float (&v)[8], float d)
 {
     if (!(d < __builtin_inff())) return make_uint2(0, 0);
-    const float r = 1.0f / d;
+    const float r = __builtin_amdgcn_rcpf(d);                 // (off by 2^-23 of itself at most; d and r are normal)
     float t[8], low = __builtin_inff();
     uint32_t border = ~0u;                                    // the smallest distance to a border, plus 4, << 12
     auto test = [&](float f) {
@@ -166,18 +170,16 @@ __device__ __forceinline__ uint2 f8_codes(const float (&v)[8], float d)
         }
     }
     if (border < 9u << 12) {
-        const double d64 = (double)d;
+        // (scaled up where the difference could underflow)
+        const float up = d < 0x1p-60f ? 0x1p60f : 1.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const double q = (double)v[j] / d64;
-            const float f = (float)q;
-            uint32_t b = __float_as_uint(f);
-            const double back = (double)f;
-            if (back != q) {
-                if (__builtin_fabs(back) > __builtin_fabs(q)) b -= 1u;
-                b |= 1u;
-            }
-            t[j] = __uint_as_float(b);
+            const float m = __builtin_fabsf(t[j]), more = m < 0x1p-6f ? 0x1p-6f : 0.0f;
+            const uint32_t b = __float_as_uint(m + more);
+            const float at = __uint_as_float((b & 0xFFF00000u) | 0x80000u) - more;
+            const float side = __builtin_fmaf(-at, d * up, __builtin_fabsf(v[j]) * up);
+            const uint32_t e = __float_as_uint(at) + (side > 0.0f ? 1u : side < 0.0f ? ~0u : 0u);
+            if ((b << 12) + ((0x80000u + 4u) << 12) < 9u << 12) t[j] = __builtin_copysignf(__uint_as_float(e), v[j]);
         }
     }
     int lo = 0, hi = 0;
@@ -212,6 +214,23 @@ __device__ __forceinline__ uint32_t amax_bits8(const float (&v)[8])
         m = m > b ? m : b;
     }
     return m;
+}
+
+// The same of values as loaded: 16-bit patterns two at a time.
+template <int T> __device__ __forceinline__ uint32_t amax_bits8(const Raw8 &r)
+{
+    if constexpr (T == QMX_T_F32) {
+        float v[8];
+        raw_to_f32(r, T, v);
+        return amax_bits8(v);
+    } else {
+        typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+        u16x2 h = {0, 0};
+        for (const uint32_t w : {r.a.x, r.a.y, r.a.z, r.a.w})
+            h = __builtin_elementwise_max(h, __builtin_bit_cast(u16x2, w & 0x7FFF7FFFu));
+        const uint16_t o = h[0] > h[1] ? h[0] : h[1];
+        return T == QMX_T_BF16 ? (uint32_t)o << 16 : __float_as_uint((float)__builtin_bit_cast(_Float16, o));
+    }
 }
 
 template <int CTRL> __device__ __forceinline__ uint32_t row_max_step(uint32_t m)

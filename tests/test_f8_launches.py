@@ -133,8 +133,8 @@ def test_steps(L):
     for D, G_ in ((32, 4), (40, 8), (128, 16), (256, 32), (264, 64)):
         assert steps(L, *qk(1, 8, 2, D))[0][0] == f"qmt_qk_norm_rope_kernel<{G_}, 1, -1, -1, -1>"
         for xt, yt, style in ((0, 1, 0), (1, 1, 1), (2, 0, 0), (1, 2, 1)):
-            assert steps(L, *qk(2000, 8, 2, D, xt, yt, style)) == \
-                [(f"qmt_qk_norm_rope_kernel<{G_}, 4, {xt}, {yt}, {style}>", -(-2000 * 3 * G_ // 256))]
+            assert steps(L, *qk(4000, 8, 2, D, xt, yt, style)) == \
+                [(f"qmt_qk_norm_rope_kernel<{G_}, 4, {xt}, {yt}, {style}>", -(-4000 * 3 * G_ // 256))]
     assert [n for _, n in steps(L, *qk(4100, 4096, 0, 264))] == [1 << 20, 1024]
 
     def logprobs(M, V, top_k):

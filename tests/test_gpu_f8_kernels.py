@@ -144,6 +144,19 @@ def test_two_streams_at_once():
         assert all(torch.equal(o, v) for o, v in zip(out, want))
 
 
+@pytest.mark.parametrize("t", [torch.bfloat16, torch.float16])
+def test_ties_of_short_values(t):
+    """Quotients of 16-bit values by their block's largest: many lie on a border between two codes, more next to one."""
+    rng = np.random.default_rng(6)
+    largest = torch.from_numpy(np.concatenate([np.arange(128, 256) / 32.0, [3.5 / 2 ** 9, 7 / 2 ** 12]])).to(t)
+    x = torch.from_numpy(rng.integers(128, 256, (len(largest), 128)) * np.exp2(rng.integers(-18, -7, (len(largest), 128)))).to(t)
+    x = torch.where(x > largest[:, None], largest[:, None], x) * torch.from_numpy(rng.choice([-1.0, 1.0], x.shape)).to(t)
+    x[:, 5] = largest
+    T.same_codes(q.qmx_quantize(x.cuda(), "f8"), F.quantize_rows(x.float().numpy()))
+    m = x[:, None, :].repeat(1, 3, 1)
+    T.same_codes(q.qmt_quantize_weights(m.cuda()), F.quantize_weights(m.float().numpy()))
+
+
 # ------------------------------------------- more workgroups than one launch takes
 def test_a_million_matrices():
     E, N, K = (1 << 20) + 100, 1, 32
