@@ -737,7 +737,7 @@ LdsLimit g_f8_lds[2][2], g_f8_few_lds[3], g_f8_wide_lds;
 // LDS of a tile workgroup: the list of its vectors, and for all of K or each
 // half two blocks' codes and scales of the vectors and three blocks' codes of
 // 128 rows.
-constexpr int kF8Chunk = 96;
+constexpr int kF8Chunk = 96;             // (as in qmv_k_f8.hip)
 constexpr int f8_tile_lds(int halves) { return 2 * kF8Chunk + halves * (2 * kF8Chunk * (128 + 4) + 3 * 128 * 128); }
 static_assert(2 * f8_tile_lds(1) <= kLdsPerCU && f8_tile_lds(2) <= kLdsPerCU, "8 waves a CU");
 

@@ -17,8 +17,8 @@
 // takes chunks q and q + 4 (16 bytes each) of row c's 128.  (A sum does not care
 // which k a lane holds, as long as both operands agree.)
 //
-// Times here are a kernel's own: its median in a trace of ten calls with three
-// sets of weights and vectors in turn.
+// Times here and at the choices between these kernels are of a call among others
+// in a graph, with three sets of weights and vectors in turn.
 #include "qmv_routed.hpp"
 
 #include <type_traits>
@@ -28,7 +28,7 @@ namespace qmv {
 
 constexpr int kF8Few = 16;           // vectors of a few-vector workgroup
 constexpr int kF8Waves = kRoutedWaves;
-constexpr int kF8Chunk = 96;         // vectors of a tile at most
+constexpr int kF8Chunk = 96;         // vectors of a tile at most (also in qmv.hip)
 constexpr int kF8Block = 128;        // weights of a block, and code bytes
 
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
@@ -353,8 +353,10 @@ __device__ __forceinline__ void f8_tile(const Args &a, uint8_t *lds, int e, int 
     }
 }
 
-// Workgroup b runs on XCD b % 8; the tiles (item-major) are dealt to the XCDs
-// in contiguous parts, so that an XCD's L2 holds the vectors of a few experts.
+// Workgroup b runs on XCD b % 8; the tiles are dealt to the XCDs in contiguous
+// parts, expert by expert, row tile by row tile, so that an XCD's L2 holds the
+// vectors of a few experts, and a row tile's codes for all of the expert's chunks
+// (512 tokens, top 4 of 32, 2880 -> 2880, chunk by chunk: 702 MB for 531 of codes).
 template <int MODE, int HV>
 __global__ __launch_bounds__(64 * kF8Waves * HV, 2) void qmv_f8_tile_kernel(const Args a)
 {
@@ -362,15 +364,24 @@ __global__ __launch_bounds__(64 * kF8Waves * HV, 2) void qmv_f8_tile_kernel(cons
     constexpr int CHUNK = kF8Chunk, TR = MODE == 1 ? 64 : 128;
     uint16_t *const list = (uint16_t *)lds;           // [CHUNK]
     uint8_t *const buf = lds + 2 * CHUNK;             // (16-byte aligned)
-    int item = -1, rt = 0;
+    int item = -1, rt = 0, place = 0;
     auto pick = [&](int items) {
         const int all = items * a.bt_row_tiles, per_xcd = (all + 7) / 8, i = blockIdx.x >> 3;
         const int r = i < per_xcd ? (int)(blockIdx.x & 7) * per_xcd + i : all;
         if (r < all) {
             item = r / a.bt_row_tiles;
             rt = r - item * a.bt_row_tiles;
+            place = r;
         }
         return item;
+    };
+    // the same places of all chunks first .. first + n - 1, row tile by row tile
+    auto order = [&](int, int first, int n) {
+        const int at = place - first * a.bt_row_tiles;
+        rt = at / n;
+        const int chunk = at - rt * n;
+        item = first + chunk;
+        return chunk;
     };
     int e = 0, nv, vstart = 0;
     const bool gather = a.ids != nullptr;
@@ -378,7 +389,8 @@ __global__ __launch_bounds__(64 * kF8Waves * HV, 2) void qmv_f8_tile_kernel(cons
         // (a call without any id in [0, E) still has its zero rows: one item.
         // The first half counts; the other has no pairs)
         const int P = threadIdx.x < 64 * kRoutedWaves ? a.M * a.top_k : 0;
-        const RoutedItem it = routed_item<CHUNK>(a.ids, P, a.E, (int *)buf, list, [&](int items) { return pick(max(items, 1)); });
+        const RoutedItem it = routed_item<CHUNK>(a.ids, P, a.E, (int *)buf, list, [&](int items) { return pick(max(items, 1)); },
+                                                  order);
         if (item < 0) return;
         e = it.e;
         nv = it.nv;
@@ -387,7 +399,7 @@ __global__ __launch_bounds__(64 * kF8Waves * HV, 2) void qmv_f8_tile_kernel(cons
     } else {
         const int chunks = (a.M + CHUNK - 1) / CHUNK, cs = (a.M + chunks - 1) / chunks;   // equal chunks
         if (pick(chunks) < 0) return;
-        vstart = item * cs;
+        vstart = order(item, 0, chunks) * cs;
         nv = min(cs, a.M - vstart);
     }
     const uint16_t *const vecs = gather ? list : nullptr;
@@ -407,6 +419,11 @@ __global__ __launch_bounds__(64 * kF8Waves * HV, 2) void qmv_f8_tile_kernel(cons
 // on their way from the start; the vectors and the scales are staged in LDS
 // once.  The waves' partial tiles are summed in wave order.  Columns past the
 // last vector repeat one (nothing of them is stored).
+//
+// Bound by the weight bytes where there are many: gate/up of one token, top 8 of
+// 256, 7168 -> 2048 (235 MB) 42 us, 5.6 TB/s; combine of 4 tokens, 2048 -> 7168 (470
+// MB) 94 us; 7168 -> 40960 (294 MB) 51 us; by one trip to memory after another
+// where there are few: 7168 -> 2048 (15 MB) 8.2 us.
 constexpr int kF8Ahead = 4;
 
 // Bytes from vector to vector of the staged codes (whole blocks, and 16 more

@@ -42,10 +42,12 @@ __device__ __forceinline__ int wave_scan(int v)
 }
 
 // cnt: 1024 + 8 words of LDS.  `pick` maps the number of items to this
-// workgroup's item (or -1); the chunk's pairs go to list.  ids: thread t
-// looks at ids t, t + 256, ...  Every wave finds the item by itself.
-template <int CHUNK, class Pick>
-__device__ __forceinline__ RoutedItem routed_item(const int32_t *ids, int P, int E, int *cnt, uint16_t *list, Pick pick)
+// workgroup's item (or -1), and `order` that, the first item of its expert and
+// how many it has to the workgroup's chunk of the expert; the chunk's pairs go to
+// list.  ids: thread t looks at ids t, t + 256, ...  Every wave finds the item by
+// itself.
+template <int CHUNK, class Pick, class Order>
+__device__ __forceinline__ RoutedItem routed_item(const int32_t *ids, int P, int E, int *cnt, uint16_t *list, Pick pick, Order order)
 {
     int tid = threadIdx.x;
     asm volatile("" : "+v"(tid));
@@ -80,18 +82,18 @@ __device__ __forceinline__ RoutedItem routed_item(const int32_t *ids, int P, int
     RoutedItem it = {0, 0, items};
     if (item < 0 || item >= items) return it;
     const unsigned long long owner = __ballot(item >= before && item < before + n);
-    int e = 0, chunk = 0, total = 0;
+    int e = 0, first = 0, total = 0;
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
         const int k = (c[i] + CHUNK - 1) / CHUNK;
-        if (item >= before && item < before + k) e = 16 * lane + i, chunk = item - before, total = c[i];
+        if (item >= before && item < before + k) e = 16 * lane + i, first = before, total = c[i];
         before += k;
     }
     const int o = __ffsll((long long)owner) - 1;
     it.e = __builtin_amdgcn_readlane(e, o);
-    chunk = __builtin_amdgcn_readlane(chunk, o);
+    first = __builtin_amdgcn_readlane(first, o);
     total = __builtin_amdgcn_readlane(total, o);
-    const int nch = (total + CHUNK - 1) / CHUNK;
+    const int nch = (total + CHUNK - 1) / CHUNK, chunk = order(item, first, nch);
     const int cs = (total + nch - 1) / nch;           // equal chunks
     it.nv = min(cs, total - chunk * cs);
     uint32_t m = 0;
@@ -116,6 +118,13 @@ __device__ __forceinline__ RoutedItem routed_item(const int32_t *ids, int P, int
     }
     __syncthreads();
     return it;
+}
+
+// The chunks of an expert in order.
+template <int CHUNK, class Pick>
+__device__ __forceinline__ RoutedItem routed_item(const int32_t *ids, int P, int E, int *cnt, uint16_t *list, Pick pick)
+{
+    return routed_item<CHUNK>(ids, P, E, cnt, list, pick, [](int item, int first, int) { return item - first; });
 }
 
 // The rows [n0, n1) of pairs whose id is outside [0, E) are zeros: of `items`

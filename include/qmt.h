@@ -93,8 +93,9 @@ qmv_status_t qmt_qk_norm_rope(qmx_type_t xtype, const void *x, int row, int head
  * id -1 and -infinity; a row with every logit masked has entropy 0.  +infinity
  * makes a row's log probabilities and entropy NaN.  A token outside [0, V) is
  * not an error: its log probability is 0.
- * Exponentials are fp32, s is summed in fp64 (a log probability next to 0
- * keeps its digits), the rest of a row's arithmetic is fp64.
+ * Exponentials are fp32; sums are fp64, of terms or of up to eight fp32 terms
+ * none of which is the largest logit's (so that a log probability next to 0 keeps
+ * its digits); the rest of a row's arithmetic is fp64.
  *   logits     ltype [M][V]
  *   tokens     int32 [M], or NULL with logprobs NULL
  *   logprobs   fp32 [M], or NULL

@@ -179,7 +179,9 @@ typedef enum {
  * weights with int8 (or in-kernel quantized bf16) activations and M >= 8 on
  * the int8 matrix-core kernel; (MXFP4, MXFP4) with any M on the block-scaled
  * matrix cores (16 rows and 16 vectors a workgroup with K split over its
- * waves, 128 x 64 tiles, or 256 x 256 tiles for many);
+ * waves, 128 x 64 tiles, or 256 x 256 tiles for many); (F8B128, F8B128) with
+ * any M on the bf16 matrix cores (16 rows and 16 vectors likewise, tiles of
+ * 128 x 96, K in halves where they are few, or of 256 x 128 for many);
  * every other M > 4 call on the grouped kernel.
  */
 qmv_status_t qmv_dense(qmv_wfmt_t wfmt, const void *w_codes, const void *w_scales,
@@ -215,6 +217,9 @@ qmv_status_t qmv_dense(qmv_wfmt_t wfmt, const void *w_codes, const void *w_scale
  *     too); chunks of up to 16 while 16 rows a workgroup do not fill the chip,
  *     else of up to 64, or 128 from 48 pairs an expert on where K leaves the
  *     LDS for them;
+ *   (F8B128, F8B128): likewise on the bf16 matrix cores (e4m3 values are bf16
+ *     values), chunks of up to 16 while the chip holds 2 in 5 of the
+ *     workgroups of 16 rows at a time, else of up to 96;
  *   at most 64 tokens with fewer than two pairs per expert: groups of up to
  *     4 tokens on the decode kernels, one launch per group;
  *   every other call: the decode kernels' own multiply-adds in one launch,
@@ -240,8 +245,8 @@ qmv_status_t qmv_gather_moe(qmv_wfmt_t wfmt, const void *w_codes, const void *w_
  * directly.  Arguments, limits and errors as qmv_gather_moe (M > 4
  * included: (MXFP4, BF16) with M * top_k >= 2 E on the batched matrix-core
  * kernel with a gate and an up fragment per output fragment, (MXFP4, MXFP4)
- * likewise on the block-scaled ones, every other call on the grouped
- * kernel); silu is evaluated in fp32.
+ * likewise on the block-scaled ones, (F8B128, F8B128) on the bf16 ones, every
+ * other call on the grouped kernel); silu is evaluated in fp32.
  */
 qmv_status_t qmv_gather_moe_swiglu(qmv_wfmt_t wfmt, const void *gate_codes, const void *gate_scales,
                                    const void *up_codes, const void *up_scales, int E,
@@ -269,8 +274,8 @@ qmv_status_t qmv_gather_moe_swiglu(qmv_wfmt_t wfmt, const void *gate_codes, cons
  * multiply-add onto a sum that starts at zero; results are bitwise
  * reproducible.  An out-of-range id contributes route_weights[t][j] * 0.
  * Up to 4 tokens: one launch, a workgroup per token and row tile, each lane
- * carrying one row of four of the token's slots (with (MXFP4, MXFP4) the
- * slots one after another on the matrix cores, their partial rows summed in
+ * carrying one row of four of the token's slots (with (MXFP4, MXFP4) and
+ * (F8B128, F8B128) the slots one after another on the matrix cores, their partial rows summed in
  * slot order).  More than 4 tokens: the
  * gather of qmv_gather_moe (same kernels and routing) writes every (token,
  * slot) row to a temporary of M * top_k * N floats from the library's pool
