@@ -132,13 +132,16 @@ constexpr __host__ __device__ int from_k(int k) { return k < 2 ? 0 : k == 8 ? 16
 // one barrier a block.
 //
 // Bound by the weight bytes (gate/up of 32 experts top 4, 2880 -> 2880, 531 MB:
-// 64 tokens 124 us, 4.3 TB/s; with rows of 2816 109, 4.8 TB/s: their blocks do not
-// straddle cache lines), with many vectors by what a block costs beside them (512
-// tokens 153 us, 700 170; without any load from memory 109 and 133 with rows of
-// 2816).  Fragments of 16 x 16 staged through registers, 64 vectors a tile: 512
-// tokens of popular and unpopular experts 185 us, so 181; 7168 -> 7168, 1024 vectors
-// 156 us, so 147.  All tiles in two halves: 227 and 153.  Runs of row tiles that
-// share the counting of the pairs: 2 187 us, 3 215.
+// 64 tokens 120 us, 4.4 TB/s; with rows of 2816 109, 4.8 TB/s: their blocks do not
+// straddle cache lines), with many vectors by the chain of a block beside them --
+// barrier, LDS, widening, eight products one after another -- with two waves a
+// SIMD (512 tokens 151 us; 1024 tokens top 8 of 256, 7168 -> 2048, 3.7 GB: 715, 5.2
+// TB/s).  Without any load from memory 109 of 142, without products 133, without
+// widening the later fragments 136.  16 x 16 fragments staged through registers,
+// 64 vectors a tile: 512 tokens of popular and unpopular experts 185 us, so 176; 7168
+// -> 7168, 1024 vectors 156, so 147.  All tiles in two halves: 227 and 153.  Runs of
+// row tiles that share the counting of the pairs: 2 187 us, 3 215.  Row tiles dealt
+// to the XCDs in turn: no faster.
 constexpr int kF8Ring = 3;           // blocks of the rows' codes in LDS
 
 // Row tile rt of expert e against nv vectors: pairs vecs[0..nv) of a routed
@@ -189,31 +192,35 @@ __device__ __forceinline__ void f8_tile(const Args &a, uint8_t *lds, int e, int 
     }
     const int sv = 64 * w + lane;                    // the vector whose scale this lane stages
     const uint32_t os = sv < nv ? vec_row(sv) * (uint32_t)KB * 4u : kXPast;
-    // the blocks that are loaded next, rows' and vectors': number, place
-    // (chunks past the row's end read zeros: the bytes there are another row's;
-    // as many loads past the last block as before it, of zeros)
+    // The blocks that are loaded next, rows' and vectors': number, place.  A block
+    // is the loads' scalar offset, past every buffer's end behind the last block:
+    // as many loads, of zeros.  (Chunks past the row's end read zeros too: the
+    // bytes there are another row's.)
+    const bool cut0 = lc >= U - 8 * (KB - 1), cut1 = (lc ^ 4) >= U - 8 * (KB - 1);
+    constexpr int PAST = 0x7FFFFFF0, PIECES = PX + 5;
     int u_l = half, at_l = 0, u_x = half, at_x = 0;
-    auto load_rows = [&] {
-        const uint32_t past0 = 8 * u_l + lc < U ? 128u * u_l : kXPast;
-        const uint32_t past1 = 8 * u_l + (lc ^ 4) < U ? 128u * u_l : kXPast;
-#pragma unroll
-        for (int p = 0; p < 4; ++p)                                  // (oc < 2^31: the sum does not wrap)
+    // Piece q: the vectors' codes, their scales, the rows' codes last.
+    auto load = [&](int q) {
+        if (q < PX) {
+            const bool out = u_x == KB - 1 && (w & 1 ? cut1 : cut0);
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_t *)(lx + at_x * (CF * 4096) + q * 4096 + w * 1024), 16,
+                                                     out ? kXPast : ox[q], u_x < KB ? 128 * u_x : PAST, 0, 0);
+        } else if (q == PX) {
+            if (w < (CF + 1) / 2 && sv < 32 * CF)
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_t *)(ls + at_x * (32 * CF) + 64 * w), 4, os,
+                                                         u_x < KB ? 4 * u_x : PAST, 0, 0);
+            at_x ^= 1;
+            u_x += HV;
+        } else {
+            const int p = q - PX - 1;
+            const bool out = u_l == KB - 1 && (p & 1 ? cut1 : cut0);
             __builtin_amdgcn_raw_ptr_buffer_load_lds(MODE == 1 && p >= 2 ? rc1 : rc0, (lds_t *)(lw + at_l * 4096 + p * 1024), 16,
-                                                     oc[p] + (p & 1 ? past1 : past0), 0, 0, 0);
-        at_l = at_l == R - 1 ? 0 : at_l + 1;
-        u_l += HV;
-    };
-    auto load_vecs = [&] {
-        const uint32_t past = 8 * u_x + (w & 1 ? lc ^ 4 : lc) < U ? 128u * u_x : kXPast;
-#pragma unroll
-        for (int k = 0; k < PX; ++k)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rx, (lds_t *)(lx + at_x * (CF * 4096) + k * 4096 + w * 1024), 16,
-                                                     past == kXPast ? kXPast : ox[k] + past, 0, 0, 0);
-        if (w < (CF + 1) / 2 && sv < 32 * CF)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_t *)(ls + at_x * (32 * CF) + 64 * w), 4,
-                                                     u_x < KB ? os + 4u * u_x : kXPast, 0, 0, 0);
-        at_x ^= 1;
-        u_x += HV;
+                                                     out ? kXPast : oc[p], u_l < KB ? 128 * u_l : PAST, 0, 0);
+            if (p == 3) {
+                at_l = at_l == R - 1 ? 0 : at_l + 1;
+                u_l += HV;
+            }
+        }
     };
     // the tile's rows lie in one block row of the scales
     typedef const __attribute__((address_space(4))) float scalar_float;
@@ -233,6 +240,7 @@ __device__ __forceinline__ void f8_tile(const Args &a, uint8_t *lds, int e, int 
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc[g][i] = sum[g][i] = 0.0f;
     }
+    static_assert(PIECES <= 8, "one with each product of the first fragment");
     auto scale = [&](int g, int i0, int i1) {
 #pragma unroll
         for (int i = i0; i < i1; ++i) {
@@ -242,17 +250,16 @@ __device__ __forceinline__ void f8_tile(const Args &a, uint8_t *lds, int e, int 
     };
     const f32x16 zero = {};
 
-    load_rows();
-    load_vecs();
-    load_rows();
+#pragma unroll
+    for (int q = PX + 1; q < PIECES; ++q) load(q);
+#pragma unroll
+    for (int q = 0; q < PIECES; ++q) load(q);
     float sw0 = row_scale(a.scales, half), sw1 = MODE == 1 ? row_scale(a.scales2, half) : 0.0f;
     int at = 0, ax = 0;
     for (int u = half; u < KB + half; u += HV) {     // (both halves as often)
         // this block's codes are here (the last loads are the next one's
         // rows), and the places of the one before are free
         wait_loads_barrier<4>();
-        load_vecs();
-        load_rows();
         const uint8_t *const pa = lw + at * 4096, *const pb = lx + ax * (CF * 4096);
         auto chunk = [&](const uint8_t *base, int j) { return *(const u32x4 *)(base + (rd ^ (32 * j))); };
         u32x4 ra[4], rb[4];
@@ -282,6 +289,8 @@ __device__ __forceinline__ void f8_tile(const Args &a, uint8_t *lds, int e, int 
                 pin(sum[g]);
                 // (the sums of the fragment before, of the block before)
                 if constexpr (CF > 1) scale(g ? g - 1 : CF - 1, from_k(k), from_k(k + 1));
+                // (given out together, the loads would hold up the products behind them)
+                if (g == 0 && k < PIECES) load(k);
                 if (g + 1 < CF && (k & 1)) {
                     widen_chunk(rb[k >> 1], B[k - 1], B[k]);
                     pin(B[k - 1]);
