@@ -129,12 +129,11 @@ def qmt_dequantize_weights(codes, scales, dtype=torch.bfloat16, y=None, stream=N
 # than its checks take).
 
 @functools.lru_cache(maxsize=256)
-def _qk_plan(x_shape, table_shape, heads, kv_heads, head_dim, style, dtype):
+def _qk_plan(x_shape, table_shape, H, Hk, D, style, dtype):
     """(M, row, H, Hk, D, P, R, rotation, ytype; shape and strides of q, of k)"""
     rotation = _choice(style, _STYLE, "style")
     if dtype not in _TYPE:
         raise ValueError(f"dtype is {dtype}, expected one of {tuple(_TYPE)}")
-    H, Hk, D = int(heads), int(kv_heads), int(head_dim)
     if len(x_shape) != 2 or 0 in x_shape:
         raise ValueError(f"x has shape {tuple(x_shape)}, expected [M][row]")
     M, row = x_shape
@@ -166,8 +165,8 @@ def qmt_qk_norm_rope(x, heads, kv_heads, head_dim, table, positions, q_weight=No
     _tensor(x, "x", _TYPE)
     dev = x.device
     _tensor(table, "table", _F32, dev)
-    M, row, H, Hk, D, P, R, rotation, ytype, qs, ks = _qk_plan(x.shape, table.shape, heads, kv_heads, head_dim, style,
-                                                               dtype)
+    M, row, H, Hk, D, P, R, rotation, ytype, qs, ks = _qk_plan(x.shape, table.shape, int(heads), int(kv_heads),
+                                                               int(head_dim), style, dtype)
     _tensor(positions, "positions", _I32, dev, (M,))
     if q_weight is not None:
         _tensor(q_weight, "q_weight", _TYPE, dev, (D,))
@@ -190,15 +189,14 @@ def qmt_qk_norm_rope(x, heads, kv_heads, head_dim, table, positions, q_weight=No
 
 @functools.lru_cache(maxsize=256)
 def _logprobs_plan(shape, top_k):
-    """(M, V, top_k, bytes of the workspace)"""
+    """(M, V, bytes of the workspace)"""
     if len(shape) != 2 or 0 in shape:
         raise ValueError(f"logits has shape {tuple(shape)}, expected [M][V]")
     M, V = shape
     _q._ints(M, V)
-    top_k = int(top_k)
     if not 0 <= top_k <= 32:
         raise ValueError(f"top_k is {top_k}, expected 0 to 32")
-    return M, V, top_k, qmt_lib().qmt_logprobs_workspace(M, V, top_k)
+    return M, V, qmt_lib().qmt_logprobs_workspace(M, V, top_k)
 
 
 def qmt_logprobs(logits, tokens=None, top_k=0, logprobs=None, entropy=None, top_ids=None, top_logprobs=None,
@@ -214,7 +212,8 @@ def qmt_logprobs(logits, tokens=None, top_k=0, logprobs=None, entropy=None, top_
     least qmt_lib().qmt_logprobs_workspace(M, V, top_k) bytes, is taken from
     torch where it is not given."""
     _tensor(logits, "logits", _TYPE)
-    M, V, top_k, need = _logprobs_plan(logits.shape, top_k)
+    top_k = int(top_k)
+    M, V, need = _logprobs_plan(logits.shape, top_k)
     dev = logits.device
     if tokens is not None:
         _tensor(tokens, "tokens", _I32, dev, (M,))
