@@ -16,8 +16,8 @@ using namespace qmt_host;
 // One workgroup takes a block of 128 x 128: 16 lanes a row, 16 rows at a time,
 // the whole block in registers between the maximum and the codes.  (A kernel for
 // each type: 16-bit values take half the registers, and twice the waves are
-// there to wait for memory.)  32 matrices of 2880 x 2880 from bf16 (797 MB) 174
-// us, 4.6 TB/s, and back 145, 5.5 TB/s; with one kernel for all types, a
+// there to wait for memory.)  32 matrices of 2880 x 2880 from bf16 (797 MB) 170
+// us, 4.7 TB/s, and back 142, 5.6 TB/s (148 with neighbours on different XCDs); with one kernel for all types, a
 // maximum in fp32 and 64-bit quotients of all values below the normal range 257.
 struct SquareBlock {
     long long at;        // of the thread's first value
@@ -37,13 +37,20 @@ struct SquareBlock {
     __device__ __forceinline__ size_t index(int p) const { return (size_t)(at + (long long)(16 * p) * K); }
 };
 
+// Workgroup b runs on XCD b % 8: blocks that are neighbours in a row go to one XCD, whose L2 has the
+// cache lines that rows of odd multiples of 32 have in common.  (The grid is a multiple of 8.)
+__device__ __forceinline__ long long first_square()
+{
+    return (long long)(blockIdx.x & 7) * (gridDim.x >> 3) + (blockIdx.x >> 3);
+}
+
 template <int XT>
 __global__ __launch_bounds__(256) void qmt_quantize_weights_kernel(const void *x, void *codes, float *scales,
                                                                    long long blocks, int N, int K)
 {
     __shared__ uint32_t part[2][16];
     int turn = 0;
-    for (long long b = blockIdx.x; b < blocks; b += gridDim.x, turn ^= 1) {
+    for (long long b = first_square(); b < blocks; b += gridDim.x, turn ^= 1) {
         const SquareBlock s(b, N, K);
         Raw8 r[8];
 #pragma unroll
@@ -77,7 +84,7 @@ __global__ __launch_bounds__(256) void qmt_quantize_weights_kernel(const void *x
 __global__ __launch_bounds__(256) void qmt_dequantize_weights_kernel(const void *codes, const float *scales, int yt,
                                                                      void *y, long long blocks, int N, int K)
 {
-    for (long long b = blockIdx.x; b < blocks; b += gridDim.x) {
+    for (long long b = first_square(); b < blocks; b += gridDim.x) {
         const SquareBlock s(b, N, K);
         const float d = scales[s.scale];
         uint2 c[8];
@@ -944,7 +951,7 @@ qmv_status_t go_all(const void *fn, Args &a, long long Args::*first, long long u
     return QMV_OK;
 }
 
-long long square_groups(long long blocks) { return blocks < kMaxGroups ? blocks : kMaxGroups; }
+long long square_groups(long long blocks) { return blocks < kMaxGroups ? (blocks + 7) / 8 * 8 : kMaxGroups; }
 
 }  // namespace
 
