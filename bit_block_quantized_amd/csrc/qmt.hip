@@ -17,8 +17,9 @@ using namespace qmt_host;
 // the whole block in registers between the maximum and the codes.  (A kernel for
 // each type: 16-bit values take half the registers, and twice the waves are
 // there to wait for memory.)  32 matrices of 2880 x 2880 from bf16 (797 MB) 170
-// us, 4.7 TB/s, and back 142, 5.6 TB/s (148 with neighbours on different XCDs); with one kernel for all types, a
-// maximum in fp32 and 64-bit quotients of all values below the normal range 257.
+// us, 4.7 TB/s, and back 142, 5.6 TB/s (148 with neighbours on different XCDs);
+// with one kernel for all types, a maximum in fp32 and 64-bit quotients of all
+// values below the normal range 257.
 struct SquareBlock {
     long long at;        // of the thread's first value
     int k, row, N, K;    // its column and row in the matrix
