@@ -135,13 +135,14 @@ constexpr __host__ __device__ int from_k(int k) { return k < 2 ? 0 : k == 8 ? 16
 // 64 tokens 120 us, 4.4 TB/s; with rows of 2816 109, 4.8 TB/s: their blocks do not
 // straddle cache lines), with many vectors by the chain of a block beside them --
 // barrier, LDS, widening, eight products one after another -- with two waves a
-// SIMD (512 tokens 151 us; 1024 tokens top 8 of 256, 7168 -> 2048, 3.7 GB: 715, 5.2
+// SIMD (512 tokens 150 us; 1024 tokens top 8 of 256, 7168 -> 2048, 3.7 GB: 715, 5.2
 // TB/s).  Without any load from memory 109 of 142, without products 133, without
 // widening the later fragments 136.  16 x 16 fragments staged through registers,
-// 64 vectors a tile: 512 tokens of popular and unpopular experts 185 us, so 176; 7168
+// 64 vectors a tile: 512 tokens of popular and unpopular experts 185 us, so 171 to 179; 7168
 // -> 7168, 1024 vectors 156, so 147.  All tiles in two halves: 227 and 153.  Runs of
 // row tiles that share the counting of the pairs: 2 187 us, 3 215.  Row tiles dealt
-// to the XCDs in turn: no faster.
+// to the XCDs in turn, the next block's first operands widened beside the last
+// products: no faster.  A tile's start and end, without any block, take 36 us of 146.
 constexpr int kF8Ring = 3;           // blocks of the rows' codes in LDS
 
 // Row tile rt of expert e against nv vectors: pairs vecs[0..nv) of a routed
@@ -308,21 +309,14 @@ __device__ __forceinline__ void f8_tile(const Args &a, uint8_t *lds, int e, int 
     scale(CF - 1, 0, 16);
 
     const bool vec4 = (N & 3) == 0 && ((uintptr_t)a.y & 15) == 0;
-    auto store = [&](int v, int n0, const float (&r)[4]) {
-        if (v < nv && n0 < N) {
-            float *const yr = a.y + (size_t)(gather ? (int)vecs[v] : vstart + v) * N + n0;
-            if (vec4) {
-                *(float4 *)yr = make_float4(r[0], r[1], r[2], r[3]);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    if (n0 + k < N) yr[k] = r[k];
-            }
-        }
-    };
-    const int row0 = rt * TR + (MODE == 1 ? 16 : 32) * w + 4 * hk;   // registers 4 i ..: rows row0 + 8 i ..
+    const int row0 = (MODE == 1 ? 16 : 32) * w + 4 * hk;   // registers 4 i ..: rows row0 + 8 i .. of the tile
+    auto y_row = [&](int v) { return a.y + (size_t)(gather ? (int)vecs[v] : vstart + v) * N + rt * TR; };
+    const int rows = min(TR, N - rt * TR);
     wait_loads_barrier<0>();                         // (nothing on its way into LDS; all its codes are read)
     if constexpr (HV == 1) {
+        // by way of LDS, a vector's rows together (in 16-byte pieces, 32 vectors a store: 156 us for the 512 tokens' 150)
+        constexpr int PITCH = TR + 4;
+        float *const out = (float *)lds;
 #pragma unroll
         for (int g = 0; g < CF; ++g)
 #pragma unroll
@@ -331,10 +325,34 @@ __device__ __forceinline__ void f8_tile(const Args &a, uint8_t *lds, int e, int 
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                     q[k] = MODE == 1 ? swiglu(acc[g][4 * i + k], acc[g][(4 * i + 8 + k) & 15]) : acc[g][4 * i + k];
-                store(32 * g + n, row0 + 8 * i, q);
+                *(float4 *)(out + (32 * g + n) * PITCH + row0 + 8 * i) = make_float4(q[0], q[1], q[2], q[3]);
             }
+        __syncthreads();
+        if (vec4) {
+            for (int t = tid; t < nv * (TR / 4); t += 64 * kF8Waves) {
+                const int v = t / (TR / 4), r = 4 * (t % (TR / 4));
+                if (r < rows) *(float4 *)(y_row(v) + r) = *(const float4 *)(out + v * PITCH + r);
+            }
+        } else {
+            for (int t = tid; t < nv * TR; t += 64 * kF8Waves) {
+                const int v = t / TR, r = t % TR;
+                if (r < rows) y_row(v)[r] = out[v * PITCH + r];
+            }
+        }
         return;
     }
+    auto store = [&](int v, int r0, const float (&r)[4]) {
+        if (v < nv && r0 < rows) {
+            float *const yr = y_row(v) + r0;
+            if (vec4) {
+                *(float4 *)yr = make_float4(r[0], r[1], r[2], r[3]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (r0 + k < rows) yr[k] = r[k];
+            }
+        }
+    };
     // Each half gives the other one half of its registers (gate/up: of the
     // gate's and of the up projection's), and stores the rest.
     float *const give = (float *)lds + (4 * half + w) * (CF * 512) + lane;
