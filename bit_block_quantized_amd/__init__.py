@@ -29,6 +29,7 @@ qmx_quantize and qmx_rmsnorm).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch  # noqa: F401  -- loads the HIP runtime that libqmv.so binds to
@@ -298,18 +299,36 @@ def _gpu(dev, fn):
         raise ValueError(f"{fn} runs on the GPU only; pass device tensors")
 
 
+@functools.lru_cache(maxsize=256)
+def _f8_dense(codes, scales, x, x_scales):
+    """(M, N, K) of a dense "f8" call whose tensors have these shapes, None if they do not fit."""
+    if len(codes) != 2 or len(x) != 2:
+        return None
+    (N, K), M = codes, x[0]
+    fits = x[1] == K and scales == (_blocks128(N), _blocks128(K)) and x_scales == (M, _blocks128(K))
+    return (M, N, K) if fits and max(M, N, K) < 1 << 31 else None
+
+
 def qmv_dense(wfmt, w_codes, w_scales, x, x_scales=None, y=None, stream=None):
     """Dense GEMV: y[m][n] = sum_k w(n,k) x(m,k); returns y (float32 [M][N]).
     ``x`` is [M][K]."""
     w = _wfmt(wfmt)
-    if not (isinstance(x, torch.Tensor) and x.dim() == 2):
-        raise ValueError("x must be a 2-D tensor [M][K]")
-    M, K = x.shape[0], _k_of(w, x)
-    N = w_codes.shape[0]
-    a, xd = _afmt(w, x)
-    _ints(M, N, K)
-    _check_weights(w, w_codes, w_scales, (N,), K)
-    _check_x(x, x_scales, M, K, a)
+    # (one token's call is over in less time than all checks of its sizes take one by one)
+    sizes = None
+    if w == W_F8B128 and type(x) is type(x_scales) is type(w_codes) is type(w_scales) is _Tensor:
+        sizes = _f8_dense(w_codes.shape, w_scales.shape, x.shape, x_scales.shape)
+    if sizes is not None:
+        M, N, K = sizes
+        a, xd = A_F8B128, F8_DT
+    else:
+        if not (isinstance(x, torch.Tensor) and x.dim() == 2):
+            raise ValueError("x must be a 2-D tensor [M][K]")
+        M, K = x.shape[0], _k_of(w, x)
+        N = w_codes.shape[0]
+        a, xd = _afmt(w, x)
+        _ints(M, N, K)
+        _check_weights(w, w_codes, w_scales, (N,), K)
+        _check_x(x, x_scales, M, K, a)
     if y is not None:
         _check_y(y, (M, N))
     dev = w_codes.device
