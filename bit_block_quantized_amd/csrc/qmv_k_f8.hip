@@ -133,16 +133,17 @@ constexpr __host__ __device__ int from_k(int k) { return k < 2 ? 0 : k == 8 ? 16
 //
 // Bound by the weight bytes (gate/up of 32 experts top 4, 2880 -> 2880, 531 MB:
 // 64 tokens 120 us, 4.4 TB/s; with rows of 2816 109, 4.8 TB/s: their blocks do not
-// straddle cache lines), with many vectors by the chain of a block beside them --
-// barrier, LDS, widening, eight products one after another -- with two waves a
-// SIMD (512 tokens 150 us; 1024 tokens top 8 of 256, 7168 -> 2048, 3.7 GB: 715, 5.2
-// TB/s).  Without any load from memory 109 of 142, without products 133, without
-// widening the later fragments 136.  16 x 16 fragments staged through registers,
-// 64 vectors a tile: 512 tokens of popular and unpopular experts 185 us, so 171 to 179; 7168
-// -> 7168, 1024 vectors 156, so 147.  All tiles in two halves: 227 and 153.  Runs of
-// row tiles that share the counting of the pairs: 2 187 us, 3 215.  Row tiles dealt
-// to the XCDs in turn, the next block's first operands widened beside the last
-// products: no faster.  A tile's start and end, without any block, take 36 us of 146.
+// straddle cache lines; gather of 1024 tokens top 8 of 256, 7168 -> 2048, 3.7 GB:
+// 715, 5.2 TB/s).  With many vectors a tile (512 tokens 150 us) its start and end,
+// without any block, take 36 us of 146, and the vectors' loads 14; without any load
+// of the rows it takes 109, without products 133, without widening the later
+// fragments 136.
+//
+// Tried: 16 x 16 fragments staged through registers, 64 vectors a tile: 512 tokens of
+// popular and unpopular experts 185 us, so 171 to 179; 7168 -> 7168, 1024 vectors
+// 156, so 147.  All tiles in two halves: 227 and 153.  Runs of row tiles that share
+// the counting of the pairs: 2 187 us, 3 215.  Row tiles dealt to the XCDs in turn,
+// the next block's first operands widened beside the last products: no faster.
 constexpr int kF8Ring = 3;           // blocks of the rows' codes in LDS
 
 // Row tile rt of expert e against nv vectors: pairs vecs[0..nv) of a routed
