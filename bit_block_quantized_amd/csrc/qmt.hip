@@ -708,10 +708,14 @@ __global__ __launch_bounds__(512) void qmt_logprobs_kernel(const LogArgs a)
     Sums sums = {low, 0.0, 0.0};                               // m is the wave's
     TopList top(wait[w]);
     float tau = low;                                           // only logits above it can be among the top
-    auto largest = [&](const float (&l)[8]) {                  // (NaN is no maximum)
+    auto biggest = [&](const float (&l)[8]) {                  // (NaN is no maximum)
         float big = low;
 #pragma unroll
         for (int j = 0; j < 8; ++j) big = l[j] > big ? l[j] : big;
+        return big;
+    };
+    auto largest = [&](const float (&l)[8]) {
+        const float big = biggest(l);
         return big > low ? order_bits(big) : 0u;
     };
     auto step = [&](const float (&l)[8], int index) {
@@ -745,10 +749,11 @@ __global__ __launch_bounds__(512) void qmt_logprobs_kernel(const LogArgs a)
         sums.s += (double)(((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7])));
         sums.u += (double)u;
         if constexpr (TOP) {
-            // (rounded differences keep the order, equal ones may stand for
-            // unequal logits; from +infinity there are none)
-            const float zz = top_z < 0.0f ? top_z : 0.0f;
-            if (sums.m == -low || __any(zz > low && zz >= tau - sums.m)) {
+            // (rounded differences keep the order, equal ones may stand for unequal
+            // logits; where the bound's is -infinity -- no bound yet, a logit of
+            // +infinity, a difference past fp32's range -- the logits themselves say)
+            const float zz = top_z < 0.0f ? top_z : 0.0f, bound = tau - sums.m;
+            if (bound > low ? __any(zz >= bound) : __any(biggest(l) > tau)) {
 #pragma unroll
                 for (int j = 0; j < 4; ++j) top.add(l[j] > tau, entry(l[j], index + j));
                 if (top.waiting >= 64) top.merge(64);

@@ -11,6 +11,7 @@ import pytest
 
 import launches
 import test_gpu_f8_kernels as G
+import test_gpu_qmt_edges as Q
 from launches import P, HERE, ROOT, SERVER
 
 W, A = 3, 5
@@ -143,3 +144,9 @@ def test_steps(L):
     assert [n for _, n in steps(L, *logprobs((1 << 20) + 77, 9, 2))] == [1 << 20, 77]
     assert [k.split("<")[0] for k, _ in steps(L, *logprobs(1, 200000, 20))] == ["qmt_logprobs_part_kernel", "qmt_logprobs_join_kernel"]
     assert [k.split("<")[0] for k, _ in steps(L, *logprobs(2000, 131071, 5))] == ["qmt_logprobs_kernel"]
+
+
+def test_edges_of_log_probabilities(L):
+    """The rows of test_gpu_qmt_edges.py reach the kernels that they are meant for."""
+    for M, want in zip(Q.PLANS, (["qmt_logprobs_part_kernel", "qmt_logprobs_join_kernel"], ["qmt_logprobs_kernel"])):
+        assert [k.split("<")[0] for k, _ in steps(L, "qmt_logprobs", 0, P(), M, 5003, P(), 2, P(), P(), P(), P(), P(), None)] == want
