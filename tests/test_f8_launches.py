@@ -150,3 +150,16 @@ def test_edges_of_log_probabilities(L):
     """The rows of test_gpu_qmt_edges.py reach the kernels that they are meant for."""
     for M, want in zip(Q.PLANS, (["qmt_logprobs_part_kernel", "qmt_logprobs_join_kernel"], ["qmt_logprobs_kernel"])):
         assert [k.split("<")[0] for k, _ in steps(L, "qmt_logprobs", 0, P(), M, 5003, P(), 2, P(), P(), P(), P(), P(), None)] == want
+
+
+def test_many_heads(L):
+    """Every kernel that takes four heads a group, and only those, in the cases of test_gpu_qmt_edges.py with many."""
+    t, seen = {"f32": 0, "bf16": 1, "f16": 2}, set()
+    for (M, H, Hk), D, xt, yt, style in Q.HEADS:
+        ((kernel, _),) = steps(L, *qk(M, H, Hk, D, t[xt], t[yt], Q.STYLES.index(style)))
+        if M == Q.MANY[0]:
+            seen.add(kernel)
+        else:
+            assert kernel.endswith(", 1, -1, -1, -1>")
+    assert seen == {f"qmt_qk_norm_rope_kernel<{g}, 4, {x}, {y}, {s}>" for g in (4, 8, 16, 32, 64) for x in range(3) for y in range(3)
+                    for s in range(2)}

@@ -1,6 +1,7 @@
-"""Log probabilities (include/qmt.h) where their arithmetic is at its edge, against
-the 64-bit forms of f8_ref.py (needs an MI355X): logits further apart than fp32
-holds, rows that rise at every step.
+"""Log probabilities and head norms (include/qmt.h) where their arithmetic is at
+its edge, against 64-bit forms (needs an MI355X): logits further apart than fp32
+holds, rows that rise at every step; a normed value's one rounding, in every
+kernel for many heads.
 """
 import numpy as np
 import pytest
@@ -9,7 +10,7 @@ import torch
 import bit_block_quantized_amd as q
 import f8_ref as F
 import test_gpu_qmt
-from test_gpu_qmt import host
+from test_gpu_qmt import HALF_STEP, TYPES, host, values
 
 pytestmark = pytest.mark.gpu
 
@@ -82,3 +83,57 @@ def test_logprobs_of_rows_that_rise_slowly(M, rise):
     for g, w in ((host(lp[:1]), want[0]), (host(top[0]), want[3][0])):
         assert (np.abs(g - w) <= dlog + E * np.abs(w)).all(), (np.abs(g - w) / E, dlog / E)
     assert abs(host(H)[0] - want[1][0]) <= dlog + (12.25 * Z + 2.3 * Z2) * E + Z * dlog + E * abs(want[1][0])
+
+
+def heads64(x, heads, kv_heads, D, table, pos, qw, kw, eps, style):
+    """f8_ref.qk_norm_rope on the GPU, all heads at a time, and |a cos| + |b sin| of each output."""
+    M, R = x.shape[0], table.shape[1]
+    h = x[:, :(heads + kv_heads) * D].double().view(M, heads + kv_heads, D)
+    w = torch.cat([qw.double().expand(heads, D), kw.double().expand(kv_heads, D)])
+    n = h / ((h * h).mean(2, keepdim=True) + float(np.float32(eps))).sqrt() * w
+    inside = ((pos >= 0) & (pos < table.shape[0]))[:, None, None]
+    row = table[pos.long().clamp(0, table.shape[0] - 1)].double()[:, None]
+    c, s = row[..., :R // 2], row[..., R // 2:]
+    a, b = (slice(0, R // 2), slice(R // 2, R)) if style == "half" else (slice(0, R, 2), slice(1, R, 2))
+    y, mag = n.clone(), n.abs()
+    y[..., a], y[..., b] = n[..., a] * c - n[..., b] * s, n[..., b] * c + n[..., a] * s
+    mag[..., a] = (n[..., a] * c).abs() + (n[..., b] * s).abs()
+    mag[..., b] = (n[..., b] * c).abs() + (n[..., a] * s).abs()
+    return torch.where(inside, y, 0.0), torch.where(inside, mag, 0.0)
+
+
+MANY = (3300, 7, 3)                                             # tokens, heads and key heads: 33000 heads
+STYLES = ["half", "pairs"]
+HEADS = [(MANY, D, xt, yt, style) for D in (32, 56, 128, 200, 264) for xt in TYPES for yt in TYPES for style in STYLES] + \
+        [((5, 7, 3), D, xt, yt, style) for D, xt, yt, style in ((32, "f32", "f32", "half"), (56, "bf16", "f32", "pairs"),
+         (128, "f16", "f32", "half"), (200, "f32", "f32", "pairs"), (264, "bf16", "f32", "half"))]
+
+
+@pytest.mark.parametrize("sizes,D,xt,yt,style", HEADS)
+def test_heads_round_once_before_the_rotation(sizes, D, xt, yt, style):
+    """Tolerance: the norm's products are formed in 64 bits and rounded to fp32
+    (half a step, E), 1 / sqrt to 2^-45; values that are not turned are then as they
+    are, or rounded to the output's type; turned ones have two products and a sum
+    in fp32: each term E of its own and E of the rounded norm, the sum E of itself, at
+    most 3 E (1 + 2^-20) of |a cos| + |b sin| in all.  A 16-bit type's subnormals
+    are 2^-24 (fp16), 2^-133 (bf16) apart: half of that more.
+    """
+    M, H, Hk = sizes
+    rng = np.random.default_rng(D + len(xt) + 2 * len(yt))
+    R, rest = D // 2 // 8 * 8, 4
+    x = values(rng, (M, (H + Hk) * D + rest), xt, 3.0)
+    angle = rng.uniform(-np.pi, np.pi, (50, R // 2))
+    table = torch.from_numpy(np.concatenate([np.cos(angle), np.sin(angle)], 1).astype(np.float32)).cuda()
+    table[0, :R // 2], table[0, R // 2:] = 1.0, 0.0             # position 0 turns nothing
+    pos = torch.from_numpy(rng.integers(-1, 51, M).astype(np.int32)).cuda()
+    pos[::3] = 0
+    qw, kw = (values(rng, (D,), "f32") for _ in range(2))
+    got = torch.cat(q.qmt_qk_norm_rope(x, H, Hk, D, table, pos, qw, kw, style=style, dtype=TYPES[yt]), 1).double()
+    want, mag = heads64(x, H, Hk, D, table, pos, qw, kw, 1e-5, style)
+    turned = torch.zeros((M, 1, D), dtype=torch.bool, device="cuda")
+    turned[pos != 0, :, :R] = True
+    off = torch.where(turned, 3 * E * mag, E * want.abs()) * (1 + 2.0 ** -20)
+    if yt != "f32":
+        off = off + HALF_STEP[yt] * (want.abs() + off) + (2.0 ** -25 if yt == "f16" else 2.0 ** -134)
+    bad = (got - want).abs() > off
+    assert not bad.any(), (int(bad.sum()), bad.numel(), bad.nonzero()[:3], ((got - want).abs() / off.clamp(min=1e-300)).max())
