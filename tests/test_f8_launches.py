@@ -10,6 +10,7 @@ import sys
 import pytest
 
 import launches
+import test_gpu_f8 as D
 import test_gpu_f8_kernels as G
 import test_gpu_qmt_edges as Q
 from launches import P, HERE, ROOT, SERVER
@@ -112,6 +113,25 @@ def lds_limits(L):
                     seen.add(name(kernel))
                     assert limit.get((int(dev), kernel), 0) >= int(v[4]), (fn, args, device)
     assert {G.FEW, G.FEW_GU, G.FEW_COMB, G.TILE, G.TILE_GU, G.HALVES, G.HALVES_GU, G.WIDE} <= seen | {G.FEW_COMB}, seen
+
+
+def test_combine_has_its_lds_limit_on_every_device(tmp_path):
+    """Slots staged beyond 64 KB."""
+    with Launches(tmp_path) as L:                               # (limits are set once in a process)
+        combine_limit(L)
+
+
+def combine_limit(L):
+    limit = {}
+    for device in (0, 1, 0):
+        for case in D.BIG_COMBINE:
+            fn, args = combine(*case)
+            status, lines = L.lines(fn, *args, device=device)
+            assert status == 0
+            limit.update({(int(l[1]), l[2]): int(l[3]) for l in lines if l[0] == "attr"})
+            ((dev, kernel, lds),) = [(int(l[1]), l[2], int(l[7])) for l in lines if l[0] == "launch"]
+            assert name(kernel) == G.FEW_COMB and dev == device
+            assert 64 * 1024 < lds <= limit.get((dev, kernel), 0) <= 160 * 1024, (case, device, lds)
 
 
 def steps(L, fn, *args):

@@ -162,6 +162,16 @@ def test_combine(M, E, top_k, N, K, per_slot):
     assert torch.equal(free, y)
 
 
+# up to 4 tokens whose slots take more than 64 KB of LDS, of two groups of them the first
+BIG_COMBINE = [(4, 16, 8, 100, 7168), (1, 16, 16, 100, 7168), (2, 20, 8, 257, 7072), (3, 9, 11, 70, 6144)]
+
+
+@pytest.mark.parametrize("per_slot", [False, True])
+@pytest.mark.parametrize("M,E,top_k,N,K", BIG_COMBINE)
+def test_combine_of_many_slots_of_long_rows(M, E, top_k, N, K, per_slot):
+    test_combine(M, E, top_k, N, K, per_slot)
+
+
 def small_exact(rng, shape):
     """Codes of -2 .. 2 in steps of a half: sums of up to 16384 products stay whole quarters below 2^18."""
     v = rng.integers(-4, 5, shape) * 0.5
