@@ -170,6 +170,9 @@ def test_edges_of_log_probabilities(L):
     """The rows of test_gpu_qmt_edges.py reach the kernels that they are meant for."""
     for M, want in zip(Q.PLANS, (["qmt_logprobs_part_kernel", "qmt_logprobs_join_kernel"], ["qmt_logprobs_kernel"])):
         assert [k.split("<")[0] for k, _ in steps(L, "qmt_logprobs", 0, P(), M, 5003, P(), 2, P(), P(), P(), P(), P(), None)] == want
+    for M, V, parts in Q.LONG:
+        got = steps(L, "qmt_logprobs", 0, P(), M, V, P(), 2, P(), P(), P(), P(), P(), None)
+        assert got[0][0].split("<")[0] == "qmt_logprobs_kernel" and got[0][1] == M * parts and len(got) == 1 + (parts > 1)
 
 
 def test_many_heads(L):

@@ -85,6 +85,23 @@ def test_logprobs_of_rows_that_rise_slowly(M, rise):
     assert abs(host(H)[0] - want[1][0]) <= dlog + (12.25 * Z + 2.3 * Z2) * E + Z * dlog + E * abs(want[1][0])
 
 
+LONG = [(130, 70001, 3), (513, 20001, 1), (2, 300001, 74), (1500, 4097, 1)]     # M, V, parts of a row
+
+
+@pytest.mark.parametrize("t", list(TYPES))
+@pytest.mark.parametrize("top_k", [0, 1, 32])
+@pytest.mark.parametrize("M,V,parts", LONG)
+def test_logprobs_in_long_parts(M, V, parts, top_k, t):
+    """Rows, or several parts of them, that a workgroup takes in many steps, at every alignment; some masked."""
+    rng = np.random.default_rng(M + V + top_k)
+    off = int(rng.integers(8))
+    l = values(rng, (M * V + 8,), t, 3.0)[off:off + M * V].view(M, V)
+    l[:, rng.integers(0, V, V // 4)] = -float("inf")
+    l[1] = -float("inf")
+    l[0, rng.integers(0, V, 9)] = float("nan")
+    test_gpu_qmt.check_logprobs(l, rng.integers(-1, V + 1, M).astype(np.int32), top_k)
+
+
 def heads64(x, heads, kv_heads, D, table, pos, qw, kw, eps, style):
     """f8_ref.qk_norm_rope on the GPU, all heads at a time, and |a cos| + |b sin| of each output."""
     M, R = x.shape[0], table.shape[1]
