@@ -193,10 +193,11 @@ struct QkArgs {
 // its token, all their loads given out at once; the lane's cosines, sines and
 // weights serve them all.
 //
-// 8192 tokens of 40 heads of 128, bf16 (168 MB): 40 us, 4.2 TB/s; of that a SIMD
-// issues 13400 vector instructions, 34 of a head's 130 in 64 bits, and is never
-// without one.  A square root and a division in 64 bits, sums by way of LDS, and
-// types looked up at every load 52.  (XT, YT, PAIRS: the types and the rotation,
+// 8192 tokens of 40 heads of 128, bf16 (168 MB): 42 us, 4.0 TB/s.  A SIMD issues 14100
+// vector instructions, 176 for four heads (one a group), 33 of them additions and
+// products in 64 bits; the vector ALUs have work in 70% of a CU's cycles.  A square
+// root and a division in 64 bits, sums by way of LDS, and types looked up at every
+// load took 52.  (XT, YT, PAIRS: the types and the rotation,
 // or -1 for those of the arguments, which serve calls of few heads: a launch's
 // time whatever they do.)
 template <int G, int UN, int XT, int YT, int PAIRS>
@@ -433,7 +434,7 @@ struct TopList {
         if (have) wait[waiting + lanes_below(m)] = e;
         waiting += (int)__popcll(m);
     }
-    // Merges until less than `left` wait (64 at least but for the last).
+    // Merges, 64 at a time or what there is, until less than `left` wait.
     __device__ __forceinline__ void merge(int left)
     {
         const int lane = threadIdx.x & 63;
@@ -726,9 +727,10 @@ __global__ __launch_bounds__(256) void qmt_logprobs_part_kernel(const LogArgs a)
 
 // A row, or a long part of one: 8 waves, `steps` groups of 8 logits a lane of
 // them, two always on their way; the rest of the row is one more step, the last,
-// of the first part's first wave.  2 steps at least.  1024 rows of 131071 bf16
-// logits, top 5 (268 MB): 76 us, 3.5 TB/s; the exponentials and their sums, not
-// memory, bound it.
+// of the first part's first wave.  (A part may have one step only: the second load
+// is of masked logits then.)  1024 rows of 131071 bf16 logits, top 5 (268 MB): 74 us,
+// 3.6 TB/s.  The vector ALUs bound it, at work in every cycle of a CU's, with 17
+// instructions a logit; without a top list it takes two thirds.
 template <int TYPE, bool TOP>
 __global__ __launch_bounds__(512) void qmt_logprobs_kernel(const LogArgs a)
 {
@@ -879,7 +881,7 @@ __global__ __launch_bounds__(64 * kJoinWaves) void qmt_logprobs_join_kernel(cons
 #pragma unroll
         for (int i = 0; i < PER; ++i) e[i] = w + NW * i < a.parts ? in[(w + NW * i) * 64 + lane] : 0;
     }
-    // (only wave 0 needs these; they are loaded here, before anything is waited for)
+    // (the sums are wave 0's, the maxima every wave's, for its bound; loaded here, before anything is waited for)
     Sums half[kMaxParts / 64];                                 // lane l's parts l, l + 64, ..
 #pragma unroll
     for (int i = 0; i < kMaxParts / 64; ++i) {

@@ -61,7 +61,8 @@ typedef enum { QMT_HALF = 0, QMT_PAIRS = 1 } qmt_rotation_t;
  *   QMT_PAIRS  (a, b) = (n[2 i], n[2 i + 1])
  *   written in their places: a cos - b sin,  b cos + a sin
  * The values R .. D - 1 of a head are only normed.  The statistics and the
- * norm's products are formed in fp64, the rotation in fp32.
+ * norm's products are formed in fp64 and rounded to fp32 once, the rotation in
+ * fp32.
  *   x          xtype [M][row]: the query heads, then the key heads, D values
  *              each; what follows them (row >= (heads + kv_heads) * D, the
  *              values say) is not read
